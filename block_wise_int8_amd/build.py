@@ -7,13 +7,14 @@ from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libqar.so")
-SOURCES = [os.path.join(CSRC, "qar_kernels.hip"), os.path.join(CSRC, "qar_api.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in ("qar_kernels.hip", "qar_kv8.hip", "qar_mx4.hip", "qar_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -32,12 +33,25 @@ FLAGS = [
 
 
 def build(output: str = LIBRARY, extra: list[str] | None = None, verbose: bool = False) -> str:
-    """Compile every source and link the shared library; returns its path."""
+    """Compile every source (at once, they share nothing but headers) and
+    link the shared library; returns its path."""
     tmp = output + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(extra or []), "-shared", *SOURCES, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    def compile_one(source):
+        obj = f"{output}.{os.path.basename(source)}.o"
+        run([HIPCC, *FLAGS, *(extra or []), "-c", source, "-o", obj])
+        return obj
+
+    with ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = list(pool.map(compile_one, SOURCES))
+    run([HIPCC, f"--offload-arch={ARCH}", *(extra or []), "-shared", *objects, "-o", tmp])
+    for obj in objects:
+        os.remove(obj)
     os.replace(tmp, output)
     return output
 

@@ -849,4 +849,260 @@ qar_status qar_ring_step_rows(const int8_t* codes_in, const float* scales_in, co
     return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_ring_step_rows");
 }
 
+// ---------------------------------------------------------------------------
+// microscaled 4-bit floating point
+
+static qar_status mx4_sizes(size_t a, size_t b) {
+    return a > QAR_MX4_MAX_DIM || b > QAR_MX4_MAX_DIM || a * b > QAR_MAX_ELEMENTS ? QAR_ERR_INVALID_ARG : QAR_OK;
+}
+
+static size_t mx4_blocks(size_t cols) { return (cols + QAR_MX4_BLOCK - 1) / QAR_MX4_BLOCK; }
+
+qar_status qar_mx4_quantize(const void* x, qar_dtype dtype, size_t rows, size_t cols, uint8_t* codes,
+                            uint8_t* scales, void* stream) {
+    if (rows == 0 || cols == 0) return QAR_OK;
+    const qar_status st = mx4_sizes(rows, cols);
+    if (st != QAR_OK) return st;
+    if (!x || !codes || !scales) return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(codes, 16)) return QAR_ERR_MISALIGNED;
+    const size_t nb = rows * mx4_blocks(cols);
+    const Range xi = range(x, rows * cols * dtype_bytes(dtype)), co = range(codes, nb * 16), so = range(scales, nb);
+    if (overlap(xi, co) || overlap(xi, so) || overlap(co, so)) return QAR_ERR_INVALID_ARG;
+    const hipError_t e = qar::launch_mx4_quantize(x, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, rows, cols, codes,
+                                                  scales, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_mx4_quantize");
+}
+
+qar_status qar_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, size_t cols, void* out,
+                              qar_dtype out_dtype, void* stream) {
+    if (rows == 0 || cols == 0) return QAR_OK;
+    const qar_status st = mx4_sizes(rows, cols);
+    if (st != QAR_OK) return st;
+    if (!codes || !scales || !out) return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(out_dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(codes, 16) || !aligned(out, 16)) return QAR_ERR_MISALIGNED;
+    const size_t nb = rows * mx4_blocks(cols);
+    const Range oo = range(out, rows * cols * dtype_bytes(out_dtype));
+    if (overlap(oo, range(codes, nb * 16)) || overlap(oo, range(scales, nb))) return QAR_ERR_INVALID_ARG;
+    const hipError_t e = qar::launch_mx4_dequantize(codes, scales, rows, cols, out,
+                                                    out_dtype == QAR_BF16 ? qar::kOutBF16 : qar::kOutF32,
+                                                    (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_mx4_dequantize");
+}
+
+size_t qar_mx4_linear_workspace_bytes(size_t rows, size_t inner, size_t cols) {
+    if (rows == 0 || inner == 0 || cols == 0) return 0;
+    if (mx4_sizes(rows, inner) != QAR_OK || mx4_sizes(cols, inner) != QAR_OK || mx4_sizes(rows, cols) != QAR_OK)
+        return 0;
+    return qar::mx4_linear_workspace(rows, inner, cols);
+}
+
+qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                          const uint8_t* scales, size_t cols, void* out, qar_dtype out_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    if (rows == 0 || cols == 0) return QAR_OK;
+    if (inner == 0) return QAR_ERR_INVALID_ARG;
+    if (mx4_sizes(rows, inner) != QAR_OK || mx4_sizes(cols, inner) != QAR_OK || mx4_sizes(rows, cols) != QAR_OK)
+        return QAR_ERR_INVALID_ARG;
+    if (!x || !codes || !scales || !out) return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(out, 16)) return QAR_ERR_MISALIGNED;
+    const size_t need = qar::mx4_linear_workspace(rows, inner, cols);
+    if (need && (!workspace || workspace_bytes < need)) return QAR_ERR_INVALID_ARG;
+    if (need && !aligned(workspace, 256)) return QAR_ERR_MISALIGNED;
+    const size_t nb = cols * mx4_blocks(inner);
+    const Range in[3] = {range(x, rows * inner * dtype_bytes(dtype)), range(codes, nb * 16), range(scales, nb)};
+    const Range oo = range(out, rows * cols * dtype_bytes(out_dtype)), wo = range(workspace, need);
+    for (const Range& r : in)
+        if (overlap(oo, r) || (need && overlap(wo, r))) return QAR_ERR_INVALID_ARG;
+    if (need && overlap(wo, oo)) return QAR_ERR_INVALID_ARG;
+    const hipError_t e = qar::launch_mx4_linear(
+        x, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, rows, inner, codes, scales, cols, out,
+        out_dtype == QAR_BF16 ? qar::kOutBF16 : qar::kOutF32, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_mx4_linear");
+}
+
+// ---------------------------------------------------------------------------
+// the 8-bit paged cache
+
+// Largest grid of a launch, and the bound on table_width that keeps positions
+// in 31 bits.
+static constexpr size_t kMaxGroups = ((size_t)1 << 31) - 1;
+static constexpr uint32_t kMaxTableWidth = 1u << 24;
+
+static qar_status check_cache(const qar_kv8_cache* c) {
+    if (!c) return QAR_ERR_INVALID_ARG;
+    if (c->dim != 64 && c->dim != 128 && c->dim != 256) return QAR_ERR_UNSUPPORTED;
+    if (!c->k || !c->k_scales || !c->v || !c->v_scales || !c->page_table || !c->lengths) return QAR_ERR_INVALID_ARG;
+    if (c->pages == 0 || c->pages > (1u << 31) - 1 || c->kv_heads == 0 || c->batch == 0 || c->table_width == 0 ||
+        c->table_width > kMaxTableWidth)
+        return QAR_ERR_INVALID_ARG;
+    const size_t heads = (size_t)c->pages * c->kv_heads;
+    if (heads > QAR_MAX_ELEMENTS / (QAR_KV8_PAGE * (size_t)c->dim) || (size_t)c->batch * c->kv_heads > kMaxGroups)
+        return QAR_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4) ||
+        !aligned(c->page_table, 4) || !aligned(c->lengths, 4))
+        return QAR_ERR_MISALIGNED;
+    return QAR_OK;
+}
+
+struct CacheRanges {
+    Range r[6];
+    explicit CacheRanges(const qar_kv8_cache* c) {
+        const size_t heads = (size_t)c->pages * c->kv_heads, codes = heads * QAR_KV8_PAGE * c->dim;
+        r[0] = range(c->k, codes);
+        r[1] = range(c->v, codes);
+        r[2] = range(c->k_scales, heads * 4);
+        r[3] = range(c->v_scales, heads * 4);
+        r[4] = range(c->page_table, (size_t)c->batch * c->table_width * 4);
+        r[5] = range(c->lengths, (size_t)c->batch * 4);
+    }
+    bool touches(Range o) const {
+        for (const Range& x : r)
+            if (overlap(o, x)) return true;
+        return false;
+    }
+};
+
+static qar::Kv8 kernel_cache(const qar_kv8_cache* c) {
+    return qar::Kv8{c->k,     c->k_scales, c->v,     c->v_scales,    c->page_table, c->lengths,
+                    c->pages, c->kv_heads, c->batch, c->table_width, (int)c->dim};
+}
+
+// Workgroups of append and read: two for each head and page that can be touched.
+static bool kv8_tokens_ok(const qar_kv8_cache* c, uint32_t tokens) {
+    if (tokens > (1u << 30)) return false;
+    const size_t touched = ((size_t)tokens + QAR_KV8_PAGE - 2) / QAR_KV8_PAGE + 1;
+    return (size_t)c->batch * c->kv_heads * 2 <= kMaxGroups / touched;
+}
+
+qar_status qar_kv8_append(const qar_kv8_cache* cache, const int32_t* starts, const void* k_new, const void* v_new,
+                          qar_dtype dtype, uint32_t tokens, void* stream) {
+    if (cache && (cache->batch == 0 || tokens == 0)) return QAR_OK;
+    const qar_status st = check_cache(cache);
+    if (st != QAR_OK) return st;
+    if (!starts || !k_new || !v_new || !kv8_tokens_ok(cache, tokens)) return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(starts, 4) || !aligned(k_new, 16) || !aligned(v_new, 16)) return QAR_ERR_MISALIGNED;
+    const size_t bytes = (size_t)cache->batch * tokens * cache->kv_heads * cache->dim * dtype_bytes(dtype);
+    const CacheRanges held(cache);
+    for (int i = 0; i < 4; ++i) {
+        if (overlap(held.r[i], range(k_new, bytes)) || overlap(held.r[i], range(v_new, bytes)) ||
+            overlap(held.r[i], range(starts, (size_t)cache->batch * 4)))
+            return QAR_ERR_INVALID_ARG;
+        for (int j = 0; j < 6; ++j)
+            if (i != j && overlap(held.r[i], held.r[j])) return QAR_ERR_INVALID_ARG;
+    }
+    const hipError_t e = qar::launch_kv8_append(kernel_cache(cache), starts, k_new, v_new,
+                                                dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, tokens,
+                                                (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_append");
+}
+
+qar_status qar_kv8_read(const qar_kv8_cache* cache, const int32_t* starts, uint32_t tokens, void* k_out, void* v_out,
+                        qar_dtype out_dtype, void* stream) {
+    if (cache && (cache->batch == 0 || tokens == 0)) return QAR_OK;
+    const qar_status st = check_cache(cache);
+    if (st != QAR_OK) return st;
+    if (!starts || !k_out || !v_out || !kv8_tokens_ok(cache, tokens)) return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(out_dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(starts, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return QAR_ERR_MISALIGNED;
+    const size_t bytes = (size_t)cache->batch * tokens * cache->kv_heads * cache->dim * dtype_bytes(out_dtype);
+    const Range ko = range(k_out, bytes), vo = range(v_out, bytes), si = range(starts, (size_t)cache->batch * 4);
+    const CacheRanges held(cache);
+    if (overlap(ko, vo) || overlap(ko, si) || overlap(vo, si) || held.touches(ko) || held.touches(vo))
+        return QAR_ERR_INVALID_ARG;
+    const hipError_t e = qar::launch_kv8_read(kernel_cache(cache), starts, tokens, k_out, v_out,
+                                              out_dtype == QAR_BF16 ? qar::kOutBF16 : qar::kOutF32,
+                                              (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_read");
+}
+
+// Rows of a key head: every query of every head that shares it.
+static bool kv8_rows_ok(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads, uint32_t width) {
+    if (kv_heads == 0 || heads == 0 || heads % kv_heads || width > kMaxTableWidth) return false;
+    const size_t rows = (size_t)queries * (heads / kv_heads);
+    // tiles of 16 rows or more, at most 2048 + width workgroups for the cuts of one
+    return queries <= (1u << 30) && rows <= (1u << 30) &&
+           (size_t)batch * kv_heads <= kMaxGroups / ((rows + 15) / 16 + 2048 + width) &&
+           (size_t)batch * kv_heads * rows <= QAR_MAX_ELEMENTS / 256;
+}
+
+size_t qar_kv8_attention_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
+                                         uint32_t dim, uint32_t table_width, int with_weights) {
+    if (batch == 0 || queries == 0 || table_width == 0 || (dim != 64 && dim != 128 && dim != 256) ||
+        !kv8_rows_ok(batch, queries, heads, kv_heads, table_width))
+        return 0;
+    return qar::kv8_attention_workspace(batch, kv_heads, queries * (heads / kv_heads), (int)dim, table_width,
+                                        with_weights != 0);
+}
+
+qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
+                             uint32_t heads, const int32_t* q_lens, float scale, float* weights, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    if (cache && (cache->batch == 0 || queries == 0)) return QAR_OK;
+    const qar_status st = check_cache(cache);
+    if (st != QAR_OK) return st;
+    if (!q || !out || !kv8_rows_ok(cache->batch, queries, heads, cache->kv_heads, cache->table_width))
+        return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(out, 16) || (q_lens && !aligned(q_lens, 4)) || (weights && !aligned(weights, 4)))
+        return QAR_ERR_MISALIGNED;
+    const size_t need = qar::kv8_attention_workspace(cache->batch, cache->kv_heads, queries * (heads / cache->kv_heads),
+                                                     (int)cache->dim, cache->table_width, weights != nullptr);
+    if (need && (!workspace || workspace_bytes < need)) return QAR_ERR_INVALID_ARG;
+    if (need && !aligned(workspace, 256)) return QAR_ERR_MISALIGNED;
+    const size_t bytes = (size_t)cache->batch * queries * heads * cache->dim * dtype_bytes(dtype);
+    const size_t summed = weights ? (size_t)cache->batch * cache->kv_heads * cache->table_width * QAR_KV8_PAGE * 4 : 0;
+    const CacheRanges held(cache);
+    // what the call writes: nothing else may overlap it
+    const Range w[3] = {range(out, bytes), range(weights, summed), range(workspace, need)};
+    const Range qi = range(q, bytes), li = range(q_lens, q_lens ? (size_t)cache->batch * 4 : 0);
+    for (int i = 0; i < 3; ++i) {
+        if (w[i].lo == w[i].hi) continue;
+        if (overlap(w[i], qi) || overlap(w[i], li) || held.touches(w[i])) return QAR_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(w[i], w[j])) return QAR_ERR_INVALID_ARG;
+    }
+    const hipError_t e = qar::launch_kv8_attention(kernel_cache(cache), q, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32,
+                                                   queries, heads, q_lens, scale, weights, out, workspace,
+                                                   (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_attention");
+}
+
+qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, const float* weights, uint32_t recent,
+                         uint32_t keep, int32_t* kept, float* moved, void* stream) {
+    if (cache && into && cache->batch == 0 && into->batch == 0) return QAR_OK;
+    qar_status st = check_cache(cache);
+    if (st == QAR_OK) st = check_cache(into);
+    if (st != QAR_OK) return st;
+    if (cache->batch != into->batch || cache->kv_heads != into->kv_heads || cache->dim != into->dim)
+        return QAR_ERR_INVALID_ARG;
+    if (!weights || !kept || !moved || keep == 0 || keep > (size_t)into->table_width * QAR_KV8_PAGE)
+        return QAR_ERR_INVALID_ARG;
+    if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(moved, 4)) return QAR_ERR_MISALIGNED;
+    const size_t items = (size_t)cache->batch * cache->kv_heads;
+    if (items * 2 > kMaxGroups / (keep / QAR_KV8_PAGE + 1)) return QAR_ERR_INVALID_ARG;
+    const Range wi = range(weights, items * cache->table_width * QAR_KV8_PAGE * 4);
+    const Range ko = range(kept, items * keep * 4), mo = range(moved, items * keep * 4);
+    const CacheRanges from(cache), to(into);
+    if (overlap(ko, mo) || overlap(ko, wi) || overlap(mo, wi) || from.touches(ko) || from.touches(mo) || to.touches(ko) ||
+        to.touches(mo))
+        return QAR_ERR_INVALID_ARG;
+    // One pool may serve both caches (disjoint pages are the caller's word); its
+    // buffers are then the same.  Otherwise what is written overlaps nothing.
+    for (int i = 0; i < 6; ++i) {
+        if (i == 4) continue;                       // into's page table is read only
+        if (overlap(to.r[i], wi)) return QAR_ERR_INVALID_ARG;
+        for (int j = 0; j < 6; ++j) {
+            if (i != j && overlap(to.r[i], to.r[j])) return QAR_ERR_INVALID_ARG;
+            if (bad_overlap(to.r[i], from.r[j], i == j && i < 4)) return QAR_ERR_INVALID_ARG;
+        }
+    }
+    const hipError_t e = qar::launch_kv8_evict(kernel_cache(cache), kernel_cache(into), weights, recent, keep, kept, moved,
+                                               (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_evict");
+}
+
 } // extern "C"

@@ -1,0 +1,1248 @@
+// qar_kv8.hip -- a paged cache of keys and values held in 8 bits on gfx950:
+// tokens enter it, are read back, attended to, and evicted by weight.
+//
+// A page holds 64 tokens of every head: keys as [64][dim], values as
+// [dim][64] codes (each the layout whose contiguous bytes run along the sum
+// of its matrix product), and one binary32 scale for each page and head of
+// either.  value = code * scale; scale = absmax / 127, codes as everywhere
+// in this library.
+//
+// Entries of the page table outside [0, pages) stand for pages that are not
+// there: nothing is written to them, they read as zeros and attention sees
+// none of their keys.
+#include <float.h>
+#include <hip/hip_runtime.h>
+
+#include "qar_device.h"
+#include "qar_launch.h"
+
+namespace qar {
+namespace {
+
+typedef _Float16 kv_half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 kv_half2 __attribute__((ext_vector_type(2)));
+typedef float kv_f32x4 __attribute__((ext_vector_type(4)));
+typedef float kv_f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kPage = 64;
+
+// ---------------------------------------------------------------------------
+// small pieces
+
+__device__ __forceinline__ int32_t valid_page(int32_t id, uint32_t pages) { return (uint32_t)id < pages ? id : -1; }
+
+__device__ __forceinline__ int32_t clamp_length(int32_t n, uint32_t top) {
+    return n < 0 ? 0 : (uint32_t)n > top ? (int32_t)top : n;
+}
+
+// Elements e .. e + 3 (a multiple of 4, aligned) as binary32.
+template <int IN>
+__device__ __forceinline__ kv_f32x4 load4(const void* x, size_t e) {
+    if constexpr (IN == kInBF16) {
+        const uint2 q = *reinterpret_cast<const uint2*>((const uint16_t*)x + e);
+        return kv_f32x4{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+    } else {
+        return *reinterpret_cast<const kv_f32x4*>((const float*)x + e);
+    }
+}
+
+template <int OUT>
+__device__ __forceinline__ void store4(void* x, size_t e, kv_f32x4 v) {
+    if constexpr (OUT == kOutBF16)
+        store_b64((uint16_t*)x + e, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+    else
+        store_b128((float*)x + e, __builtin_bit_cast(uint4, v));
+}
+
+// The codes of four values, packed.
+__device__ __forceinline__ uint32_t codes4(kv_f32x4 v, float s) {
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    uint32_t w[4];
+    int_code_words(f, s, 127.0f, w);
+    return pack4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ kv_f32x4 values4(uint32_t w, float s) {
+    return kv_f32x4{code_f32(w, 0) * s, code_f32(w, 1) * s, code_f32(w, 2) * s, code_f32(w, 3) * s};
+}
+
+__device__ __forceinline__ float absmax4(kv_f32x4 v, float m) {
+    return fmaxf(fmaxf(fmaxf(m, fabsf(v[0])), fmaxf(fabsf(v[1]), fabsf(v[2]))), fabsf(v[3]));
+}
+
+// 4 x 4 bytes: word i of the result holds byte i of each of the four words.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4]) {
+    const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400), b = __builtin_amdgcn_perm(w[1], w[0], 0x07030602);
+    const uint32_t c = __builtin_amdgcn_perm(w[3], w[2], 0x05010400), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602);
+    w[0] = __builtin_amdgcn_perm(c, a, 0x05040100);
+    w[1] = __builtin_amdgcn_perm(c, a, 0x07060302);
+    w[2] = __builtin_amdgcn_perm(d, b, 0x05040100);
+    w[3] = __builtin_amdgcn_perm(d, b, 0x07060302);
+}
+
+// The maximum over a workgroup of kThreads; every thread gets it.
+__device__ __forceinline__ float group_max(float m, float (&shared)[kThreads / 64]) {
+    m = lanes_max<64>(m);
+    if (threadIdx.x % 64 == 0) shared[threadIdx.x / 64] = m;
+    __syncthreads();
+    return fmaxf(fmaxf(shared[0], shared[1]), fmaxf(shared[2], shared[3]));
+}
+
+// ---------------------------------------------------------------------------
+// append.  A workgroup takes one page of one head, keys or values.  It holds
+// the page's new values in registers between the maximum and the codes, so
+// they are read once.  Old tokens of the page (its first new token need not
+// be its first) keep their codes unless the new ones raise the page's scale;
+// then their values are quantized again with it.
+
+struct AppendArgs {
+    Kv8 c;
+    const int32_t* starts;
+    const void *k_new, *v_new;
+    uint32_t tokens, touched;      // pages that `tokens` tokens can touch
+};
+
+template <int DIM, int IN>
+__global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
+    constexpr int Q = DIM / 4;              // groups of four channels
+    constexpr int U = kPage * Q / kThreads; // of them for each thread
+    __shared__ float shared[kThreads / 64];
+    __shared__ uint32_t tile[Q][kPage + 1]; // values: word (channels / 4, token)
+    const uint32_t which = blockIdx.x % 2, h = blockIdx.x / 2 % a.c.heads;
+    const uint32_t rest = blockIdx.x / 2 / a.c.heads, b = rest / a.touched;
+    const int64_t start = a.starts[b];
+    if (start < 0) return;
+    const int64_t page = start / kPage + rest % a.touched, p0 = page * kPage;
+    const int64_t lo = start > p0 ? start : p0;
+    const int64_t hi = start + a.tokens < p0 + kPage ? start + a.tokens : p0 + kPage;
+    if (lo >= hi || page >= a.c.width) return;
+    const int32_t id = valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages);
+    if (id < 0) return;
+    const int old = (int)(lo - p0), fresh = (int)(hi - lo);
+    const size_t at = (size_t)id * a.c.heads + h;
+    const void* x = which ? a.v_new : a.k_new;
+    float* scale_at = (which ? a.c.v_scales : a.c.k_scales) + at;
+    int8_t* codes = (which ? a.c.v : a.c.k) + at * (kPage * DIM);
+    const float before = old ? *scale_at : 0.0f;
+
+    kv_f32x4 v[U];
+    float m = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + threadIdx.x, t = i / Q, q = i % Q;
+        v[u] = kv_f32x4{};
+        if (t < fresh)
+            v[u] = load4<IN>(x, (((size_t)b * a.tokens + (size_t)(lo - start) + t) * a.c.heads + h) * DIM + q * 4);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = absmax4(v[u], m);
+    const float scale = fmaxf(before, group_max(m, shared) / 127.0f);   // waits until all have read `before`
+    const bool grown = scale > before;
+    if (threadIdx.x == 0) *scale_at = scale;
+
+    if (which == 0) {
+        if (grown)
+            for (int i = threadIdx.x; i < old * Q; i += kThreads) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(codes) + i;
+                *w = codes4(values4(*w, before), scale);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * kThreads + threadIdx.x;
+            if (i / Q < fresh) reinterpret_cast<uint32_t*>(codes)[old * Q + i] = codes4(v[u], scale);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * kThreads + threadIdx.x;
+            if (i / Q < fresh) tile[i % Q][old + i / Q] = codes4(v[u], scale);
+        }
+        __syncthreads();
+        // four channels by four tokens at a time
+        for (int i = threadIdx.x; i < Q * (kPage / 4); i += kThreads) {
+            const int q = i / (kPage / 4), t = i % (kPage / 4) * 4;
+            if (t >= old + fresh || (t + 4 <= old && !grown)) continue;
+            uint32_t w[4], keep[4] = {};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = t + k >= old && t + k < old + fresh ? tile[q][t + k] : 0;
+            transpose4(w);
+            uint32_t* row = reinterpret_cast<uint32_t*>(codes + (size_t)q * 4 * kPage + t);
+            if (t < old) {
+                const uint32_t mask = old - t >= 4 ? ~0u : (1u << (8 * (old - t))) - 1u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    keep[k] = row[k * (kPage / 4)];
+                    if (grown) keep[k] = codes4(values4(keep[k], before), scale);
+                    keep[k] &= mask;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) row[k * (kPage / 4)] = w[k] | keep[k];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// read.  The same workgroups; the values' codes change from [dim][token] to
+// [token][dim] by 4 x 4 byte transposes on the way into LDS.
+
+struct ReadArgs {
+    Kv8 c;
+    const int32_t* starts;
+    void *k_out, *v_out;
+    uint32_t tokens, touched;
+};
+
+template <int DIM, int OUT>
+__global__ __launch_bounds__(kThreads) void kv8_read_kernel(ReadArgs a) {
+    constexpr int Q = DIM / 4;
+    constexpr int U = kPage * Q / kThreads;
+    __shared__ uint32_t tile[kPage][Q + 1];
+    const uint32_t which = blockIdx.x % 2, h = blockIdx.x / 2 % a.c.heads;
+    const uint32_t rest = blockIdx.x / 2 / a.c.heads, b = rest / a.touched;
+    const int64_t start = a.starts[b] < 0 ? 0 : a.starts[b];
+    const int64_t page = start / kPage + rest % a.touched, p0 = page * kPage;
+    const int64_t lo = start > p0 ? start : p0;
+    const int64_t hi = start + a.tokens < p0 + kPage ? start + a.tokens : p0 + kPage;
+    if (lo >= hi) return;
+    const int32_t n = clamp_length(a.c.lengths[b], a.c.width * kPage);
+    const int skip = (int)(lo - p0), count = (int)(hi - lo);
+    int there = n > lo && a.starts[b] >= 0 ? (int)(n - lo < count ? n - lo : count) : 0;    // tokens of this page that the cache holds
+    const int32_t id = there ? valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages) : -1;
+    if (id < 0) there = 0;
+    const size_t at = id < 0 ? 0 : (size_t)id * a.c.heads + h;
+    const float s = there ? (which ? a.c.v_scales : a.c.k_scales)[at] : 0.0f;
+    const int8_t* codes = (which ? a.c.v : a.c.k) + at * (kPage * DIM);
+    void* out = which ? a.v_out : a.k_out;
+    const size_t first = (size_t)b * a.tokens + (size_t)(lo - start);
+
+    if (which && there) {
+#pragma unroll
+        for (int u = 0; u < U / 4; ++u) {
+            const int i = u * kThreads + threadIdx.x, q = i / (kPage / 4), t = i % (kPage / 4);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(codes)[(q * 4 + k) * (kPage / 4) + t];
+            transpose4(w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tile[t * 4 + k][q] = w[k];
+        }
+    }
+    if (which) __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + threadIdx.x, t = i / Q, q = i % Q;
+        if (t >= count) break;
+        uint32_t w = 0;
+        if (t < there) w = which ? tile[skip + t][q] : reinterpret_cast<const uint32_t*>(codes)[skip * Q + i];
+        store4<OUT>(out, ((first + t) * a.c.heads + h) * DIM + q * 4, values4(w, s));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// attention.
+//
+// Scores are formed transposed, S^T = K Q^T, and so is the output, O^T = V^T
+// P^T: a lane's accumulators then hold many keys (or channels) of ONE row, so
+// the softmax needs one exchange between lanes for a whole page, its factors
+// multiply accumulators without being broadcast, and the scores leave the
+// first product in the registers in which the second wants them.  That last
+// step works by the order in which keys are given to the rows of the first
+// product; see the two kernels.
+//
+// Codes are exact in binary16, so the cache enters the products without
+// rounding.  A query row enters multiplied by the power of two that brings
+// its largest magnitude into [2^14, 2^15): bfloat16's 8 bits are then exact
+// for all but elements 2^29 times smaller than the row's largest; binary32
+// queries are split in two binary16 terms (22 bits, an error of 2^-23 of an
+// element).  The softmax's numerators enter the second product multiplied by
+// 2^14, in one term (an error of 2^-12 of each, for outputs that are rounded
+// to 2^-9) or, for binary32, two.  Sums, maxima and outputs are binary32.
+
+constexpr float kLift = 14.0f;          // log2 of the numerators' factor
+
+struct AttendArgs {
+    Kv8 c;
+    const void* q;
+    const int32_t* q_lens;              // may be null: every sequence has `queries`
+    void* out;
+    float *part, *stats;                // of the splits
+    float* lse;                         // log2 of each row's sum, for the weights; may be null
+    float* weights;
+    uint32_t queries, heads, group, rows, splits, pages_per_split, tiles;
+    float scale;                        // of the scores, times log2(e)
+};
+
+// The maximum and the sum over lanes i, i + 32 and over lanes i, i + 16, ...:
+// each exchange swaps half the rows of two copies of v, so that a lane has its
+// own value in one and its partner's in the other.
+struct Pair {
+    float a, b;
+};
+__device__ __forceinline__ Pair with_lane_32(float v) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ Pair with_lane_16(float v) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    const uint32_t a = r[0], b = r[1];
+    return {__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
+__device__ __forceinline__ float max_over_32(float v) {
+    const Pair p = with_lane_32(v);
+    return fmaxf(p.a, p.b);
+}
+__device__ __forceinline__ float max_over_16(float v) {
+    const Pair p = with_lane_16(v);
+    return max_over_32(fmaxf(p.a, p.b));
+}
+__device__ __forceinline__ float sum_over_32(float v) {
+    const Pair p = with_lane_32(v);
+    return p.a + p.b;
+}
+__device__ __forceinline__ float sum_over_16(float v) {
+    const Pair p = with_lane_16(v);
+    return sum_over_32(p.a + p.b);
+}
+
+// Eight codes as binary16: the byte of code + 128 under the high byte 0x64
+// is 1024 + 128 + code, from which 1152 is taken exactly.
+__device__ __forceinline__ kv_half8 half_codes(uint32_t lo, uint32_t hi) {
+    const kv_half2 bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+    uint32_t w[4];
+    lo ^= 0x80808080u;
+    hi ^= 0x80808080u;
+    w[0] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u);
+    w[1] = __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u);
+    w[2] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u);
+    w[3] = __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u);
+    uint4 q;
+    q.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_half2, w[0]) + bias);
+    q.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_half2, w[1]) + bias);
+    q.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_half2, w[2]) + bias);
+    q.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(kv_half2, w[3]) + bias);
+    return __builtin_bit_cast(kv_half8, q);
+}
+
+// Eight binary32 values as T binary16 terms.
+template <int T>
+__device__ __forceinline__ void half_terms(const float (&x)[8], kv_half8 (&out)[T]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[0][i] = (_Float16)x[i];
+    if constexpr (T == 2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[1][i] = (_Float16)(x[i] - (float)out[0][i]);
+    }
+}
+
+// A lane's share of a query row: runs of RUN channels from channel `first`,
+// one every STEP, as binary16 fragments of eight; returns what undoes the
+// row's factor.  OVER: the lanes that hold the row's other channels.
+template <int IN, int DIM, int RUN, int STEP, int OVER, int T>
+__device__ __forceinline__ float load_query(const void* q, size_t row, int first, bool there,
+                                            kv_half8 (&out)[DIM / STEP * (RUN / 8)][T]) {
+    constexpr int N = DIM / STEP * (RUN / 8);
+    float x[N][8];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const size_t e = row * DIM + i / (RUN / 8) * STEP + first + i % (RUN / 8) * 8;
+        kv_f32x4 lo = {}, hi = {};
+        if (there) {
+            lo = load4<IN>(q, e);
+            hi = load4<IN>(q, e + 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[i][k] = lo[k], x[i][4 + k] = hi[k];
+        m = absmax4(hi, absmax4(lo, m));
+    }
+    m = OVER == 16 ? max_over_16(m) : max_over_32(m);
+    const int e = min(268 - (int)(__builtin_bit_cast(uint32_t, m) >> 23), 253);
+    const float f = __builtin_bit_cast(float, (uint32_t)e << 23);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] *= f;
+        half_terms<T>(x[i], out[i]);
+    }
+    return __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
+}
+
+// A sequence's numbers.  Row r of a kv head is query r / group with head
+// r % group of its group; it sees the keys below limit(r).
+struct Sequence {
+    int32_t n, m;
+    uint32_t group, rows;
+    __device__ __forceinline__ Sequence(const AttendArgs& a, uint32_t b)
+        : n(clamp_length(a.c.lengths[b], a.c.width * kPage)),
+          m(a.q_lens ? clamp_length(a.q_lens[b], a.queries) : (int32_t)a.queries), group(a.group), rows(a.rows) {}
+    __device__ __forceinline__ bool counts(uint32_t r) const { return r < rows && (int32_t)(r / group) < m; }
+    __device__ __forceinline__ int32_t limit(uint32_t r) const { return n - m + (int32_t)(r / group) + 1; }
+};
+
+// Row of the queries' and outputs' [batch, queries, heads] for row r.
+__device__ __forceinline__ size_t query_row(const AttendArgs& a, uint32_t b, uint32_t h, uint32_t r) {
+    return ((size_t)b * a.queries + r / a.group) * a.heads + h * a.group + r % a.group;
+}
+
+template <int OUT>
+__device__ __forceinline__ void store1(void* x, size_t e, float v) {
+    if constexpr (OUT == kOutBF16)
+        ((uint16_t*)x)[e] = (uint16_t)pack_bf16x2(v, 0.0f);
+    else
+        ((float*)x)[e] = v;
+}
+
+// --- few rows (16 MT at most): bound by reading the cache.  Every wave takes
+// a page at a time, straight from memory to registers, the next page's keys
+// on their way while this page's are used and the values likewise; no wave
+// waits for another until the end.
+//
+// 16x16x32 products: lane l = 16 g + r gives row r (a key, a channel) eight
+// elements of the sum and receives, for row r of the queries, the keys 4 g ..
+// 4 g + 3 of a tile of 16.  Row r of tile t is given key 16 (r / 4) + 4 t +
+// r % 4: then lane group g receives keys 16 g .. 16 g + 15 over the four
+// tiles, which are the 16 contiguous bytes that it loads of each channel of
+// the values.
+
+template <int DIM, int MT, int IN, int NW>
+__global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    constexpr int KC = DIM / 64, VC = DIM / 16;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
+    const uint32_t split = blockIdx.x % a.splits, bh = blockIdx.x / a.splits, h = bh % a.c.heads, b = bh / a.c.heads;
+    const Sequence seq(a, b);
+    const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
+    const uint32_t first = split * a.pages_per_split, last = min(first + a.pages_per_split, pages);
+    if (first >= last && split) return;
+
+    kv_half8 q[MT][DIM / 32][T];
+    float undo[MT];
+    int32_t limit[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const uint32_t row = i * 16 + r;
+        const bool there = seq.counts(row);
+        undo[i] = load_query<IN, DIM, 16, 64, 16, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there, q[i]) * a.scale;
+        limit[i] = there ? seq.limit(row) : INT32_MAX;       // rows that are not there are not stored
+    }
+    const int32_t all_see = seq.n - seq.m + 1;               // every row sees the keys below
+
+    kv_f32x4 o[MT][VC] = {};
+    float top[MT], total[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) top[i] = -FLT_MAX, total[i] = 0.0f;
+
+    const size_t head_bytes = (size_t)kPage * DIM;
+    const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16, v_at = r * kPage + g * 16;
+    uint4 kr[4][KC], vr[VC];
+    auto load_k = [&](int32_t id) {
+        const int8_t* p = a.c.k + ((size_t)max(id, 0) * a.c.heads + h) * head_bytes + k_at;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kr[t][c] = load_b128(p + t * 4 * DIM + c * 64);
+    };
+    auto load_v = [&](int32_t id) {
+        const int8_t* p = a.c.v + ((size_t)max(id, 0) * a.c.heads + h) * head_bytes + v_at;
+#pragma unroll
+        for (int c = 0; c < VC; ++c) vr[c] = load_b128(p + c * 16 * kPage);
+    };
+
+    // up to 64 of the wave's pages at a time, one in each lane
+    for (uint32_t base = first + wave; base < last; base += 64 * NW) {
+        const uint32_t mine = base + lane * NW;
+        int32_t my_id = -1;
+        float my_ks = 0.0f, my_vs = 0.0f;
+        if (mine < last) {
+            my_id = valid_page(a.c.table[(size_t)b * a.c.width + mine], a.c.pages);
+            if (my_id >= 0) {
+                my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
+                my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
+            }
+        }
+        const uint32_t count = min(64u, (last - base + NW - 1) / NW);
+        int32_t id = __builtin_amdgcn_readlane(my_id, 0);
+        load_k(id);
+        load_v(id);
+        for (uint32_t i = 0; i < count; ++i) {
+            const int32_t next = __builtin_amdgcn_readlane(my_id, min(i + 1, count - 1));
+            const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i));
+            const float vs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i));
+            const int32_t key0 = (int32_t)((base + i * NW) * kPage);
+
+            kv_f32x4 s[MT][4] = {};
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const kv_half8 lo = half_codes(kr[t][c].x, kr[t][c].y), hi = half_codes(kr[t][c].z, kr[t][c].w);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int e = 0; e < T; ++e) {
+                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[j][2 * c][e], s[j][t], 0, 0, 0);
+                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[j][2 * c + 1][e], s[j][t], 0, 0, 0);
+                        }
+                }
+            if (i + 1 < count) load_k(next);
+
+            kv_half8 p[MT][2][T];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const float factor = ks * undo[j];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) s[j][t] *= factor;
+                if (key0 + kPage > all_see || id < 0) {
+                    const int32_t sees = (id < 0 ? 0 : limit[j]) - key0 - (int32_t)g * 16;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s[j][t][k] = 4 * t + k < sees ? s[j][t][k] : -INFINITY;
+                }
+                float m = -FLT_MAX;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) m = fmaxf(fmaxf(fmaxf(m, s[j][t][0]), fmaxf(s[j][t][1], s[j][t][2])), s[j][t][3]);
+                m = fmaxf(max_over_16(m), top[j]);
+                if (__any(m > top[j])) {
+                    const float shrink = __builtin_amdgcn_exp2f(top[j] - m);
+                    total[j] *= shrink;
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink;
+                    top[j] = m;
+                }
+                const float off = kLift - m;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = __builtin_amdgcn_exp2f(s[j][2 * u + k / 4][k % 4] + off);
+                    total[j] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                    half_terms<T>(x, p[j][u]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < VC; ++c) {
+                const kv_half8 lo = half_codes(vr[c].x, vr[c].y), hi = half_codes(vr[c].z, vr[c].w);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    kv_f32x4 y = {};
+#pragma unroll
+                    for (int e = 0; e < T; ++e) {
+                        y = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, p[j][0][e], y, 0, 0, 0);
+                        y = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, p[j][1][e], y, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[j][c][k] = __builtin_fmaf(y[k], vs, o[j][c][k]);
+                }
+            }
+            if (i + 1 < count) load_v(next);
+            id = next;
+        }
+    }
+
+    // the waves' results meet in LDS, 16 rows at a time
+    __shared__ float os[NW][16][DIM + 4];
+    __shared__ float tops[NW][16], totals[NW][16];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        if (j) __syncthreads();
+        if (j * 16u < a.rows) {
+            total[j] = sum_over_16(total[j]);
+            if (g == 0) tops[wave][r] = top[j], totals[wave][r] = total[j];
+#pragma unroll
+            for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[j][c];
+        }
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 16 * DIM; i += NW * 64) {
+            const uint32_t row16 = i / DIM, d = i % DIM, row = j * 16 + row16;
+            if (row >= a.rows) break;
+            float m = tops[0][row16], l = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) m = fmaxf(m, tops[w][row16]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = __builtin_amdgcn_exp2f(tops[w][row16] - m);
+                l = __builtin_fmaf(totals[w][row16], f, l);
+                y = __builtin_fmaf(os[w][row16][d], f, y);
+            }
+            if (a.splits == 1) {
+                const bool seen = seq.counts(row) && l > 0.0f;
+                store1<IN>(a.out, query_row(a, b, h, row) * DIM + d, seen ? y / l : 0.0f);
+                if (a.lse && d == 0) a.lse[(size_t)bh * a.rows + row] = seen ? m - kLift + __builtin_amdgcn_logf(l) : INFINITY;
+            } else {
+                const size_t at = ((size_t)bh * a.splits + split) * a.rows + row;
+                a.part[at * DIM + d] = y;
+                if (d == 0) a.stats[at * 2] = m, a.stats[at * 2 + 1] = l;
+            }
+        }
+    }
+}
+
+// The splits' results joined: a thread has four channels of a row.
+template <int DIM, int OUT>
+__global__ __launch_bounds__(kThreads) void kv8_join_kernel(AttendArgs a) {
+    const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x, item = i / (DIM / 4);
+    const uint32_t d = (uint32_t)(i % (DIM / 4)) * 4;
+    if (item >= (size_t)a.c.batch * a.c.heads * a.rows) return;
+    const uint32_t row = (uint32_t)(item % a.rows), bh = (uint32_t)(item / a.rows), h = bh % a.c.heads, b = bh / a.c.heads;
+    const Sequence seq(a, b);
+    // the splits that hold keys which this row may see
+    const int32_t seen_keys = seq.counts(row) ? min(seq.limit(row), seq.n) : 0;
+    const uint32_t pages = seen_keys > 0 ? (uint32_t)(seen_keys + kPage - 1) / kPage : 0;
+    const uint32_t used = (pages + a.pages_per_split - 1) / a.pages_per_split;
+    float m = -FLT_MAX, l = 0.0f;
+    for (uint32_t s = 0; s < used; ++s) m = fmaxf(m, a.stats[(((size_t)bh * a.splits + s) * a.rows + row) * 2]);
+    kv_f32x4 y = {};
+    for (uint32_t s = 0; s < used; ++s) {
+        const size_t at = ((size_t)bh * a.splits + s) * a.rows + row;
+        const float f = __builtin_amdgcn_exp2f(a.stats[at * 2] - m);
+        l = __builtin_fmaf(a.stats[at * 2 + 1], f, l);
+        const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], f, y[k]);
+    }
+    const bool seen = l > 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = seen ? y[k] / l : 0.0f;
+    store4<OUT>(a.out, query_row(a, b, h, row) * DIM + d, y);
+    if (a.lse && d == 0) a.lse[item] = seen ? m - kLift + __builtin_amdgcn_logf(l) : INFINITY;
+}
+
+// --- many rows: four waves of 32 rows share a page in LDS, converted to
+// binary16 once for all of them, in two buffers; the page behind it is on its
+// way to registers meanwhile.  32x32x16 products: lane l = 32 g + r.  Row m of
+// a tile of 32 keys is given the key with bits 2 and 3 of m exchanged: lane
+// half g then receives keys 16 a + 8 g .. + 7, the eight contiguous keys of
+// the values' fragment for step a.  LDS rows are eight 16-byte slots or a
+// multiple, slot c of row r lies at c ^ (r % 8).
+
+constexpr int kTileRows = 128;
+
+__device__ __forceinline__ uint32_t exchange_bits_2_3(uint32_t v) {
+    return (v & ~12u) | (v & 4u) << 1 | (v & 8u) >> 1;
+}
+
+template <int DIM, int IN>
+__global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
+    constexpr int KR = DIM / 8;                        // slots of a row of keys
+    __shared__ kv_half8 k_tile[2][kPage * KR], v_tile[2][DIM * 8];
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, r = lane % 32, g = lane / 32;
+    // the last tiles see the most keys: first
+    const uint32_t split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
+    const uint32_t bh = rest % (a.c.heads * a.c.batch), tile = a.tiles - 1 - rest / (a.c.heads * a.c.batch);
+    const uint32_t h = bh % a.c.heads, b = bh / a.c.heads;
+    const Sequence seq(a, b);
+    const uint32_t row = tile * kTileRows + wave * 32 + r;
+    const bool there = seq.counts(row);
+
+    // pages that the tile's last row and the wave's last row see
+    const auto pages_of = [&](uint32_t last_row) {
+        const int32_t i = min((int32_t)(min(last_row, seq.rows - 1) / seq.group), seq.m - 1);
+        const int32_t keys = seq.m > 0 && (int32_t)(tile * kTileRows / seq.group) < seq.m ? seq.n - seq.m + i + 1 : 0;
+        return keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u;
+    };
+    const uint32_t first = split * a.pages_per_split;
+    const uint32_t last = min(first + a.pages_per_split, pages_of(tile * kTileRows + kTileRows - 1));
+    const uint32_t my_last = tile * kTileRows + wave * 32 < seq.rows ? pages_of(tile * kTileRows + wave * 32 + 31) : 0;
+
+    kv_half8 q[DIM / 16][T];
+    const float undo = load_query<IN, DIM, 8, 16, 32, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 8, there, q) * a.scale;
+    const int32_t limit = there ? seq.limit(row) : INT32_MAX;
+    // every row of the wave sees the keys below (rows without a query see all)
+    const int32_t all_see = seq.n - seq.m + (int32_t)((tile * kTileRows + wave * 32) / seq.group) + 1;
+
+    kv_f32x16 o[DIM / 32] = {};
+    float top = -FLT_MAX, total = 0.0f;
+
+    uint4 kr[U], vr[U];
+    int32_t id = -1, next_id = -1;
+    float ks = 0.0f, vs = 0.0f, next_ks = 0.0f, next_vs = 0.0f;
+    const int32_t* table = a.c.table + (size_t)b * a.c.width;
+    auto load_page = [&](uint32_t p) {
+        next_id = valid_page(table[p], a.c.pages);
+        const size_t at = (size_t)max(next_id, 0) * a.c.heads + h;
+        next_ks = next_id < 0 ? 0.0f : a.c.k_scales[at];    // what page 0 holds must not matter
+        next_vs = next_id < 0 ? 0.0f : a.c.v_scales[at];
+        const int8_t* k = a.c.k + at * (kPage * DIM) + tid * 16;
+        const int8_t* v = a.c.v + at * (kPage * DIM) + tid * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            kr[u] = *reinterpret_cast<const uint4*>(k + u * kThreads * 16);
+            vr[u] = *reinterpret_cast<const uint4*>(v + u * kThreads * 16);
+        }
+    };
+    auto put_page = [&](int buffer) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid;
+            const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
+            k_tile[buffer][lr * KR + (c ^ lr % 8)] = half_codes(kr[u].x, kr[u].y);
+            k_tile[buffer][lr * KR + ((c + 1) ^ lr % 8)] = half_codes(kr[u].z, kr[u].w);
+            const uint32_t d = i / 4, e = i % 4 * 2;
+            v_tile[buffer][d * 8 + (e ^ d % 8)] = half_codes(vr[u].x, vr[u].y);
+            v_tile[buffer][d * 8 + ((e + 1) ^ d % 8)] = half_codes(vr[u].z, vr[u].w);
+        }
+    };
+
+    if (first < last) load_page(first);
+    for (uint32_t page = first; page < last; ++page) {
+        const int buffer = (page - first) % 2;
+        put_page(buffer);
+        id = next_id, ks = next_ks, vs = next_vs;
+        __syncthreads();                    // the page before last is no longer read
+        if (page + 1 < last) load_page(page + 1);
+        if (page >= my_last) continue;
+        const int32_t key0 = (int32_t)(page * kPage);
+
+        kv_f32x16 s[2] = {};
+#pragma unroll
+        for (int c = 0; c < DIM / 16; ++c)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t lr = t * 32 + r;
+                const kv_half8 k = k_tile[buffer][lr * KR + ((c * 2 + g) ^ lr % 8)];
+#pragma unroll
+                for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
+            }
+
+        const float factor = ks * undo;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s[t] *= factor;
+        if (key0 + kPage > all_see || id < 0) {
+            // register k of tile t is key 32 t + 16 (k / 8) + 8 g + k % 8
+            const int32_t sees = (id < 0 ? 0 : limit) - key0 - (int32_t)g * 8;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) s[t][k] = 32 * t + 16 * (k / 8) + k % 8 < sees ? s[t][k] : -INFINITY;
+        }
+        float m = -FLT_MAX;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 16; ++k) m = fmaxf(m, s[t][k]);
+        m = fmaxf(max_over_32(m), top);
+        if (__any(m > top)) {
+            const float shrink = __builtin_amdgcn_exp2f(top - m);
+            total *= shrink;
+#pragma unroll
+            for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink;
+            top = m;
+        }
+        const float off = kLift - m;
+        kv_half8 p[4][T];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = __builtin_amdgcn_exp2f(s[u / 2][u % 2 * 8 + k] + off);
+            total += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            half_terms<T>(x, p[u]);
+        }
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d) {
+            kv_f32x16 y = {};
+            const uint32_t lr = d * 32 + r;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const kv_half8 v = v_tile[buffer][lr * 8 + ((u * 2 + g) ^ lr % 8)];
+#pragma unroll
+                for (int e = 0; e < T; ++e) y = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], y, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[d][k] = __builtin_fmaf(y[k], vs, o[d][k]);
+        }
+    }
+
+    total = sum_over_32(total);
+    if (row >= a.rows) return;
+    // register k of tile d is channel 32 d + 8 (k / 4) + 4 g + k % 4
+    if (a.splits == 1) {
+        const bool seen = there && total > 0.0f;
+        const float f = seen ? 1.0f / total : 0.0f;
+        const size_t at = query_row(a, b, h, row) * DIM + g * 4;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                const kv_f32x4 y = {o[d][k] * f, o[d][k + 1] * f, o[d][k + 2] * f, o[d][k + 3] * f};
+                store4<IN>(a.out, at + d * 32 + k * 2, seen ? y : kv_f32x4{});
+            }
+        if (a.lse && g == 0) a.lse[(size_t)bh * a.rows + row] = seen ? top - kLift + __builtin_amdgcn_logf(total) : INFINITY;
+    } else {
+        const size_t at = ((size_t)bh * a.splits + split) * a.rows + row;
+#pragma unroll
+        for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+            for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<kv_f32x4*>(a.part + at * DIM + d * 32 + k * 2 + g * 4) =
+                    kv_f32x4{o[d][k], o[d][k + 1], o[d][k + 2], o[d][k + 3]};
+        if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
+    }
+}
+
+// --- the weights that the keys received: with every row's log2 sum known, a
+// wave forms a page's scores again (reading its keys only), and adds up their
+// exponentials over the rows.  Each weight belongs to one wave, which adds in
+// one order: no atomics.  ONE: 16 rows at most, whose queries stay in
+// registers over the wave's pages.
+
+template <int DIM, int IN, bool ONE>
+__global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    constexpr int KC = DIM / 64;
+    const uint32_t lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+    const uint32_t waves = a.splits * (kThreads / 64);
+    const uint32_t bh = blockIdx.x / a.splits, h = bh % a.c.heads, b = bh / a.c.heads;
+    const uint32_t wave = blockIdx.x % a.splits * (kThreads / 64) + threadIdx.x / 64;
+    const Sequence seq(a, b);
+    const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
+    if (wave >= pages || seq.m == 0) return;
+
+    kv_half8 q[DIM / 32][T];
+    float undo = 0.0f, lse = INFINITY;
+    int32_t limit = 0;
+    auto load_rows = [&](uint32_t tile) {
+        const uint32_t row = tile * 16 + r;
+        const bool there = seq.counts(row);
+        undo = load_query<IN, DIM, 16, 64, 16, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there, q) * a.scale;
+        lse = there ? a.lse[(size_t)bh * a.rows + row] : INFINITY;
+        limit = there ? seq.limit(row) : 0;
+    };
+    if (ONE) load_rows(0);
+    const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16;
+    for (uint32_t page = wave; page < pages; page += waves) {
+        const int32_t id = valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages);
+        if (id < 0) continue;
+        const size_t at = (size_t)id * a.c.heads + h;
+        const float ks = a.c.k_scales[at];
+        uint4 kr[4][KC];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+                kr[t][c] = *reinterpret_cast<const uint4*>(a.c.k + at * (kPage * DIM) + k_at + t * 4 * DIM + c * 64);
+        kv_f32x4 sum[4] = {};
+        const int32_t key0 = (int32_t)(page * kPage + g * 16);
+        const uint32_t tiles = ONE ? 1 : (a.rows + 15) / 16;
+        for (uint32_t tile = 0; tile < tiles; ++tile) {
+            if (!ONE) {
+                // a tile whose last query ends before this page adds nothing
+                if (seq.limit(min(tile * 16 + 15, a.rows - 1)) <= (int32_t)(page * kPage)) continue;
+                load_rows(tile);
+            }
+            kv_f32x4 s[4] = {};
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const kv_half8 lo = half_codes(kr[t][c].x, kr[t][c].y), hi = half_codes(kr[t][c].z, kr[t][c].w);
+#pragma unroll
+                    for (int e = 0; e < T; ++e) {
+                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[2 * c][e], s[t], 0, 0, 0);
+                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[2 * c + 1][e], s[t], 0, 0, 0);
+                    }
+                }
+            const float factor = ks * undo;
+            const int32_t sees = limit - key0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sum[t][k] += 4 * t + k < sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k], factor, -lse)) : 0.0f;
+        }
+        // over the 16 lanes of a row; lane r of them adds key 16 g + r
+        float mine = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v = sum[t][k];
+                v += dpp_move<kDppSwapAdjacent>(v);
+                v += dpp_move<kDppSwapPairs>(v);
+                v += dpp_move<kDppRowHalfMirror>(v);
+                v += dpp_move<kDppRowMirror>(v);
+                if (r == (uint32_t)(4 * t + k)) mine = v;
+            }
+        const int32_t key = key0 + (int32_t)r;
+        if (key < seq.n) a.weights[(size_t)bh * a.c.width * kPage + key] += mine;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// evict.  First the choice: one workgroup for each sequence and head finds the
+// weight of the last token that stays by three histograms (11, 11 and 10 bits
+// of the weights' order-preserving bit patterns), then writes the kept
+// indexes in order: each wave counts what it keeps of its stretch of tokens,
+// and then places it.  The lower index stays where weights are equal.
+
+constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64, kBins = 2048;
+
+struct EvictArgs {
+    Kv8 c, into;
+    const float* weights;
+    uint32_t recent, keep;
+    int32_t* kept;
+    float* moved;
+};
+
+// Ascending unsigned integers for ascending weights; -0 counts as 0, NaN above everything.
+__device__ __forceinline__ uint32_t order_of(float w) {
+    if (w != w) return ~0u;
+    const uint32_t bits = __builtin_bit_cast(uint32_t, w + 0.0f);
+    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+}
+
+__global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a) {
+    __shared__ uint32_t bins[kBins], wave_sum[kSelectWaves], wave_more[kSelectWaves], wave_equal[kSelectWaves];
+    __shared__ uint32_t found_bin, found_above;
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const uint32_t bh = blockIdx.x, h = bh % a.c.heads, b = bh / a.c.heads;
+    const uint32_t n = (uint32_t)clamp_length(a.c.lengths[b], a.c.width * kPage);
+    const uint32_t recent = min(a.recent, a.keep);
+    const float* w = a.weights + (size_t)bh * a.c.width * kPage;
+    int32_t* kept = a.kept + (size_t)bh * a.keep;
+    float* moved = a.moved + (size_t)bh * a.keep;
+    if (h == 0 && tid == 0) a.into.lengths[b] = (int32_t)min(n, a.keep);
+    if (n <= a.keep) {
+        for (uint32_t i = tid; i < a.keep; i += kSelectThreads) {
+            kept[i] = i < n ? (int32_t)i : -1;
+            moved[i] = i < n ? w[i] : 0.0f;
+        }
+        return;
+    }
+    const uint32_t free = n - recent, need = a.keep - recent;      // `need` of the first `free` tokens stay
+    for (uint32_t i = tid; i < recent; i += kSelectThreads) {
+        kept[need + i] = (int32_t)(free + i);
+        moved[need + i] = w[free + i];
+    }
+    if (need == 0) return;
+
+    uint32_t prefix = 0, mask = 0, left = need;        // the threshold's bits so far, and which they are
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t top = pass == 2 ? 1023 : 2047;
+        for (uint32_t i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
+        __syncthreads();
+        for (uint32_t i = tid; i < free; i += kSelectThreads) {
+            const uint32_t o = order_of(w[i]);
+            if ((o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
+        }
+        __syncthreads();
+        // tokens in this thread's two bins and in all above them
+        const uint32_t hi = bins[2 * tid + 1], lo = bins[2 * tid];
+        uint32_t suffix = hi + lo;
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t other = __shfl_down(suffix, d);
+            if (lane + d < 64) suffix += other;
+        }
+        if (lane == 0) wave_sum[wave] = suffix;
+        __syncthreads();
+        uint32_t above = suffix - hi - lo;
+        for (uint32_t v = wave + 1; v < kSelectWaves; ++v) above += wave_sum[v];
+        if (above < left && above + hi >= left) {
+            found_bin = 2 * tid + 1;
+            found_above = above;
+        } else if (above + hi < left && above + hi + lo >= left) {
+            found_bin = 2 * tid;
+            found_above = above + hi;
+        }
+        __syncthreads();
+        prefix |= found_bin << shift;
+        mask |= top << shift;
+        left -= found_above;
+    }
+
+    // all above the threshold stay, and the first `left` equal to it
+    const uint32_t stretch = ((free + kSelectThreads - 1) / kSelectThreads) * 64;
+    const uint32_t from = min(wave * stretch, free), to = min(from + stretch, free);
+    uint32_t more = 0, equal = 0;
+    for (uint32_t i = from + lane; i < to; i += 64) {
+        const uint32_t o = order_of(w[i]);
+        more += o > prefix;
+        equal += o == prefix;
+    }
+    for (int d = 32; d; d /= 2) {
+        more += __shfl_xor(more, d);
+        equal += __shfl_xor(equal, d);
+    }
+    if (lane == 0) wave_more[wave] = more, wave_equal[wave] = equal;
+    __syncthreads();
+    uint32_t more_before = 0, equal_before = 0;
+    for (uint32_t v = 0; v < wave; ++v) more_before += wave_more[v], equal_before += wave_equal[v];
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    for (uint32_t base = from; base < to; base += 64) {
+        const uint32_t i = base + lane;
+        const float weight = i < to ? w[i] : 0.0f;
+        const uint32_t o = order_of(weight);
+        const uint64_t m = __ballot(i < to && o > prefix), e = __ballot(i < to && o == prefix);
+        const uint32_t my_more = more_before + __popcll(m & below), my_equal = equal_before + __popcll(e & below);
+        if ((m >> lane & 1) || ((e >> lane & 1) && my_equal < left)) {
+            const uint32_t at = my_more + min(my_equal, left);
+            kept[at] = (int32_t)i;
+            moved[at] = weight;
+        }
+        more_before += __popcll(m);
+        equal_before += __popcll(e);
+    }
+}
+
+// Then the move: a workgroup gathers one page of one head, keys or values,
+// keeps its codes in registers between the maximum and the new codes, and
+// writes the page.  Values are gathered byte by byte, a lane for each token:
+// neighbouring kept tokens mostly share the lines of a source page.
+template <int DIM>
+__global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, uint32_t out_pages) {
+    constexpr int Q = DIM / 4, U = kPage * Q / kThreads;
+    __shared__ float shared[kThreads / 64];
+    __shared__ uint32_t tile[kPage][Q + 1];
+    __shared__ int64_t source[kPage];                  // offset of each token's page and head, -1: none
+    __shared__ int32_t token[kPage];
+    __shared__ float source_scale[kPage];
+    const uint32_t which = blockIdx.x % 2, page = blockIdx.x / 2 % out_pages, bh = blockIdx.x / 2 / out_pages;
+    const uint32_t h = bh % a.c.heads, b = bh / a.c.heads, tid = threadIdx.x;
+    const uint32_t n = (uint32_t)min(clamp_length(a.c.lengths[b], a.c.width * kPage), (int32_t)a.keep);
+    if (page * kPage >= n) return;
+    const int32_t id = valid_page(a.into.table[(size_t)b * a.into.width + page], a.into.pages);
+    if (id < 0) return;
+    if (tid < kPage) {
+        const uint32_t j = page * kPage + tid;
+        int64_t at = -1;
+        int32_t t = 0;
+        if (j < n) {
+            t = a.kept[(size_t)bh * a.keep + j];
+            const int32_t from = valid_page(a.c.table[(size_t)b * a.c.width + t / kPage], a.c.pages);
+            if (from >= 0) at = (int64_t)from * a.c.heads + h;
+        }
+        source[tid] = at;
+        token[tid] = t % kPage;
+        source_scale[tid] = at < 0 ? 0.0f : (which ? a.c.v_scales : a.c.k_scales)[at];
+    }
+    __syncthreads();
+    const size_t to = (size_t)id * a.into.heads + h;
+    uint32_t w[U];
+    float m = 0.0f;
+    if (which == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * kThreads + tid, t = i / Q, q = i % Q;
+            w[u] = 0;
+            if (source[t] >= 0)
+                w[u] = *reinterpret_cast<const uint32_t*>(a.c.k + (source[t] * kPage + token[t]) * DIM + q * 4);
+        }
+    } else {
+        // four channels of a token make a word, so that both kinds go on alike
+        const int t = tid % 64;
+        const int64_t at = source[t];
+        const int8_t* v = a.c.v + (at < 0 ? 0 : at) * (kPage * DIM) + token[t];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = u * (kThreads / 64) + tid / 64;
+            uint32_t x = 0;
+            if (at >= 0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x |= (uint32_t)(uint8_t)v[(q * 4 + k) * kPage] << (8 * k);
+            w[u] = x;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        m = absmax4(values4(w[u], source_scale[which ? tid % 64 : (u * kThreads + tid) / Q]), m);
+    const float scale = group_max(m, shared) / 127.0f;
+    if (tid == 0) (which ? a.into.v_scales : a.into.k_scales)[to] = scale;
+    if (which == 0) {
+        uint32_t* codes = reinterpret_cast<uint32_t*>(a.into.k + to * (kPage * DIM));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * kThreads + tid;
+            codes[i] = codes4(values4(w[u], source_scale[i / Q]), scale);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            tile[tid % 64][u * (kThreads / 64) + tid / 64] = codes4(values4(w[u], source_scale[tid % 64]), scale);
+        __syncthreads();
+        uint32_t* codes = reinterpret_cast<uint32_t*>(a.into.v + to * (kPage * DIM));
+#pragma unroll
+        for (int u = 0; u < U / 4; ++u) {
+            const int i = u * kThreads + tid, q = i / (kPage / 4), t = i % (kPage / 4);
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = tile[t * 4 + k][q];
+            transpose4(x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) codes[(q * 4 + k) * (kPage / 4) + t] = x[k];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+
+template <int D>
+using Dim = std::integral_constant<int, D>;
+
+template <class F>
+void with_dim(int dim, F f) {
+    if (dim == 64)
+        f(Dim<64>{});
+    else if (dim == 128)
+        f(Dim<128>{});
+    else
+        f(Dim<256>{});
+}
+
+template <class F>
+void with_kind(int kind, F f) {
+    if (kind == kInBF16)
+        f(std::integral_constant<int, kInBF16>{});
+    else
+        f(std::integral_constant<int, kInF32>{});
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// How an attention call is cut.  Few rows: a workgroup's four waves take a
+// page each in turn.  The cache's lengths are on the device, so cuts follow
+// the page table's width; workgroups behind a sequence's end leave at once.
+// Two tiles of 16 rows at 256 channels would not fit a wave's registers.
+constexpr uint32_t few_rows_of(int dim) { return dim == 256 ? 16 : 32; }
+
+struct Plan {
+    bool few;
+    uint32_t tiles, splits, pages_per_split;
+};
+
+Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width) {
+    Plan p = {};
+    p.few = rows <= few_rows_of(dim);
+    p.tiles = p.few ? 1 : (rows + kTileRows - 1) / kTileRows;
+    const size_t units = (size_t)batch * kv_heads * p.tiles;
+    auto cut = [&](size_t target, uint32_t least) {
+        const size_t want = (target + units - 1) / units, most = (width + least - 1) / least;
+        return (uint32_t)(want < most ? want : most);
+    };
+    uint32_t splits;
+    if (p.few) {
+        splits = cut(2048, 16);
+        if (units * splits < 256) splits = cut(256, 4);
+    } else {
+        splits = units >= 256 ? 1 : cut(512, 4);
+    }
+    if (splits < 1) splits = 1;
+    p.pages_per_split = (width + splits - 1) / splits;
+    if (p.pages_per_split < 1) p.pages_per_split = 1;
+    p.splits = (width + p.pages_per_split - 1) / p.pages_per_split;
+    if (p.splits < 1) p.splits = 1;
+    return p;
+}
+
+} // namespace
+
+hipError_t launch_kv8_append(const Kv8& c, const int32_t* starts, const void* k_new, const void* v_new, int kind,
+                             uint32_t tokens, hipStream_t st) {
+    AppendArgs a = {c, starts, k_new, v_new, tokens, (tokens + kPage - 2) / kPage + 1};
+    const uint32_t groups = c.batch * a.touched * c.heads * 2;
+    with_dim(c.dim, [&](auto D) {
+        with_kind(kind, [&](auto K) { kv8_append_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a); });
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_kv8_read(const Kv8& c, const int32_t* starts, uint32_t tokens, void* k_out, void* v_out, int kind,
+                           hipStream_t st) {
+    ReadArgs a = {c, starts, k_out, v_out, tokens, (tokens + kPage - 2) / kPage + 1};
+    const uint32_t groups = c.batch * a.touched * c.heads * 2;
+    with_dim(c.dim, [&](auto D) {
+        with_kind(kind, [&](auto K) { kv8_read_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a); });
+    });
+    return hipGetLastError();
+}
+
+size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, bool weights) {
+    const Plan p = plan_for(batch, kv_heads, rows, dim, width);
+    const size_t items = (size_t)batch * kv_heads * rows;
+    size_t bytes = weights ? align256(items * 4) : 0;
+    if (p.splits > 1) bytes += align256(items * p.splits * 8) + align256(items * p.splits * dim * 4);
+    return bytes;
+}
+
+hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads,
+                                const int32_t* q_lens, float scale, float* weights, void* out, void* workspace,
+                                hipStream_t st) {
+    AttendArgs a = {};
+    a.c = c, a.q = q, a.q_lens = q_lens, a.out = out, a.weights = weights;
+    a.queries = queries, a.heads = heads, a.group = heads / c.heads, a.rows = queries * a.group;
+    a.scale = scale * 1.44269504088896340736f;
+    const Plan p = plan_for(c.batch, c.heads, a.rows, c.dim, c.width);
+    a.tiles = p.tiles, a.splits = p.splits, a.pages_per_split = p.pages_per_split;
+    const size_t items = (size_t)c.batch * c.heads * a.rows;
+    uint8_t* at = (uint8_t*)workspace;
+    if (weights) {
+        a.lse = (float*)at;
+        at += align256(items * 4);
+    }
+    if (a.splits > 1) {
+        a.stats = (float*)at;
+        a.part = (float*)(at + align256(items * a.splits * 8));
+    }
+    const uint32_t groups = c.batch * c.heads * a.tiles * a.splits;
+    with_dim(c.dim, [&](auto D) {
+        with_kind(kind, [&](auto K) {
+            if (!p.few)
+                kv8_attend_many_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a);
+            else if (a.rows <= 16)
+                kv8_attend_few_kernel<D(), 1, K(), 4><<<groups, kThreads, 0, st>>>(a);
+            else if constexpr (few_rows_of(D()) > 16)
+                kv8_attend_few_kernel<D(), 2, K(), 4><<<groups, kThreads, 0, st>>>(a);
+        });
+    });
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.splits > 1) {
+        with_dim(c.dim, [&](auto D) {
+            with_kind(kind, [&](auto K) {
+                const size_t threads = items * (D() / 4);
+                kv8_join_kernel<D(), K()><<<(uint32_t)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+            });
+        });
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (weights) {
+        // a wave for each few pages
+        a.splits = (c.width + 15) / 16;
+        with_dim(c.dim, [&](auto D) {
+            with_kind(kind, [&](auto K) {
+                const uint32_t g = c.batch * c.heads * a.splits;
+                if (a.rows <= 16)
+                    kv8_weights_kernel<D(), K(), true><<<g, kThreads, 0, st>>>(a);
+                else
+                    kv8_weights_kernel<D(), K(), false><<<g, kThreads, 0, st>>>(a);
+            });
+        });
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
+                            int32_t* kept, float* moved, hipStream_t st) {
+    EvictArgs a = {c, into, weights, recent, keep, kept, moved};
+    kv8_select_kernel<<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const uint32_t out_pages = (keep + kPage - 1) / kPage;
+    with_dim(c.dim, [&](auto D) {
+        kv8_move_kernel<D()><<<c.batch * c.heads * out_pages * 2, kThreads, 0, st>>>(a, out_pages);
+    });
+    return hipGetLastError();
+}
+
+} // namespace qar

@@ -81,4 +81,36 @@ hipError_t static_workspace(uint8_t** ptr);
 hipError_t launch_dequantize(const int8_t* codes, const float* scales, size_t n, int block, void* out,
                              int out_kind, hipStream_t st, int code = kCodeInt8);
 
+// Microscaled 4-bit floating point (qar_mx4.hip).
+hipError_t launch_mx4_quantize(const void* x, int kind, size_t rows, size_t cols, uint8_t* codes, uint8_t* scales,
+                               hipStream_t st);
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, size_t cols, void* out,
+                                 int kind, hipStream_t st);
+size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols);
+hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner, const uint8_t* codes,
+                             const uint8_t* scales, size_t cols, void* out, int out_kind, void* workspace,
+                             hipStream_t st);
+
+// The 8-bit paged cache (qar_kv8.hip).
+struct Kv8 {
+    int8_t* k;
+    float* k_scales;
+    int8_t* v;
+    float* v_scales;
+    const int32_t* table;
+    int32_t* lengths;
+    uint32_t pages, heads, batch, width;
+    int dim;
+};
+hipError_t launch_kv8_append(const Kv8& c, const int32_t* starts, const void* k_new, const void* v_new, int kind,
+                             uint32_t tokens, hipStream_t st);
+hipError_t launch_kv8_read(const Kv8& c, const int32_t* starts, uint32_t tokens, void* k_out, void* v_out, int kind,
+                           hipStream_t st);
+size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, bool weights);
+hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads,
+                                const int32_t* q_lens, float scale, float* weights, void* out, void* workspace,
+                                hipStream_t st);
+hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
+                            int32_t* kept, float* moved, hipStream_t st);
+
 } // namespace qar

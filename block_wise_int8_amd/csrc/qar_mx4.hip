@@ -1,0 +1,712 @@
+// qar_mx4.hip -- microscaled 4-bit floating point on gfx950: quantize,
+// dequantize, and the product of 4-bit weights with activations that are
+// quantized on the way.
+//
+// A block is 32 consecutive elements of a row: 32 E2M1 codes (16 bytes, the
+// even element in the low nibble) and one byte e that stands for 2^(e-127).
+// With the block's largest magnitude in [2^p, 2^(p+1)) the scale is 2^(p-2):
+// that maps it into [4, 8), and what lies above 6 becomes 6.  Codes are the
+// nearest of 0, .5, 1, 1.5, 2, 3, 4, 6, the even code where two are as near,
+// the sign kept; the hardware's scaled conversions do exactly that
+// (tests/test_gpu_mx4.py compares them with the definition).
+#include <hip/hip_runtime.h>
+
+#include "qar_device.h"
+#include "qar_launch.h"
+
+namespace qar {
+namespace {
+
+typedef int mx_i32x8 __attribute__((ext_vector_type(8)));
+typedef int mx_i32x4 __attribute__((ext_vector_type(4)));
+typedef float mx_f32x4 __attribute__((ext_vector_type(4)));
+typedef float mx_f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned short mx_u16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kE2M1 = 4;                // the matrix instructions' format code
+constexpr uint32_t kScaleOfZero = 124;  // an all-zero block: exponent 0 - 3
+
+// The scale byte of a block from the bits of its largest magnitude (binary32;
+// bf16 values enter with their bits shifted up).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t peak) {
+    const int e = (int)(peak >> 23) - 2;
+    return peak == 0 ? kScaleOfZero : (uint32_t)min(max(e, 1), 252);
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    // 2^-127 is a subnormal; the quantizer never makes it, a caller's weights may
+    return __builtin_bit_cast(float, byte ? byte << 23 : 0x00400000u);
+}
+
+// Eight elements as they lie in memory: bf16 pairs or binary32.
+template <int IN>
+struct Eight {
+    uint32_t w[IN == kInBF16 ? 4 : 8];
+};
+
+template <int IN>
+__device__ __forceinline__ Eight<IN> load8(const void* x, size_t e) {
+    Eight<IN> v;
+    if constexpr (IN == kInBF16) {
+        const uint4 q = *reinterpret_cast<const uint4*>((const uint16_t*)x + e);
+        v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+    } else {
+        const uint4 a = *reinterpret_cast<const uint4*>((const float*)x + e);
+        const uint4 b = *reinterpret_cast<const uint4*>((const float*)x + e + 4);
+        v.w[0] = a.x, v.w[1] = a.y, v.w[2] = a.z, v.w[3] = a.w;
+        v.w[4] = b.x, v.w[5] = b.y, v.w[6] = b.z, v.w[7] = b.w;
+    }
+    return v;
+}
+
+// The first `count` of eight elements, zero for the others.
+template <int IN>
+__device__ __forceinline__ Eight<IN> load8_some(const void* x, size_t e, int count) {
+    Eight<IN> v = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < count) {
+            if constexpr (IN == kInBF16)
+                v.w[i / 2] |= (uint32_t)((const uint16_t*)x)[e + i] << (16 * (i % 2));
+            else
+                v.w[i] = ((const uint32_t*)x)[e + i];
+        }
+    return v;
+}
+
+// Largest magnitude, as binary32 bits (for bf16 the two halves' maxima are
+// joined by peak_of).
+template <int IN>
+__device__ __forceinline__ uint32_t abs_max(const Eight<IN>& v, uint32_t m) {
+    if constexpr (IN == kInBF16) {
+        mx_u16x2 t = __builtin_bit_cast(mx_u16x2, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t = __builtin_elementwise_max(t, __builtin_bit_cast(mx_u16x2, v.w[i] & 0x7FFF7FFFu));
+        return __builtin_bit_cast(uint32_t, t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, v.w[i] & 0x7FFFFFFFu);
+        return m;
+    }
+}
+
+template <int IN>
+__device__ __forceinline__ uint32_t peak_of(uint32_t m) {
+    if constexpr (IN == kInBF16) return max(m & 0xFFFF0000u, m << 16);
+    return m;
+}
+
+// The eight codes, four bytes.
+template <int IN>
+__device__ __forceinline__ uint32_t codes8(const Eight<IN>& v, float scale) {
+    uint32_t c = 0;
+    if constexpr (IN == kInBF16) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(qar_bf16x2, v.w[0]), scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(qar_bf16x2, v.w[1]), scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(qar_bf16x2, v.w[2]), scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(qar_bf16x2, v.w[3]), scale, 3);
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __builtin_bit_cast(float, v.w[i]);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], scale, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], scale, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4], f[5], scale, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6], f[7], scale, 3);
+    }
+    return c;
+}
+
+// The maximum over a block's four lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppSwapAdjacent, 0xF, 0xF, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppSwapPairs, 0xF, 0xF, false));
+    return m;
+}
+
+// ---------------------------------------------------------------------------
+// quantize.  A lane owns eight elements, four lanes a block.  Three places for
+// the result: as the caller's rows of codes, as the fragments that the
+// few-row product reads, and as the padded rows of the tiled product.
+
+enum : int { kRows = 0, kFragments = 1, kTiles = 2 };
+
+struct QuantizeArgs {
+    const void* x;
+    uint8_t *codes, *scales;
+    size_t rows, cols;
+    uint32_t blocks;      // of a row
+    uint32_t padded;      // blocks that are written of each row (those behind the last are zero)
+    const uint8_t* w_scales;   // kTiles: weight scales that are laid out in the same launch
+    uint8_t* w_tiles;
+    size_t w_rows;
+    uint32_t quantize_groups;
+};
+
+// Byte address of a scale in the tiled product's order: for 32 rows and eight
+// blocks, a 32-bit word for each lane (row % 32, block % 2), its bytes the
+// four steps of the matrix instruction.
+__device__ __forceinline__ size_t tile_scale_at(size_t row, uint32_t block, uint32_t padded) {
+    return ((row / 32) * (padded / 8) + block / 8) * 256 + ((block % 2) * 32 + row % 32) * 4 + block % 8 / 2;
+}
+
+template <int IN, int PLACE, bool FAST>
+__global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(QuantizeArgs a) {
+    constexpr int U = 4;
+    if constexpr (PLACE == kTiles) {
+        if (blockIdx.x >= a.quantize_groups) {
+            // weight scales: a thread gathers one word
+            const size_t chunks = a.padded / 8, words = (a.w_rows + 31) / 32 * chunks * 64;
+            const size_t i = (size_t)(blockIdx.x - a.quantize_groups) * kThreads + threadIdx.x;
+            if (i >= words) return;
+            const uint32_t lane = i % 64;
+            const size_t chunk = i / 64 % chunks, row = i / 64 / chunks * 32 + lane % 32;
+            uint32_t word = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const size_t block = chunk * 8 + 2 * s + lane / 32;
+                const uint32_t byte = row < a.w_rows && block < a.blocks ? a.w_scales[row * a.blocks + block] : 127u;
+                word |= byte << (8 * s);
+            }
+            reinterpret_cast<uint32_t*>(a.w_tiles)[i] = word;
+            return;
+        }
+    }
+    const uint32_t per_row = a.padded * 4;
+    const size_t total = a.rows * per_row;
+    const size_t first = (size_t)blockIdx.x * (U * kThreads) + threadIdx.x;
+    Eight<IN> v[U];
+    size_t row[U];
+    uint32_t part[U];                              // eighth of a row, its block * 4 + lane of the block
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const size_t i = first + (size_t)u * kThreads;
+        v[u] = Eight<IN>{};
+        if (i >= total) continue;
+        if constexpr (FAST && PLACE == kRows) {
+            // rows of whole blocks: the tensor is one row
+            v[u] = load8<IN>(a.x, i * 8);
+        } else {
+            if (total >> 32) {
+                row[u] = i / per_row;
+                part[u] = (uint32_t)(i % per_row);
+            } else {
+                row[u] = (uint32_t)i / per_row;
+                part[u] = (uint32_t)i % per_row;
+            }
+            const size_t e = (size_t)part[u] * 8;
+            if (FAST) {
+                if (e < a.cols) v[u] = load8<IN>(a.x, row[u] * a.cols + e);
+            } else if (e < a.cols) {
+                v[u] = load8_some<IN>(a.x, row[u] * a.cols + e, (int)min((size_t)8, a.cols - e));
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const size_t i = first + (size_t)u * kThreads;
+        const uint32_t byte = scale_byte(quad_max(peak_of<IN>(abs_max<IN>(v[u], 0))));
+        if (i >= total) continue;
+        const uint32_t c = codes8<IN>(v[u], scale_value(byte));
+        const bool leads = threadIdx.x % 4 == 0;
+        if constexpr (PLACE == kRows) {
+            store_b32(a.codes + i * 4, c);
+            if (leads) a.scales[i / 4] = (uint8_t)byte;
+        } else {
+            const uint32_t block = part[u] / 4, quarter = part[u] % 4;
+            const size_t at = PLACE == kFragments
+                                  ? ((row[u] / 16) * (a.padded / 4) + block / 4) * 64 + block % 4 * 16 + row[u] % 16
+                                  : row[u] * a.padded + block;
+            *reinterpret_cast<uint32_t*>(a.codes + at * 16 + quarter * 4) = c;
+            if (leads) a.scales[PLACE == kFragments ? at : tile_scale_at(row[u], block, a.padded)] = (uint8_t)byte;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// dequantize.  A lane writes 16 bytes: eight bf16 or four binary32.  A code
+// has two significant bits, so its product with a power of two is exact in
+// both types.
+
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+    // 0, .5, 1, 1.5 | 2, 3, 4, 6 as the high halves of binary32 values
+    const uint32_t lo = code & 4 ? 0x40404000u : 0x3F000000u, hi = code & 4 ? 0x40C04080u : 0x3FC03F80u;
+    const uint32_t pair = code & 2 ? hi : lo;
+    const uint32_t half = code & 1 ? pair >> 16 : pair & 0xFFFFu;
+    return __builtin_bit_cast(float, (half << 16) | (code & 8) << 28);
+}
+
+template <int OUT, bool FAST>
+__global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, size_t rows,
+                                                                 size_t cols, uint32_t blocks, void* out) {
+    constexpr int P = OUT == kOutBF16 ? 8 : 4, U = 4;
+    const uint32_t per_row = blocks * (32 / P);
+    const size_t total = rows * per_row;
+    const size_t first = (size_t)blockIdx.x * (U * kThreads) + threadIdx.x;
+    uint32_t c[U] = {}, byte[U] = {};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const size_t i = first + (size_t)u * kThreads;
+        if (i >= total) continue;
+        c[u] = P == 8 ? load_b32(codes + i * 4) : load_b16(codes + i * 2);
+        byte[u] = scales[i * P / 32];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const size_t i = first + (size_t)u * kThreads;
+        if (i >= total) continue;
+        const float s = scale_value(byte[u]);
+        float y[P];
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = e2m1_value(c[u] >> (4 * k)) * s;
+        size_t at = i * P;
+        int count = P;
+        if constexpr (!FAST) {
+            const size_t row = total >> 32 ? i / per_row : (uint32_t)i / per_row;
+            const size_t e = (i - row * per_row) * P;
+            if (e >= cols) continue;
+            at = row * cols + e;
+            count = (int)min((size_t)P, cols - e);
+        }
+        if constexpr (OUT == kOutBF16) {
+            const uint4 q = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7]));
+            if constexpr (FAST) {
+                store_b128((uint16_t*)out + at, q);
+            } else {
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    if (k < count) ((uint16_t*)out)[at + k] = (uint16_t)(w[k / 2] >> (16 * (k % 2)));
+            }
+        } else {
+            if constexpr (FAST) {
+                store_b128((float*)out + at, make_uint4(__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1]),
+                                                        __builtin_bit_cast(uint32_t, y[2]), __builtin_bit_cast(uint32_t, y[3])));
+            } else {
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    if (k < count) ((float*)out)[at + k] = y[k];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product, few rows of x: out[r][c] = sum over k of x[r][k] w[c][k].
+//
+// Bound by reading the weights, so these go from memory to registers once and
+// no tile of them waits in LDS: a wave takes 16 CT weight rows ("columns" of
+// the output) and every NW-th step of 128 k, and the waves' sums meet in LDS
+// at the end.  16x16x128 matrix instructions: lane l holds block l / 16 of the
+// step for row l % 16, which is 16 contiguous bytes of codes and one scale.
+// With FUSED a lane quantizes its own block of x (32 elements of one row) in
+// registers, in the layout the instruction wants: no pass over x before the
+// product and no exchange between lanes.
+
+struct LinearArgs {
+    const void* x;
+    const uint8_t *codes, *scales;     // weights
+    const uint8_t *x_codes, *x_scales; // quantized x, in fragments (FUSED: unused) or tiles
+    const uint8_t* w_tiles;            // the tiled product's weight scales
+    void* out;
+    size_t rows, inner, cols;
+    uint32_t blocks;                   // of a weight row
+    uint32_t padded;
+    uint32_t row_tiles, col_tiles;     // of the tiled product
+    int out_kind;
+};
+
+__device__ __forceinline__ mx_i32x8 operand(uint4 q) {
+    return mx_i32x8{(int)q.x, (int)q.y, (int)q.z, (int)q.w, 0, 0, 0, 0};
+}
+
+template <int IN>
+__device__ __forceinline__ void quantize_block(const void* x, size_t at, size_t left, bool aligned, uint4& codes,
+                                               uint32_t& byte) {
+    Eight<IN> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (aligned && left >= 32)
+            v[i] = load8<IN>(x, at + 8 * i);
+        else
+            v[i] = load8_some<IN>(x, at + 8 * i, left > (size_t)(8 * i) ? (int)min((size_t)8, left - 8 * i) : 0);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = abs_max<IN>(v[i], m);
+    byte = scale_byte(peak_of<IN>(m));
+    const float s = scale_value(byte);
+    codes = make_uint4(codes8<IN>(v[0], s), codes8<IN>(v[1], s), codes8<IN>(v[2], s), codes8<IN>(v[3], s));
+}
+
+template <int IN, int MT, int CT, int NW, bool FUSED>
+__global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
+    const size_t c0 = (size_t)blockIdx.x * (16 * CT);
+    const size_t row_bytes = (size_t)a.blocks * 16;
+    const uint8_t* wp[CT];
+    const uint8_t* sp[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+        const size_t c = min(c0 + t * 16 + r, a.cols - 1);
+        wp[t] = a.codes + c * row_bytes;
+        sp[t] = a.scales + c * a.blocks;
+    }
+    const uint32_t steps = a.padded / 4;
+    const bool x_aligned = a.inner % (IN == kInBF16 ? 8 : 4) == 0;
+    mx_f32x4 acc[MT][CT] = {};
+
+    uint4 w[CT];
+    uint32_t ws[CT];
+    auto load = [&](uint32_t s) {
+        const uint32_t block = s * 4 + g;
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            w[t] = make_uint4(0, 0, 0, 0);
+            ws[t] = 127;
+            if (block < a.blocks) {
+                w[t] = load_b128(wp[t] + (size_t)block * 16);
+                ws[t] = sp[t][block];
+            }
+        }
+    };
+    if (wave < steps) load(wave);
+    for (uint32_t s = wave; s < steps; s += NW) {
+        uint4 wc[CT];
+        uint32_t wsc[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) wc[t] = w[t], wsc[t] = ws[t];
+        if (s + NW < steps) load(s + NW);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            uint4 xc = make_uint4(0, 0, 0, 0);
+            uint32_t xs = 127;
+            if constexpr (FUSED) {
+                const size_t row = m * 16 + r, e = (size_t)(s * 4 + g) * 32;
+                if (row < a.rows && e < a.inner)
+                    quantize_block<IN>(a.x, row * a.inner + e, a.inner - e, x_aligned, xc, xs);
+            } else {
+                const size_t at = ((size_t)m * steps + s) * 64 + lane;
+                xc = *reinterpret_cast<const uint4*>(a.x_codes + at * 16);
+                xs = a.x_scales[at];
+            }
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                acc[m][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(wc[t]), operand(xc), acc[m][t], kE2M1,
+                                                                            kE2M1, 0, (int)wsc[t], 0, (int)xs);
+        }
+    }
+
+    // lane l holds x row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 tile
+    __shared__ mx_f32x4 sums[NW][MT * CT][64];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < CT; ++t) sums[wave][m * CT + t][lane] = acc[m][t];
+    __syncthreads();
+    // a thread adds up four columns of a row, in wave order
+    for (uint32_t i = threadIdx.x; i < MT * CT * 64; i += NW * 64) {
+        // neighbouring threads take neighbouring columns
+        const uint32_t m = i / (CT * 64), rest = i % (CT * 64), row16 = rest / (CT * 4), quad = rest % (CT * 4);
+        const uint32_t t = quad / 4, src = quad % 4 * 16 + row16;
+        mx_f32x4 y = sums[0][m * CT + t][src];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) y += sums[v][m * CT + t][src];
+        const size_t row = m * 16 + row16, col = c0 + quad * 4;
+        if (row >= a.rows) continue;
+        const size_t at = row * a.cols + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (col + k >= a.cols) break;
+            if (a.out_kind == kOutBF16)
+                ((uint16_t*)a.out)[at + k] = (uint16_t)pack_bf16x2(y[k], 0.0f);
+            else
+                ((float*)a.out)[at + k] = y[k];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product, many rows: tiles of BM rows of x and BN weight rows, 256 k at a
+// time through LDS in two buffers.  128 bytes of a row are eight blocks; they
+// arrive by direct loads to LDS, whose lanes write 16 bytes each one behind the
+// other, so the order in LDS is chosen by the addresses that the lanes read:
+// block b of row r lies in slot b ^ (r % 8), and the eight rows that a quarter
+// of a fragment read touches lie in eight different bank groups.
+// 32x32x64 matrix instructions: lane l holds block l / 32 of the step for row
+// l % 32.
+
+template <int OUT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(LinearArgs a) {
+    constexpr int NT = (BM / WM) * (BN / WN) * 64;
+    constexpr int TM = WM / 32, TN = WN / 32;
+    __shared__ uint4 a0[BM * 8], a1[BM * 8], b0[BN * 8], b1[BN * 8];
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const uint32_t wm = wave / (BN / WN), wn = wave % (BN / WN);
+
+    // XCD x takes a contiguous range of tiles; within it bands of 8 row tiles,
+    // column tile by column tile, so that what runs at once shares both operands
+    const uint32_t tiles = a.row_tiles * a.col_tiles;
+    const uint32_t t = xcd_tile(blockIdx.x, tiles);
+    const uint32_t band = t / (8 * a.col_tiles), in_band = t % (8 * a.col_tiles);
+    const uint32_t height = min(8u, a.row_tiles - band * 8);
+    const size_t m0 = (size_t)(band * 8 + in_band % height) * BM, n0 = (size_t)(in_band / height) * BN;
+
+    const uint32_t chunks = a.padded / 8;
+    const uint32_t slot_row = tid / 8, block = tid % 8 ^ slot_row % 8;
+    const uint8_t *ap[BM * 8 / NT], *bp[BN * 8 / NT];
+#pragma unroll
+    for (int i = 0; i < BM * 8 / NT; ++i)
+        ap[i] = a.x_codes + (min(m0 + i * (NT / 8) + slot_row, a.rows - 1) * a.padded + block) * 16;
+#pragma unroll
+    for (int i = 0; i < BN * 8 / NT; ++i)
+        bp[i] = a.codes + min(n0 + i * (NT / 8) + slot_row, a.cols - 1) * a.blocks * 16;
+    auto fetch = [&](uint32_t c, uint4* as, uint4* bs) {
+        // behind a row's last block x is padded with zeros, so any block of the weights will do there
+        const size_t bo = (size_t)min(c * 8 + block, a.blocks - 1) * 16;
+#pragma unroll
+        for (int i = 0; i < BM * 8 / NT; ++i)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void*)(ap[i] + (size_t)c * 128),
+                (__attribute__((address_space(3))) void*)(as + i * NT + wave * 64), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < BN * 8 / NT; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(bp[i] + bo),
+                                             (__attribute__((address_space(3))) void*)(bs + i * NT + wave * 64), 16, 0, 0);
+    };
+    const uint32_t* as_tile = reinterpret_cast<const uint32_t*>(a.x_scales) + (m0 + wm * WM) / 32 * chunks * 64 + lane;
+    const uint32_t* bs_tile = reinterpret_cast<const uint32_t*>(a.w_tiles) + (n0 + wn * WN) / 32 * chunks * 64 + lane;
+    int sa[TM], sb[TN];
+    auto fetch_scales = [&](uint32_t c) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = (int)as_tile[((size_t)i * chunks + c) * 64];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sb[j] = (int)bs_tile[((size_t)j * chunks + c) * 64];
+    };
+
+    mx_f32x16 acc[TM][TN] = {};
+    const uint32_t fr = lane % 32, half = lane / 32;
+    auto step = [&](auto S, const uint4* as, const uint4* bs, const int (&ca)[TM], const int (&cb)[TN]) {
+        constexpr int s = decltype(S)::value;
+        mx_i32x8 fa[TM], fb[TN];
+        const uint32_t slot = (2 * s + half) ^ fr % 8;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[i] = operand(as[(wm * WM + i * 32 + fr) * 8 + slot]);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fb[j] = operand(bs[(wn * WN + j * 32 + fr) * 8 + slot]);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], kE2M1, kE2M1, s, ca[i],
+                                                                           s, cb[j]);
+    };
+    auto chunk = [&](uint32_t c, uint4* as, uint4* bs, uint4* an, uint4* bn) {
+        __syncthreads();                            // this chunk has arrived; the other buffer is free
+        int ca[TM], cb[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) ca[i] = sa[i];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) cb[j] = sb[j];
+        if (c + 1 < chunks) {
+            fetch(c + 1, an, bn);
+            fetch_scales(c + 1);
+        }
+        step(std::integral_constant<int, 0>{}, as, bs, ca, cb);
+        step(std::integral_constant<int, 1>{}, as, bs, ca, cb);
+        step(std::integral_constant<int, 2>{}, as, bs, ca, cb);
+        step(std::integral_constant<int, 3>{}, as, bs, ca, cb);
+    };
+    fetch(0, a0, b0);
+    fetch_scales(0);
+    for (uint32_t c = 0; c < chunks; c += 2) {
+        chunk(c, a0, b0, a1, b1);
+        if (c + 1 < chunks) chunk(c + 1, a1, b1, a0, b0);
+    }
+
+    // lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4
+    const bool pairs = OUT == kOutBF16 && a.cols % 2 == 0;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const size_t col = n0 + wn * WN + j * 32 + fr;
+            const size_t row0 = m0 + wm * WM + i * 32 + half * 4;
+            if (pairs) {
+                // neighbouring lanes trade so that each stores two columns of every other row
+                const bool odd = lane % 2;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                    const float mine = odd ? acc[i][j][k + 1] : acc[i][j][k];
+                    const float theirs = dpp_move<kDppSwapAdjacent>(odd ? acc[i][j][k] : acc[i][j][k + 1]);
+                    const uint32_t w = odd ? pack_bf16x2(theirs, mine) : pack_bf16x2(mine, theirs);
+                    const size_t row = row0 + 8 * (k / 4) + k % 4 + odd;
+                    if (row < a.rows && col < a.cols)
+                        store_b32((uint16_t*)a.out + row * a.cols + (col - odd), w);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const size_t row = row0 + 8 * (k / 4) + k % 4;
+                    if (row >= a.rows || col >= a.cols) continue;
+                    const float y = acc[i][j][k];
+                    if constexpr (OUT == kOutBF16)
+                        ((uint16_t*)a.out)[row * a.cols + col] = (uint16_t)pack_bf16x2(y, 0.0f);
+                    else
+                        store_b32((float*)a.out + row * a.cols + col, __builtin_bit_cast(uint32_t, y));
+                }
+            }
+        }
+}
+
+uint32_t groups_for(size_t items, size_t per_group) { return (uint32_t)((items + per_group - 1) / per_group); }
+
+uint32_t round_up(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
+
+template <int IN, int PLACE>
+void quantize_into(const QuantizeArgs& a, uint32_t extra_groups, hipStream_t st) {
+    const uint32_t groups = a.quantize_groups + extra_groups;
+    // whole 16-byte loads: rows start aligned; one flat range: rows of whole blocks
+    const bool fast = PLACE == kRows ? a.cols % 32 == 0 : a.cols % 8 == 0;
+    if (fast)
+        mx4_quantize_kernel<IN, PLACE, true><<<groups, kThreads, 0, st>>>(a);
+    else
+        mx4_quantize_kernel<IN, PLACE, false><<<groups, kThreads, 0, st>>>(a);
+}
+
+template <int PLACE>
+hipError_t quantize_call(QuantizeArgs a, int kind, hipStream_t st) {
+    a.quantize_groups = groups_for(a.rows * a.padded * 4, 4 * kThreads);
+    const uint32_t extra =
+        PLACE == kTiles ? groups_for((a.w_rows + 31) / 32 * (a.padded / 8) * 64, kThreads) : 0;
+    if (kind == kInBF16)
+        quantize_into<kInBF16, PLACE>(a, extra, st);
+    else
+        quantize_into<kInF32, PLACE>(a, extra, st);
+    return hipGetLastError();
+}
+
+template <int IN, int MT, bool FUSED>
+void few_rows(const LinearArgs& a, hipStream_t st) {
+    constexpr int NW = 8;
+    // 64 columns to a workgroup read x least often; fewer where that leaves CUs without work
+    constexpr int CT = MT == 1 ? 4 : MT == 2 ? 4 : 2;
+    if (a.cols >= (size_t)256 * 16 * CT)
+        mx4_few_rows_kernel<IN, MT, CT, NW, FUSED><<<groups_for(a.cols, 16 * CT), NW * 64, 0, st>>>(a);
+    else
+        mx4_few_rows_kernel<IN, MT, 1, NW, FUSED><<<groups_for(a.cols, 16), NW * 64, 0, st>>>(a);
+}
+
+template <int IN, int BM, int BN, int WM, int WN>
+void tiled(LinearArgs& a, hipStream_t st) {
+    a.row_tiles = groups_for(a.rows, BM);
+    a.col_tiles = groups_for(a.cols, BN);
+    mx4_tiled_kernel<IN, BM, BN, WM, WN>
+        <<<a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
+}
+
+constexpr size_t kFusedRows = 16, kFewRows = 64;
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+} // namespace
+
+hipError_t launch_mx4_quantize(const void* x, int kind, size_t rows, size_t cols, uint8_t* codes, uint8_t* scales,
+                               hipStream_t st) {
+    QuantizeArgs a = {};
+    a.x = x, a.codes = codes, a.scales = scales, a.rows = rows, a.cols = cols;
+    a.blocks = a.padded = groups_for(cols, 32);
+    return quantize_call<kRows>(a, kind, st);
+}
+
+hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, size_t cols, void* out, int kind,
+                                 hipStream_t st) {
+    const uint32_t blocks = groups_for(cols, 32);
+    const bool fast = cols % 32 == 0;
+    if (kind == kOutBF16) {
+        const uint32_t groups = groups_for(rows * blocks * 4, 4 * kThreads);
+        if (fast)
+            mx4_dequantize_kernel<kOutBF16, true><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
+        else
+            mx4_dequantize_kernel<kOutBF16, false><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
+    } else {
+        const uint32_t groups = groups_for(rows * blocks * 8, 4 * kThreads);
+        if (fast)
+            mx4_dequantize_kernel<kOutF32, true><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
+        else
+            mx4_dequantize_kernel<kOutF32, false><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
+    }
+    return hipGetLastError();
+}
+
+size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols) {
+    const uint32_t blocks = groups_for(inner, 32);
+    if (rows <= kFusedRows) return 0;
+    if (rows <= kFewRows) {
+        const size_t fragments = (rows + 15) / 16 * round_up(blocks, 4) * 16;
+        return align256(fragments * 16) + align256(fragments);
+    }
+    const size_t padded = round_up(blocks, 8);
+    return align256(rows * padded * 16) + align256((rows + 255) / 256 * 256 * padded) +
+           align256((cols + 255) / 256 * 256 * padded);
+}
+
+hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner, const uint8_t* codes, const uint8_t* scales,
+                             size_t cols, void* out, int out_kind, void* workspace, hipStream_t st) {
+    LinearArgs a = {};
+    a.x = x, a.codes = codes, a.scales = scales, a.out = out, a.out_kind = out_kind;
+    a.rows = rows, a.inner = inner, a.cols = cols;
+    a.blocks = groups_for(inner, 32);
+    if (rows <= kFusedRows) {
+        a.padded = round_up(a.blocks, 4);
+        if (kind == kInBF16)
+            few_rows<kInBF16, 1, true>(a, st);
+        else
+            few_rows<kInF32, 1, true>(a, st);
+        return hipGetLastError();
+    }
+    QuantizeArgs q = {};
+    q.x = x, q.rows = rows, q.cols = inner, q.blocks = a.blocks;
+    q.codes = (uint8_t*)workspace;
+    a.x_codes = q.codes;
+    if (rows <= kFewRows) {
+        q.padded = a.padded = round_up(a.blocks, 4);
+        const size_t fragments = (rows + 15) / 16 * a.padded * 16;
+        q.scales = q.codes + align256(fragments * 16);
+        a.x_scales = q.scales;
+        const hipError_t e = quantize_call<kFragments>(q, kind, st);
+        if (e != hipSuccess) return e;
+        if (rows <= 32)
+            kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
+        else
+            kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);
+        return hipGetLastError();
+    }
+    q.padded = a.padded = round_up(a.blocks, 8);
+    q.scales = q.codes + align256(rows * q.padded * 16);
+    q.w_tiles = q.scales + align256((rows + 255) / 256 * 256 * (size_t)q.padded);
+    q.w_scales = scales;
+    q.w_rows = cols;
+    a.x_scales = q.scales;
+    a.w_tiles = q.w_tiles;
+    const hipError_t e = quantize_call<kTiles>(q, kind, st);
+    if (e != hipSuccess) return e;
+    // the large tile where it gives every CU at least one
+    const size_t large = (size_t)groups_for(rows, 256) * groups_for(cols, 256);
+    if (large >= 256) {
+        if (out_kind == kOutBF16)
+            tiled<kOutBF16, 256, 256, 128, 64>(a, st);
+        else
+            tiled<kOutF32, 256, 256, 128, 64>(a, st);
+    } else {
+        if (out_kind == kOutBF16)
+            tiled<kOutBF16, 128, 128, 64, 64>(a, st);
+        else
+            tiled<kOutF32, 128, 128, 64, 64>(a, st);
+    }
+    return hipGetLastError();
+}
+
+} // namespace qar

@@ -25,6 +25,8 @@ QAR_MAX_STREAMS = 16
 QAR_STATIC_WORKSPACE_BYTES = 64 << 20
 QAR_CHUNK_RUN_ELEMS = 1 << 18
 BLOCK_SIZES = (64, 128, 256)
+QAR_MX4_BLOCK = 32
+QAR_KV8_PAGE = 64
 
 _vp, _sz, _u32, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int
 
@@ -53,6 +55,15 @@ _SIGNATURES = {
     "qar_quantize_reduce_int4": [_vp, _int, _u32, _vp, _vp, _u32, _sz, _u32, _vp, _vp, _vp, _int, _vp],
     "qar_ring_step_int4": [_vp, _vp, _vp, _int, _sz, _u32, _vp, _vp, _vp],
     "qar_dequantize_int4": [_vp, _vp, _sz, _u32, _vp, _int, _vp],
+    "qar_mx4_quantize": [_vp, _int, _sz, _sz, _vp, _vp, _vp],
+    "qar_mx4_dequantize": [_vp, _vp, _sz, _sz, _vp, _int, _vp],
+    "qar_mx4_linear_workspace_bytes": [_sz, _sz, _sz],
+    "qar_mx4_linear": [_vp, _int, _sz, _sz, _vp, _vp, _sz, _vp, _int, _vp, _sz, _vp],
+    "qar_kv8_append": [_vp, _vp, _vp, _vp, _int, _u32, _vp],
+    "qar_kv8_read": [_vp, _vp, _u32, _vp, _vp, _int, _vp],
+    "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int],
+    "qar_kv8_attention": [_vp, _vp, _int, _u32, _u32, _vp, ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
+    "qar_kv8_evict": [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp],
     "qar_status_string": [_int],
     "qar_last_error": [],
 }
@@ -81,7 +92,8 @@ def lib() -> ctypes.CDLL:
         for name, args in _SIGNATURES.items():
             f = getattr(L, name)
             f.argtypes = args
-            f.restype = ctypes.c_char_p if name in ("qar_status_string", "qar_last_error") else _int
+            f.restype = (ctypes.c_char_p if name in ("qar_status_string", "qar_last_error")
+                         else _sz if name.endswith("_workspace_bytes") else _int)
         _lib = L
     return _lib
 
@@ -619,3 +631,246 @@ def qar_dequantize_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, ro
                                      _dev(out, "out").data_ptr(), _dtype_code(out.dtype), _stream(stream)),
            "qar_dequantize_rows")
     return out
+
+
+# ----------------------------------------------------------------------------
+# serving: microscaled 4-bit floating point
+
+
+def _workspace(given, need, device):
+    """(pointer, bytes) of the caller's workspace, or of a new one (torch's
+    allocator reuses its memory only behind the work already on this stream)."""
+    if given is None:
+        if not need:
+            return None, 0, None
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dev(given, "workspace")
+        if given.device != device:
+            raise ValueError(f"workspace is on {given.device}, the call's other tensors on {device}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
+def _matrix(t, what):
+    _dev(t, what)
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have 2 dimensions, not {t.dim()}")
+    return t
+
+
+def _mx4_blocks(cols):
+    return (cols + QAR_MX4_BLOCK - 1) // QAR_MX4_BLOCK
+
+
+def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                     stream=None):
+    """x [rows, cols] (bf16/fp32) -> (E2M1 codes, two per byte, uint8[rows, nb * 16];
+    power-of-two scales uint8[rows, nb]) with nb = ceil(cols / 32)."""
+    rows, cols = _matrix(x, "x").shape
+    dev, nb = x.device, _mx4_blocks(cols)
+    if codes is None:
+        codes = torch.empty((rows, nb * 16), dtype=torch.uint8, device=dev)
+    else:
+        _expect(codes, "codes", rows * nb * 16, (torch.uint8,), dev)
+    if scales is None:
+        scales = torch.empty((rows, nb), dtype=torch.uint8, device=dev)
+    else:
+        _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
+    _check(lib().qar_mx4_quantize(x.data_ptr(), _dtype_code(x.dtype), rows, cols, codes.data_ptr(), scales.data_ptr(),
+                                  _stream(stream)), "qar_mx4_quantize")
+    return codes, scales
+
+
+def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out: torch.Tensor | None = None,
+                       out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """codes uint8[rows, nb * 16], scales uint8[rows, nb] -> out [rows, cols] (bf16 or fp32)."""
+    rows = _matrix(codes, "codes").shape[0]
+    dev, nb = codes.device, _mx4_blocks(cols)
+    _expect(codes, "codes", rows * nb * 16, (torch.uint8,), dev)
+    _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+    else:
+        _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
+    _check(lib().qar_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
+                                    _dtype_code(out.dtype), _stream(stream)), "qar_mx4_dequantize")
+    return out
+
+
+def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, workspace: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """x [rows, inner] (bf16/fp32), quantized on the way, times the transposed mx4
+    weights codes uint8[cols, nb * 16], scales uint8[cols, nb] -> out [rows, cols]
+    (x's type unless out or out_dtype says otherwise).  ``workspace`` (at least
+    lib().qar_mx4_linear_workspace_bytes(rows, inner, cols) bytes) is allocated
+    with torch when not given."""
+    rows, inner = _matrix(x, "x").shape
+    cols = _matrix(codes, "codes").shape[0]
+    dev, nb = x.device, _mx4_blocks(inner)
+    _expect(codes, "codes", cols * nb * 16, (torch.uint8,), dev)
+    _expect(scales, "scales", cols * nb, (torch.uint8,), dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=dev)
+    else:
+        _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
+    L = lib()
+    ws, size, keep = _workspace(workspace, L.qar_mx4_linear_workspace_bytes(rows, inner, cols), dev)
+    _check(L.qar_mx4_linear(x.data_ptr(), _dtype_code(x.dtype), rows, inner, codes.data_ptr(), scales.data_ptr(), cols,
+                            out.data_ptr(), _dtype_code(out.dtype), ws, size, _stream(stream)), "qar_mx4_linear")
+    return out
+
+
+# ----------------------------------------------------------------------------
+# serving: the 8-bit paged cache
+
+
+class _KvStruct(ctypes.Structure):
+    _fields_ = [("k", _vp), ("k_scales", _vp), ("v", _vp), ("v_scales", _vp), ("page_table", _vp), ("lengths", _vp),
+                ("pages", _u32), ("kv_heads", _u32), ("dim", _u32), ("batch", _u32), ("table_width", _u32)]
+
+
+class KvCache:
+    """The tensors of a paged 8-bit cache (qar_kv8_cache in include/qar.h):
+    k int8[pages, kv_heads, 64, dim], v int8[pages, kv_heads, dim, 64],
+    k_scales and v_scales fp32[pages, kv_heads], page_table int32[batch, width],
+    lengths int32[batch].  They stay the caller's; every call looks at them anew."""
+    __slots__ = ("k", "k_scales", "v", "v_scales", "page_table", "lengths")
+
+    def __init__(self, k, k_scales, v, v_scales, page_table, lengths):
+        self.k, self.k_scales, self.v, self.v_scales = k, k_scales, v, v_scales
+        self.page_table, self.lengths = page_table, lengths
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, dim: int, batch: int, table_width: int, device="cuda") -> "KvCache":
+        """A pool of ``pages`` pages and a table without entries."""
+        return cls(torch.zeros((pages, kv_heads, QAR_KV8_PAGE, dim), dtype=torch.int8, device=device),
+                   torch.zeros((pages, kv_heads), dtype=torch.float32, device=device),
+                   torch.zeros((pages, kv_heads, dim, QAR_KV8_PAGE), dtype=torch.int8, device=device),
+                   torch.zeros((pages, kv_heads), dtype=torch.float32, device=device),
+                   torch.full((batch, table_width), -1, dtype=torch.int32, device=device),
+                   torch.zeros(batch, dtype=torch.int32, device=device))
+
+    def _struct(self, what="cache"):
+        k, table, dev = self.k, self.page_table, self.k.device
+        if k.dim() != 4 or k.shape[2] != QAR_KV8_PAGE or table.dim() != 2:
+            raise ValueError(f"{what}.k must be [pages, kv_heads, {QAR_KV8_PAGE}, dim] and {what}.page_table [batch, width]")
+        pages, heads, _, dim = k.shape
+        batch, width = table.shape
+        if tuple(self.v.shape) != (pages, heads, dim, QAR_KV8_PAGE):
+            raise ValueError(f"{what}.v must be {(pages, heads, dim, QAR_KV8_PAGE)}, not {tuple(self.v.shape)}")
+        for name, t, numel, dt in (("k", k, k.numel(), torch.int8), ("v", self.v, k.numel(), torch.int8),
+                                   ("k_scales", self.k_scales, pages * heads, torch.float32),
+                                   ("v_scales", self.v_scales, pages * heads, torch.float32),
+                                   ("page_table", table, batch * width, torch.int32),
+                                   ("lengths", self.lengths, batch, torch.int32)):
+            if t.dtype is not dt or not t.is_cuda or not t.is_contiguous() or t.numel() != numel or t.device != dev:
+                _expect(t, f"{what}.{name}", numel, (dt,), dev)
+        return _KvStruct(k.data_ptr(), self.k_scales.data_ptr(), self.v.data_ptr(), self.v_scales.data_ptr(),
+                         table.data_ptr(), self.lengths.data_ptr(), pages, heads, dim, batch, width)
+
+
+def _shaped(t, what, shape, dtypes, device):
+    if tuple(_dev(t, what).shape) != shape:
+        raise ValueError(f"{what} must be {list(shape)}, not {list(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    return t
+
+
+_INT32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def qar_kv8_append(cache: KvCache, starts: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+    """k_new, v_new [batch, tokens, kv_heads, dim] (bf16/fp32) enter the cache at
+    positions starts[b] (int32[batch]) of every sequence.  ``cache.lengths`` stays as it is."""
+    c = cache._struct()
+    dev, tokens = cache.k.device, k_new.shape[1] if k_new.dim() == 4 else -1
+    shape = (c.batch, tokens, c.kv_heads, c.dim)
+    _shaped(k_new, "k_new", shape, _DATA_DTYPES, dev)
+    _shaped(v_new, "v_new", shape, (k_new.dtype,), dev)
+    _shaped(starts, "starts", (c.batch,), _INT32, dev)
+    _check(lib().qar_kv8_append(ctypes.byref(c), starts.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                _dtype_code(k_new.dtype), tokens, _stream(stream)), "qar_kv8_append")
+
+
+def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: torch.dtype = torch.bfloat16,
+                 out: tuple | None = None, stream=None):
+    """Tokens starts[b] .. starts[b] + tokens - 1 of every sequence as values
+    (k, v), each [batch, tokens, kv_heads, dim]; zeros behind its length.
+    ``out`` = (k, v) receives them instead of new tensors."""
+    c = cache._struct()
+    dev = cache.k.device
+    shape = (c.batch, tokens, c.kv_heads, c.dim)
+    _shaped(starts, "starts", (c.batch,), _INT32, dev)
+    if out is None:
+        k, v = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+    else:
+        k, v = out
+        _shaped(k, "out[0]", shape, _DATA_DTYPES, dev)
+        _shaped(v, "out[1]", shape, (k.dtype,), dev)
+    _check(lib().qar_kv8_read(ctypes.byref(c), starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
+                              _dtype_code(k.dtype), _stream(stream)), "qar_kv8_read")
+    return k, v
+
+
+def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | None = None, scale: float | None = None,
+                      weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of q [batch, queries, heads, dim] (bf16/fp32), the last
+    q_lens[b] (default: all) tokens of every sequence, over the cache -> out like q.
+    ``scale`` defaults to dim ** -0.5.  ``weights`` fp32[batch, kv_heads, width * 64],
+    when given, has the weight that each token received added.  ``workspace`` (at
+    least lib().qar_kv8_attention_workspace_bytes(...) bytes) is allocated with
+    torch when not given."""
+    c = cache._struct()
+    dev = cache.k.device
+    if q.dim() != 4:
+        raise ValueError(f"q must be [batch, queries, heads, dim], not {list(q.shape)}")
+    _, queries, heads, _ = q.shape
+    shape = (c.batch, queries, heads, c.dim)
+    _shaped(q, "q", shape, _DATA_DTYPES, dev)
+    if q_lens is not None:
+        _shaped(q_lens, "q_lens", (c.batch,), _INT32, dev)
+    if weights is not None:
+        _shaped(weights, "weights", (c.batch, c.kv_heads, c.table_width * QAR_KV8_PAGE), _F32, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _shaped(out, "out", shape, (q.dtype,), dev)
+    L = lib()
+    ws, size, keep = _workspace(workspace, L.qar_kv8_attention_workspace_bytes(
+        c.batch, queries, heads, c.kv_heads, c.dim, c.table_width, weights is not None), dev)
+    _check(L.qar_kv8_attention(ctypes.byref(c), q.data_ptr(), _dtype_code(q.dtype), queries, heads,
+                               None if q_lens is None else q_lens.data_ptr(), c.dim ** -0.5 if scale is None else scale,
+                               None if weights is None else weights.data_ptr(), out.data_ptr(), ws, size,
+                               _stream(stream)), "qar_kv8_attention")
+    return out
+
+
+def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: int, keep: int,
+                  kept: torch.Tensor | None = None, moved: torch.Tensor | None = None, stream=None):
+    """``into`` receives, of every sequence and head, the last min(recent, keep)
+    tokens of ``cache`` and the heaviest others, ``keep`` in all, and its lengths
+    -> (kept positions int32[batch, kv_heads, keep], -1 behind them; their weights, 0 behind them)."""
+    c, d = cache._struct(), into._struct("into")
+    dev = cache.k.device
+    if into.k.device != dev:
+        raise ValueError(f"into is on {into.k.device}, cache on {dev}")
+    if not 0 <= recent < 1 << 32 or not 1 <= keep < 1 << 31:
+        raise ValueError(f"recent must be at least 0 and keep at least 1, not {recent} and {keep}")
+    _shaped(weights, "weights", (c.batch, c.kv_heads, c.table_width * QAR_KV8_PAGE), _F32, dev)
+    shape = (c.batch, c.kv_heads, keep)
+    if kept is None:
+        kept = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _shaped(kept, "kept", shape, _INT32, dev)
+    if moved is None:
+        moved = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _shaped(moved, "moved", shape, _F32, dev)
+    _check(lib().qar_kv8_evict(ctypes.byref(c), ctypes.byref(d), weights.data_ptr(), recent, keep, kept.data_ptr(),
+                               moved.data_ptr(), _stream(stream)), "qar_kv8_evict")
+    return kept, moved

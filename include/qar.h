@@ -413,6 +413,155 @@ qar_status qar_ring_step_int4(const uint8_t* codes_in, const float* scales_in, c
 qar_status qar_dequantize_int4(const uint8_t* codes, const float* scales, size_t n, uint32_t block, void* out,
                                qar_dtype out_dtype, void* stream);
 
+/*
+ * Serving a decoder layer.  The calls below are the neighbours of the
+ * quantized AllReduce in a served model: a key/value cache held with the same
+ * int8 codes, and products with 4-bit weights.  They keep the conventions at
+ * the top of this file (asynchronous, checked before anything is enqueued, no
+ * allocation and no synchronization, capturable); what differs is said here.
+ *
+ * Microscaled 4-bit floating point ("mx4").  A block is QAR_MX4_BLOCK
+ * consecutive elements of a row, the last block of a row padded with zeros:
+ *
+ *   scale  2^e  where 2^(e+2) <= absmax < 2^(e+3), e in -126 .. 125
+ *               (subnormal blocks take e = -126, all-zero blocks e = -3);
+ *               stored as the byte 127 + e
+ *   code   the E2M1 value nearest to x_i / 2^e among 0, .5, 1, 1.5, 2, 3, 4, 6
+ *          (codes 0 .. 7), ties to the even code, larger quotients become 6;
+ *          bit 3 is the sign
+ *   value  e2m1(code) * 2^e, exact in binary32 and in bf16
+ *
+ * Codes are uint8_t[rows][nb][16] with nb = ceil(cols / 32), the even element
+ * in the low nibble; scales are uint8_t[rows][nb].  Scale bytes made elsewhere
+ * may be 0 .. 254 (0 is 2^-127).
+ */
+#define QAR_MX4_BLOCK 32
+#define QAR_MX4_MAX_DIM ((size_t)1 << 30) /* of rows and of columns */
+
+/*
+ *   x       [in]  rows * cols elements of `dtype`, 16-byte aligned.
+ *   codes   [out] 16-byte aligned; scales [out].
+ */
+qar_status qar_mx4_quantize(const void* x, qar_dtype dtype, size_t rows, size_t cols, uint8_t* codes,
+                            uint8_t* scales, void* stream);
+/*
+ *   out     [out] rows * cols elements of out_dtype, 16-byte aligned.
+ */
+qar_status qar_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, size_t cols, void* out,
+                              qar_dtype out_dtype, void* stream);
+
+/*
+ * out[r][c] = sum over k of q(x)[r][k] * w[c][k]: the activations x are
+ * quantized on the way (as qar_mx4_quantize does), the weights are mx4 rows
+ * [cols][inner].  Products are exact, sums binary32, the result is rounded
+ * once.  The order of a sum depends on the sizes alone, so equal calls give
+ * equal bits.
+ *   x, out     rows * inner elements of `dtype` and rows * cols of out_dtype,
+ *              16-byte aligned.
+ *   codes, scales  [in] the weights, codes 16-byte aligned.
+ *   workspace  [scratch] qar_mx4_linear_workspace_bytes(rows, inner, cols)
+ *              bytes, 256-byte aligned; NULL when that is 0 (few rows).  It
+ *              needs no preparation and holds nothing between calls; calls
+ *              that may run at the same time need one each.
+ */
+size_t qar_mx4_linear_workspace_bytes(size_t rows, size_t inner, size_t cols);
+qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                          const uint8_t* scales, size_t cols, void* out, qar_dtype out_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * The paged cache of keys and values held in 8 bits ("kv8").  A pool of
+ * `pages` pages of QAR_KV8_PAGE tokens; page p holds, for each of kv_heads
+ * heads, the keys' int8 codes [token][dim], the values' [dim][token], and a
+ * binary32 scale for either (codes, scales and values as for the int8 blocks
+ * at the top of this file, the page of a head being the block).  Sequence b's
+ * token t lies in page page_table[b][t / QAR_KV8_PAGE] at t % QAR_KV8_PAGE.
+ * Codes behind a sequence's last token are unspecified.
+ *   An entry of the page table outside 0 .. pages - 1 is a page that is not
+ * there: nothing is written to it, its tokens read as zeros and attention
+ * sees none of them.  Lengths below 0 count as 0 and those above
+ * table_width * QAR_KV8_PAGE as that.  Pages may be shared by sequences that
+ * only read them; a page that a call writes may appear once in its table.
+ *   dim is 64, 128 or 256 (QAR_ERR_UNSUPPORTED otherwise); k and v are
+ * 16-byte aligned, the other pointers 4-byte.
+ */
+#define QAR_KV8_PAGE 64
+
+typedef struct qar_kv8_cache {
+    int8_t* k;                 /* [pages][kv_heads][QAR_KV8_PAGE][dim] */
+    float* k_scales;           /* [pages][kv_heads] */
+    int8_t* v;                 /* [pages][kv_heads][dim][QAR_KV8_PAGE] */
+    float* v_scales;           /* [pages][kv_heads] */
+    const int32_t* page_table; /* [batch][table_width] */
+    int32_t* lengths;          /* [batch]: tokens held */
+    uint32_t pages, kv_heads, dim, batch, table_width;
+} qar_kv8_cache;
+
+/*
+ * `tokens` new tokens of every sequence enter at positions starts[b] .. of
+ * sequence b.  A page that they enter behind older tokens (positions below
+ * starts[b]) keeps its scale unless they raise its absmax; then its older
+ * values are quantized again with the new scale.  `lengths` is neither read
+ * nor written.  Positions behind the table and pages that are not there are
+ * left out; a negative start leaves the sequence out.
+ *   starts        [in] int32[batch].
+ *   k_new, v_new  [in] [batch][tokens][kv_heads][dim] of `dtype`, 16-byte aligned.
+ */
+qar_status qar_kv8_append(const qar_kv8_cache* cache, const int32_t* starts, const void* k_new, const void* v_new,
+                          qar_dtype dtype, uint32_t tokens, void* stream);
+
+/*
+ * Tokens starts[b] .. starts[b] + tokens - 1 of every sequence as values;
+ * zeros behind its length (and everywhere for a negative start).
+ *   k_out, v_out  [out] [batch][tokens][kv_heads][dim] of out_dtype, 16-byte aligned.
+ */
+qar_status qar_kv8_read(const qar_kv8_cache* cache, const int32_t* starts, uint32_t tokens, void* k_out,
+                        void* v_out, qar_dtype out_dtype, void* stream);
+
+/*
+ * Causal attention of the last q_lens[b] tokens of every sequence over the
+ * cache (which holds them already): query i of sequence b sees its first
+ * lengths[b] - q_lens[b] + i + 1 tokens.
+ *   out[b][i][j] = sum over t of p_t v_t,  p = softmax(scale * q . k_t)
+ * with key head j / (heads / kv_heads) for query head j.  A row that sees no
+ * token gives zeros, and so do rows i >= q_lens[b].  Scores, maxima, sums and
+ * outputs are binary32; the softmax's numerators enter the second product in
+ * binary16 (bf16 queries) or as two binary16 terms (binary32 queries).
+ *   q, out     [batch][queries][heads][dim] of `dtype`, 16-byte aligned;
+ *              heads % kv_heads == 0.
+ *   q_lens     [in, optional] int32[batch]; NULL: `queries` for all.  Clipped
+ *              to 0 .. queries.
+ *   weights    [in/out, optional] float[batch][kv_heads][table_width * QAR_KV8_PAGE]:
+ *              each token's p, summed over the queries and the heads that
+ *              share its key head, is added.  No atomics: equal calls give
+ *              equal bits.
+ *   workspace  [scratch] qar_kv8_attention_workspace_bytes(...) bytes,
+ *              256-byte aligned, as for qar_mx4_linear; with_weights says
+ *              whether weights are passed.
+ */
+size_t qar_kv8_attention_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
+                                         uint32_t dim, uint32_t table_width, int with_weights);
+qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
+                             uint32_t heads, const int32_t* q_lens, float scale, float* weights, void* out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Every sequence and head keeps `keep` tokens: its last min(recent, keep) and,
+ * of the others, those with the largest weights, the lower position where
+ * weights are equal (NaN counts as the largest).  A sequence of at most `keep`
+ * tokens keeps all.  The kept tokens, in order, fill `into`'s pages from
+ * position 0, each page quantized with its own scale, and into->lengths[b]
+ * becomes min(lengths[b], keep).
+ *   cache, into  equal batch, kv_heads and dim.  Their pages must be disjoint
+ *                (one pool may hold both); tables and lengths are their own;
+ *                into->table_width * QAR_KV8_PAGE >= keep.
+ *   weights  [in]  float[batch][kv_heads][table_width * QAR_KV8_PAGE] (cache's).
+ *   kept     [out] int32[batch][kv_heads][keep]: the kept positions, ascending; -1 behind them.
+ *   moved    [out] float[batch][kv_heads][keep]: their weights; 0 behind them.
+ */
+qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, const float* weights,
+                         uint32_t recent, uint32_t keep, int32_t* kept, float* moved, void* stream);
+
 /* Static text for a status code. */
 const char* qar_status_string(qar_status status);
 
