@@ -1026,7 +1026,7 @@ static bool kv8_rows_ok(uint32_t batch, uint32_t queries, uint32_t heads, uint32
     // tiles of 16 rows or more, at most 2048 + width workgroups for the cuts of one
     return queries <= (1u << 30) && rows <= (1u << 30) &&
            (size_t)batch * kv_heads <= kMaxGroups / ((rows + 15) / 16 + 2048 + width) &&
-           (size_t)batch * kv_heads * rows <= QAR_MAX_ELEMENTS / 256;
+           (size_t)batch * kv_heads * rows <= kMaxGroups;
 }
 
 size_t qar_kv8_attention_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,

@@ -46,6 +46,19 @@ __device__ __forceinline__ kv_f32x4 load4(const void* x, size_t e) {
     }
 }
 
+// Elements e .. e + 7, each read once by the caller.
+template <int IN>
+__device__ __forceinline__ void load8(const void* x, size_t e, kv_f32x4 (&v)[2]) {
+    if constexpr (IN == kInBF16) {
+        const uint4 q = load_b128((const uint16_t*)x + e);
+        v[0] = kv_f32x4{bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+        v[1] = kv_f32x4{bf16_lo(q.z), bf16_hi(q.z), bf16_lo(q.w), bf16_hi(q.w)};
+    } else {
+        v[0] = __builtin_bit_cast(kv_f32x4, load_b128((const float*)x + e));
+        v[1] = __builtin_bit_cast(kv_f32x4, load_b128((const float*)x + e + 4));
+    }
+}
+
 template <int OUT>
 __device__ __forceinline__ void store4(void* x, size_t e, kv_f32x4 v) {
     if constexpr (OUT == kOutBF16)
@@ -104,10 +117,10 @@ struct AppendArgs {
 
 template <int DIM, int IN>
 __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
-    constexpr int Q = DIM / 4;              // groups of four channels
-    constexpr int U = kPage * Q / kThreads; // of them for each thread
+    constexpr int Q = DIM / 4, E = DIM / 8;  // groups of four and of eight channels
+    constexpr int U = kPage * E / kThreads;  // of the latter for each thread
     __shared__ float shared[kThreads / 64];
-    __shared__ uint32_t tile[Q][kPage + 1]; // values: word (channels / 4, token)
+    __shared__ uint32_t tile[Q][kPage + 1];  // values: word (channels / 4, token)
     const uint32_t which = blockIdx.x % 2, h = blockIdx.x / 2 % a.c.heads;
     const uint32_t rest = blockIdx.x / 2 / a.c.heads, b = rest / a.touched;
     const int64_t start = a.starts[b];
@@ -125,17 +138,17 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
     int8_t* codes = (which ? a.c.v : a.c.k) + at * (kPage * DIM);
     const float before = old ? *scale_at : 0.0f;
 
-    kv_f32x4 v[U];
+    kv_f32x4 v[U][2];
     float m = 0.0f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int i = u * kThreads + threadIdx.x, t = i / Q, q = i % Q;
-        v[u] = kv_f32x4{};
+        const int i = u * kThreads + threadIdx.x, t = i / E, e = i % E;
+        v[u][0] = v[u][1] = kv_f32x4{};
         if (t < fresh)
-            v[u] = load4<IN>(x, (((size_t)b * a.tokens + (size_t)(lo - start) + t) * a.c.heads + h) * DIM + q * 4);
+            load8<IN>(x, (((size_t)b * a.tokens + (size_t)(lo - start) + t) * a.c.heads + h) * DIM + e * 8, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) m = absmax4(v[u], m);
+    for (int u = 0; u < U; ++u) m = absmax4(v[u][1], absmax4(v[u][0], m));
     const float scale = fmaxf(before, group_max(m, shared) / 127.0f);   // waits until all have read `before`
     const bool grown = scale > before;
     if (threadIdx.x == 0) *scale_at = scale;
@@ -149,13 +162,16 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = u * kThreads + threadIdx.x;
-            if (i / Q < fresh) reinterpret_cast<uint32_t*>(codes)[old * Q + i] = codes4(v[u], scale);
+            if (i / E < fresh)
+                reinterpret_cast<uint2*>(codes)[old * E + i] = make_uint2(codes4(v[u][0], scale), codes4(v[u][1], scale));
         }
     } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = u * kThreads + threadIdx.x;
-            if (i / Q < fresh) tile[i % Q][old + i / Q] = codes4(v[u], scale);
+            const int i = u * kThreads + threadIdx.x, t = i / E, e = i % E;
+            if (t >= fresh) break;
+            tile[2 * e][old + t] = codes4(v[u][0], scale);
+            tile[2 * e + 1][old + t] = codes4(v[u][1], scale);
         }
         __syncthreads();
         // four channels by four tokens at a time
@@ -339,37 +355,43 @@ __device__ __forceinline__ void half_terms(const float (&x)[8], kv_half8 (&out)[
 }
 
 // A lane's share of a query row: runs of RUN channels from channel `first`,
-// one every STEP, as binary16 fragments of eight; returns what undoes the
-// row's factor.  OVER: the lanes that hold the row's other channels.
-template <int IN, int DIM, int RUN, int STEP, int OVER, int T>
-__device__ __forceinline__ float load_query(const void* q, size_t row, int first, bool there,
-                                            kv_half8 (&out)[DIM / STEP * (RUN / 8)][T]) {
-    constexpr int N = DIM / STEP * (RUN / 8);
-    float x[N][8];
-    float m = 0.0f;
+// one every STEP.  Loading and converting are apart so that the cache's loads
+// can be issued between them.  OVER: the lanes that hold the row's other
+// channels.
+template <int IN, int DIM, int RUN, int STEP>
+struct Query {
+    static constexpr int N = DIM / STEP * (RUN / 8);
+    kv_f32x4 x[N][2];
+    __device__ __forceinline__ void load(const void* q, size_t row, int first, bool there) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const size_t e = row * DIM + i / (RUN / 8) * STEP + first + i % (RUN / 8) * 8;
-        kv_f32x4 lo = {}, hi = {};
-        if (there) {
-            lo = load4<IN>(q, e);
-            hi = load4<IN>(q, e + 4);
+        for (int i = 0; i < N; ++i) {
+            const size_t e = row * DIM + i / (RUN / 8) * STEP + first + i % (RUN / 8) * 8;
+            x[i][0] = x[i][1] = kv_f32x4{};
+            if (there) {
+                x[i][0] = load4<IN>(q, e);
+                x[i][1] = load4<IN>(q, e + 4);
+            }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[i][k] = lo[k], x[i][4 + k] = hi[k];
-        m = absmax4(hi, absmax4(lo, m));
     }
-    m = OVER == 16 ? max_over_16(m) : max_over_32(m);
-    const int e = min(268 - (int)(__builtin_bit_cast(uint32_t, m) >> 23), 253);
-    const float f = __builtin_bit_cast(float, (uint32_t)e << 23);
+    // binary16 fragments of eight; returns what undoes the row's factor
+    template <int OVER, int T>
+    __device__ __forceinline__ float convert(kv_half8 (&out)[N][T]) {
+        float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; ++i) m = absmax4(x[i][1], absmax4(x[i][0], m));
+        m = OVER == 16 ? max_over_16(m) : max_over_32(m);
+        const int e = min(268 - (int)(__builtin_bit_cast(uint32_t, m) >> 23), 253);
+        const float f = __builtin_bit_cast(float, (uint32_t)e << 23);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] *= f;
-        half_terms<T>(x[i], out[i]);
+        for (int i = 0; i < N; ++i) {
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[i][k / 4][k % 4] * f;
+            half_terms<T>(y, out[i]);
+        }
+        return __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
     }
-    return __builtin_bit_cast(float, (uint32_t)(254 - e) << 23);
-}
+};
 
 // A sequence's numbers.  Row r of a kv head is query r / group with head
 // r % group of its group; it sees the keys below limit(r).
@@ -419,16 +441,17 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
     const uint32_t first = split * a.pages_per_split, last = min(first + a.pages_per_split, pages);
     if (first >= last && split) return;
 
-    kv_half8 q[MT][DIM / 32][T];
-    float undo[MT];
+    Query<IN, DIM, 16, 64> raw[MT];
     int32_t limit[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
         const uint32_t row = i * 16 + r;
         const bool there = seq.counts(row);
-        undo[i] = load_query<IN, DIM, 16, 64, 16, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there, q[i]) * a.scale;
+        raw[i].load(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there);
         limit[i] = there ? seq.limit(row) : INT32_MAX;       // rows that are not there are not stored
     }
+    kv_half8 q[MT][DIM / 32][T];
+    float undo[MT];
     const int32_t all_see = seq.n - seq.m + 1;               // every row sees the keys below
 
     kv_f32x4 o[MT][VC] = {};
@@ -468,6 +491,10 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
         int32_t id = __builtin_amdgcn_readlane(my_id, 0);
         load_k(id);
         load_v(id);
+        if (base == first + wave) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) undo[i] = raw[i].template convert<16, T>(q[i]) * a.scale;
+        }
         for (uint32_t i = 0; i < count; ++i) {
             const int32_t next = __builtin_amdgcn_readlane(my_id, min(i + 1, count - 1));
             const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i));
@@ -582,34 +609,58 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
     }
 }
 
-// The splits' results joined: a thread has four channels of a row.
+// The splits' results joined.  A workgroup takes one row: DIM / 4 lanes with
+// four channels each, eight times, each time an eighth of the splits, so that
+// few rows with many splits do not wait for one load after another (one group
+// only: 16.0 us instead of the present time for 256 rows of 32 splits).
+constexpr int kJoinGroups = 8;
+
 template <int DIM, int OUT>
-__global__ __launch_bounds__(kThreads) void kv8_join_kernel(AttendArgs a) {
-    const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x, item = i / (DIM / 4);
-    const uint32_t d = (uint32_t)(i % (DIM / 4)) * 4;
-    if (item >= (size_t)a.c.batch * a.c.heads * a.rows) return;
-    const uint32_t row = (uint32_t)(item % a.rows), bh = (uint32_t)(item / a.rows), h = bh % a.c.heads, b = bh / a.c.heads;
+__global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendArgs a) {
+    constexpr int Q = DIM / 4;
+    __shared__ kv_f32x4 ys[kJoinGroups][Q];
+    __shared__ float tops[kJoinGroups], totals[kJoinGroups];
+    const uint32_t item = blockIdx.x, q = threadIdx.x % Q, group = threadIdx.x / Q;
+    const uint32_t row = item % a.rows, bh = item / a.rows, h = bh % a.c.heads, b = bh / a.c.heads;
     const Sequence seq(a, b);
     // the splits that hold keys which this row may see
     const int32_t seen_keys = seq.counts(row) ? min(seq.limit(row), seq.n) : 0;
     const uint32_t pages = seen_keys > 0 ? (uint32_t)(seen_keys + kPage - 1) / kPage : 0;
     const uint32_t used = (pages + a.pages_per_split - 1) / a.pages_per_split;
     float m = -FLT_MAX, l = 0.0f;
-    for (uint32_t s = 0; s < used; ++s) m = fmaxf(m, a.stats[(((size_t)bh * a.splits + s) * a.rows + row) * 2]);
     kv_f32x4 y = {};
-    for (uint32_t s = 0; s < used; ++s) {
+#pragma unroll 4
+    for (uint32_t s = group; s < used; s += kJoinGroups) {
         const size_t at = ((size_t)bh * a.splits + s) * a.rows + row;
-        const float f = __builtin_amdgcn_exp2f(a.stats[at * 2] - m);
-        l = __builtin_fmaf(a.stats[at * 2 + 1], f, l);
-        const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + d);
+        const float2 stat = *reinterpret_cast<const float2*>(a.stats + at * 2);
+        const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + q * 4);
+        const float top = fmaxf(m, stat.x), f = __builtin_amdgcn_exp2f(m - top), e = __builtin_amdgcn_exp2f(stat.x - top);
+        m = top;
+        l = __builtin_fmaf(stat.y, e, l * f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], f, y[k]);
+        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], e, y[k] * f);
+    }
+    ys[group][q] = y;
+    if (q == 0) tops[group] = m, totals[group] = l;
+    __syncthreads();
+    if (group) return;
+    m = tops[0];
+#pragma unroll
+    for (int s = 1; s < kJoinGroups; ++s) m = fmaxf(m, tops[s]);
+    l = 0.0f;
+    y = kv_f32x4{};
+#pragma unroll
+    for (int s = 0; s < kJoinGroups; ++s) {
+        const float f = __builtin_amdgcn_exp2f(tops[s] - m);
+        l = __builtin_fmaf(totals[s], f, l);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(ys[s][q][k], f, y[k]);
     }
     const bool seen = l > 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = seen ? y[k] / l : 0.0f;
-    store4<OUT>(a.out, query_row(a, b, h, row) * DIM + d, y);
-    if (a.lse && d == 0) a.lse[item] = seen ? m - kLift + __builtin_amdgcn_logf(l) : INFINITY;
+    store4<OUT>(a.out, query_row(a, b, h, row) * DIM + q * 4, y);
+    if (a.lse && q == 0) a.lse[item] = seen ? m - kLift + __builtin_amdgcn_logf(l) : INFINITY;
 }
 
 // --- many rows: four waves of 32 rows share a page in LDS, converted to
@@ -617,8 +668,10 @@ __global__ __launch_bounds__(kThreads) void kv8_join_kernel(AttendArgs a) {
 // way to registers meanwhile.  32x32x16 products: lane l = 32 g + r.  Row m of
 // a tile of 32 keys is given the key with bits 2 and 3 of m exchanged: lane
 // half g then receives keys 16 a + 8 g .. + 7, the eight contiguous keys of
-// the values' fragment for step a.  LDS rows are eight 16-byte slots or a
-// multiple, slot c of row r lies at c ^ (r % 8).
+// the values' fragment for step a.  LDS rows are eight 16-byte slots (128 bytes)
+// or a multiple; slot c of row r lies at c ^ (r / 2 % 8), in longer rows at
+// c ^ (r % 16), so that the sixteen lanes that a 16-byte read serves at once
+// lie in different banks.
 
 constexpr int kTileRows = 128;
 
@@ -631,6 +684,7 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
     constexpr int KR = DIM / 8;                        // slots of a row of keys
+    const auto k_swizzle = [](uint32_t row) { return DIM == 64 ? row / 2 % 8 : row % 16; };
     __shared__ kv_half8 k_tile[2][kPage * KR], v_tile[2][DIM * 8];
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, r = lane % 32, g = lane / 32;
     // the last tiles see the most keys: first
@@ -652,7 +706,9 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
     const uint32_t my_last = tile * kTileRows + wave * 32 < seq.rows ? pages_of(tile * kTileRows + wave * 32 + 31) : 0;
 
     kv_half8 q[DIM / 16][T];
-    const float undo = load_query<IN, DIM, 8, 16, 32, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 8, there, q) * a.scale;
+    Query<IN, DIM, 8, 16> raw;
+    raw.load(a.q, there ? query_row(a, b, h, row) : 0, g * 8, there);
+    const float undo = raw.template convert<32, T>(q) * a.scale;
     const int32_t limit = there ? seq.limit(row) : INT32_MAX;
     // every row of the wave sees the keys below (rows without a query see all)
     const int32_t all_see = seq.n - seq.m + (int32_t)((tile * kTileRows + wave * 32) / seq.group) + 1;
@@ -682,11 +738,11 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
         for (int u = 0; u < U; ++u) {
             const uint32_t i = u * kThreads + tid;
             const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
-            k_tile[buffer][lr * KR + (c ^ lr % 8)] = half_codes(kr[u].x, kr[u].y);
-            k_tile[buffer][lr * KR + ((c + 1) ^ lr % 8)] = half_codes(kr[u].z, kr[u].w);
+            k_tile[buffer][lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
+            k_tile[buffer][lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
             const uint32_t d = i / 4, e = i % 4 * 2;
-            v_tile[buffer][d * 8 + (e ^ d % 8)] = half_codes(vr[u].x, vr[u].y);
-            v_tile[buffer][d * 8 + ((e + 1) ^ d % 8)] = half_codes(vr[u].z, vr[u].w);
+            v_tile[buffer][d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
+            v_tile[buffer][d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
         }
     };
 
@@ -706,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const uint32_t lr = t * 32 + r;
-                const kv_half8 k = k_tile[buffer][lr * KR + ((c * 2 + g) ^ lr % 8)];
+                const kv_half8 k = k_tile[buffer][lr * KR + ((c * 2 + g) ^ k_swizzle(lr))];
 #pragma unroll
                 for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
             }
@@ -751,7 +807,7 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
             const uint32_t lr = d * 32 + r;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const kv_half8 v = v_tile[buffer][lr * 8 + ((u * 2 + g) ^ lr % 8)];
+                const kv_half8 v = v_tile[buffer][lr * 8 + ((u * 2 + g) ^ lr / 2 % 8)];
 #pragma unroll
                 for (int e = 0; e < T; ++e) y = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], y, 0, 0, 0);
             }
@@ -803,31 +859,43 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
     const uint32_t wave = blockIdx.x % a.splits * (kThreads / 64) + threadIdx.x / 64;
     const Sequence seq(a, b);
     const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
-    if (wave >= pages || seq.m == 0) return;
+    // a wave has a run of pages
+    const uint32_t run = (pages + waves - 1) / waves, first = wave * run, last = min(first + run, pages);
+    if (first >= last || seq.m == 0) return;
 
+    Query<IN, DIM, 16, 64> raw;
     kv_half8 q[DIM / 32][T];
     float undo = 0.0f, lse = INFINITY;
     int32_t limit = 0;
     auto load_rows = [&](uint32_t tile) {
         const uint32_t row = tile * 16 + r;
         const bool there = seq.counts(row);
-        undo = load_query<IN, DIM, 16, 64, 16, T>(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there, q) * a.scale;
+        raw.load(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there);
         lse = there ? a.lse[(size_t)bh * a.rows + row] : INFINITY;
         limit = there ? seq.limit(row) : 0;
     };
     if (ONE) load_rows(0);
     const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16;
-    for (uint32_t page = wave; page < pages; page += waves) {
-        const int32_t id = valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages);
-        if (id < 0) continue;
-        const size_t at = (size_t)id * a.c.heads + h;
-        const float ks = a.c.k_scales[at];
-        uint4 kr[4][KC];
+    const int32_t* table = a.c.table + (size_t)b * a.c.width;
+    float* weights = a.weights + (size_t)bh * a.c.width * kPage;
+    uint4 kr[4][KC];
+    int32_t id = -1, next_id = -1;
+    float ks = 0.0f, next_ks = 0.0f, old = 0.0f, next_old = 0.0f;
+    auto load_page = [&](uint32_t page) {
+        next_id = valid_page(table[page], a.c.pages);
+        const size_t at = (size_t)max(next_id, 0) * a.c.heads + h;
+        next_ks = a.c.k_scales[at];
+        next_old = weights[page * kPage + lane];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int c = 0; c < KC; ++c)
                 kr[t][c] = *reinterpret_cast<const uint4*>(a.c.k + at * (kPage * DIM) + k_at + t * 4 * DIM + c * 64);
+    };
+    load_page(first);
+    if (ONE) undo = raw.template convert<16, T>(q) * a.scale;
+    for (uint32_t page = first; page < last; ++page) {
+        id = next_id, ks = next_ks, old = next_old;
         kv_f32x4 sum[4] = {};
         const int32_t key0 = (int32_t)(page * kPage + g * 16);
         const uint32_t tiles = ONE ? 1 : (a.rows + 15) / 16;
@@ -836,6 +904,7 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                 // a tile whose last query ends before this page adds nothing
                 if (seq.limit(min(tile * 16 + 15, a.rows - 1)) <= (int32_t)(page * kPage)) continue;
                 load_rows(tile);
+                undo = raw.template convert<16, T>(q) * a.scale;
             }
             kv_f32x4 s[4] = {};
 #pragma unroll
@@ -849,14 +918,16 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[2 * c + 1][e], s[t], 0, 0, 0);
                     }
                 }
+            if (ONE && page + 1 < last) load_page(page + 1);
             const float factor = ks * undo;
-            const int32_t sees = limit - key0;
+            const int32_t sees = id < 0 ? 0 : limit - key0;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     sum[t][k] += 4 * t + k < sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k], factor, -lse)) : 0.0f;
         }
+        if (!ONE && page + 1 < last) load_page(page + 1);
         // over the 16 lanes of a row; lane r of them adds key 16 g + r
         float mine = 0.0f;
 #pragma unroll
@@ -871,7 +942,7 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                 if (r == (uint32_t)(4 * t + k)) mine = v;
             }
         const int32_t key = key0 + (int32_t)r;
-        if (key < seq.n) a.weights[(size_t)bh * a.c.width * kPage + key] += mine;
+        if (key < seq.n && id >= 0) weights[key] = old + mine;
     }
 }
 
@@ -899,6 +970,7 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
 
+template <int HELD>
 __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a) {
     __shared__ uint32_t bins[kBins], wave_sum[kSelectWaves], wave_more[kSelectWaves], wave_equal[kSelectWaves];
     __shared__ uint32_t found_bin, found_above;
@@ -924,16 +996,30 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     }
     if (need == 0) return;
 
+    // wave v has a stretch of tokens, lane i of it every 64th; the first HELD
+    // of a lane stay in registers, those behind are read again where needed
+    const uint32_t stretch = ((free + kSelectThreads - 1) / kSelectThreads) * 64;
+    const uint32_t from = min(wave * stretch, free), to = min(from + stretch, free);
+    float held[HELD];
+#pragma unroll
+    for (int j = 0; j < HELD; ++j) held[j] = from + j * 64 + lane < to ? w[from + j * 64 + lane] : 0.0f;
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j)
+            if (from + j * 64 < to) f(from + j * 64 + lane, held[j]);
+        for (uint32_t base = from + HELD * 64; base < to; base += 64) f(base + lane, base + lane < to ? w[base + lane] : 0.0f);
+    };
+
     uint32_t prefix = 0, mask = 0, left = need;        // the threshold's bits so far, and which they are
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t top = pass == 2 ? 1023 : 2047;
         for (uint32_t i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
         __syncthreads();
-        for (uint32_t i = tid; i < free; i += kSelectThreads) {
-            const uint32_t o = order_of(w[i]);
-            if ((o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
-        }
+        each([&](uint32_t i, float weight) {
+            const uint32_t o = order_of(weight);
+            if (i < to && (o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
+        });
         __syncthreads();
         // tokens in this thread's two bins and in all above them
         const uint32_t hi = bins[2 * tid + 1], lo = bins[2 * tid];
@@ -960,14 +1046,12 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     }
 
     // all above the threshold stay, and the first `left` equal to it
-    const uint32_t stretch = ((free + kSelectThreads - 1) / kSelectThreads) * 64;
-    const uint32_t from = min(wave * stretch, free), to = min(from + stretch, free);
     uint32_t more = 0, equal = 0;
-    for (uint32_t i = from + lane; i < to; i += 64) {
-        const uint32_t o = order_of(w[i]);
-        more += o > prefix;
-        equal += o == prefix;
-    }
+    each([&](uint32_t i, float weight) {
+        const uint32_t o = order_of(weight);
+        more += i < to && o > prefix;
+        equal += i < to && o == prefix;
+    });
     for (int d = 32; d; d /= 2) {
         more += __shfl_xor(more, d);
         equal += __shfl_xor(equal, d);
@@ -977,9 +1061,7 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     uint32_t more_before = 0, equal_before = 0;
     for (uint32_t v = 0; v < wave; ++v) more_before += wave_more[v], equal_before += wave_equal[v];
     const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (uint32_t base = from; base < to; base += 64) {
-        const uint32_t i = base + lane;
-        const float weight = i < to ? w[i] : 0.0f;
+    each([&](uint32_t i, float weight) {
         const uint32_t o = order_of(weight);
         const uint64_t m = __ballot(i < to && o > prefix), e = __ballot(i < to && o == prefix);
         const uint32_t my_more = more_before + __popcll(m & below), my_equal = equal_before + __popcll(e & below);
@@ -990,23 +1072,27 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
         }
         more_before += __popcll(m);
         equal_before += __popcll(e);
-    }
+    });
 }
 
-// Then the move: a workgroup gathers one page of one head, keys or values,
-// keeps its codes in registers between the maximum and the new codes, and
+// Then the move: a workgroup gathers one page of one head, keys and values,
+// keeps their codes in registers between the maxima and the new codes, and
 // writes the page.  Values are gathered byte by byte, a lane for each token:
-// neighbouring kept tokens mostly share the lines of a source page.
+// neighbouring kept tokens mostly share the lines of a source page.  Keys and
+// values go together because a workgroup's time is the chain of loads before
+// them (length, position, page, scale): apart they took 113 us for 128 heads
+// of 4,096 kept tokens.
 template <int DIM>
 __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, uint32_t out_pages) {
     constexpr int Q = DIM / 4, U = kPage * Q / kThreads;
-    __shared__ float shared[kThreads / 64];
+    __shared__ float shared[2][kThreads / 64];
     __shared__ uint32_t tile[kPage][Q + 1];
-    __shared__ int64_t source[kPage];                  // offset of each token's page and head, -1: none
+    __shared__ int64_t source[kPage];                  // each token's page and head, -1: none
     __shared__ int32_t token[kPage];
-    __shared__ float source_scale[kPage];
-    const uint32_t which = blockIdx.x % 2, page = blockIdx.x / 2 % out_pages, bh = blockIdx.x / 2 / out_pages;
-    const uint32_t h = bh % a.c.heads, b = bh / a.c.heads, tid = threadIdx.x;
+    __shared__ float source_k_scale[kPage], source_v_scale[kPage];
+    // a source page feeds neighbouring pages: these run on one XCD, whose L2 then has it
+    const uint32_t unit = xcd_tile(blockIdx.x, gridDim.x), page = unit % out_pages, bh = unit / out_pages;
+    const uint32_t h = bh % a.c.heads, b = bh / a.c.heads, tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const uint32_t n = (uint32_t)min(clamp_length(a.c.lengths[b], a.c.width * kPage), (int32_t)a.keep);
     if (page * kPage >= n) return;
     const int32_t id = valid_page(a.into.table[(size_t)b * a.into.width + page], a.into.pages);
@@ -1022,63 +1108,58 @@ __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, uint32_
         }
         source[tid] = at;
         token[tid] = t % kPage;
-        source_scale[tid] = at < 0 ? 0.0f : (which ? a.c.v_scales : a.c.k_scales)[at];
+        source_k_scale[tid] = at < 0 ? 0.0f : a.c.k_scales[at];
+        source_v_scale[tid] = at < 0 ? 0.0f : a.c.v_scales[at];
     }
     __syncthreads();
     const size_t to = (size_t)id * a.into.heads + h;
-    uint32_t w[U];
-    float m = 0.0f;
-    if (which == 0) {
+    uint32_t kw[U], vw[U];
+    // values: a lane has a token; four channels make a word
+    const int64_t v_at = source[lane];
+    const int8_t* v = a.c.v + (v_at < 0 ? 0 : v_at) * (kPage * DIM) + token[lane];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = u * kThreads + tid, t = i / Q, q = i % Q;
-            w[u] = 0;
-            if (source[t] >= 0)
-                w[u] = *reinterpret_cast<const uint32_t*>(a.c.k + (source[t] * kPage + token[t]) * DIM + q * 4);
-        }
-    } else {
-        // four channels of a token make a word, so that both kinds go on alike
-        const int t = tid % 64;
-        const int64_t at = source[t];
-        const int8_t* v = a.c.v + (at < 0 ? 0 : at) * (kPage * DIM) + token[t];
+    for (int u = 0; u < U; ++u) {
+        const int q = u * (kThreads / 64) + wave;
+        uint32_t x = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int q = u * (kThreads / 64) + tid / 64;
-            uint32_t x = 0;
-            if (at >= 0)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x |= (uint32_t)(uint8_t)v[(q * 4 + k) * kPage] << (8 * k);
-            w[u] = x;
-        }
+        for (int k = 0; k < 4; ++k) x |= (uint32_t)(uint8_t)v[(q * 4 + k) * kPage] << (8 * k);
+        vw[u] = v_at < 0 ? 0 : x;
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        m = absmax4(values4(w[u], source_scale[which ? tid % 64 : (u * kThreads + tid) / Q]), m);
-    const float scale = group_max(m, shared) / 127.0f;
-    if (tid == 0) (which ? a.into.v_scales : a.into.k_scales)[to] = scale;
-    if (which == 0) {
-        uint32_t* codes = reinterpret_cast<uint32_t*>(a.into.k + to * (kPage * DIM));
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + tid, t = i / Q, q = i % Q;
+        const int64_t at = source[t];
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(a.c.k + ((at < 0 ? 0 : at) * kPage + token[t]) * DIM + q * 4);
+        kw[u] = at < 0 ? 0 : x;
+    }
+    float mk = 0.0f, mv = 0.0f;
+    const float v_scale = source_v_scale[lane];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = u * kThreads + tid;
-            codes[i] = codes4(values4(w[u], source_scale[i / Q]), scale);
-        }
-    } else {
+    for (int u = 0; u < U; ++u) {
+        mk = absmax4(values4(kw[u], source_k_scale[(u * kThreads + tid) / Q]), mk);
+        mv = absmax4(values4(vw[u], v_scale), mv);
+    }
+    const float k_new = group_max(mk, shared[0]) / 127.0f, v_new = group_max(mv, shared[1]) / 127.0f;
+    if (tid == 0) a.into.k_scales[to] = k_new, a.into.v_scales[to] = v_new;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            tile[tid % 64][u * (kThreads / 64) + tid / 64] = codes4(values4(w[u], source_scale[tid % 64]), scale);
-        __syncthreads();
-        uint32_t* codes = reinterpret_cast<uint32_t*>(a.into.v + to * (kPage * DIM));
+    for (int u = 0; u < U; ++u) tile[lane][u * (kThreads / 64) + wave] = codes4(values4(vw[u], v_scale), v_new);
+    uint32_t* k_codes = reinterpret_cast<uint32_t*>(a.into.k + to * (kPage * DIM));
 #pragma unroll
-        for (int u = 0; u < U / 4; ++u) {
-            const int i = u * kThreads + tid, q = i / (kPage / 4), t = i % (kPage / 4);
-            uint32_t x[4];
+    for (int u = 0; u < U; ++u) {
+        const int i = u * kThreads + tid;
+        k_codes[i] = codes4(values4(kw[u], source_k_scale[i / Q]), k_new);
+    }
+    __syncthreads();
+    uint32_t* v_codes = reinterpret_cast<uint32_t*>(a.into.v + to * (kPage * DIM));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = tile[t * 4 + k][q];
-            transpose4(x);
+    for (int u = 0; u < U / 4; ++u) {
+        const int i = u * kThreads + tid, q = i / (kPage / 4), t = i % (kPage / 4);
+        uint32_t x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) codes[(q * 4 + k) * (kPage / 4) + t] = x[k];
-        }
+        for (int k = 0; k < 4; ++k) x[k] = tile[t * 4 + k][q];
+        transpose4(x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v_codes[(q * 4 + k) * (kPage / 4) + t] = x[k];
     }
 }
 
@@ -1208,16 +1289,15 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
     if (a.splits > 1) {
         with_dim(c.dim, [&](auto D) {
             with_kind(kind, [&](auto K) {
-                const size_t threads = items * (D() / 4);
-                kv8_join_kernel<D(), K()><<<(uint32_t)((threads + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+                kv8_join_kernel<D(), K()><<<(uint32_t)items, kJoinGroups * D() / 4, 0, st>>>(a);
             });
         });
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (weights) {
-        // a wave for each few pages
-        a.splits = (c.width + 15) / 16;
+        // about eight pages to a wave
+        a.splits = (c.width + 31) / 32;
         with_dim(c.dim, [&](auto D) {
             with_kind(kind, [&](auto K) {
                 const uint32_t g = c.batch * c.heads * a.splits;
@@ -1235,12 +1315,16 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st) {
     EvictArgs a = {c, into, weights, recent, keep, kept, moved};
-    kv8_select_kernel<<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
+    // the table's width bounds the tokens: weights in registers up to 24,576
+    if (c.width * kPage <= kSelectThreads * 8)
+        kv8_select_kernel<8><<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
+    else
+        kv8_select_kernel<24><<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const uint32_t out_pages = (keep + kPage - 1) / kPage;
     with_dim(c.dim, [&](auto D) {
-        kv8_move_kernel<D()><<<c.batch * c.heads * out_pages * 2, kThreads, 0, st>>>(a, out_pages);
+        kv8_move_kernel<D()><<<c.batch * c.heads * out_pages, kThreads, 0, st>>>(a, out_pages);
     });
     return hipGetLastError();
 }

@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(QuantizeArgs a) 
         } else {
             const uint32_t block = part[u] / 4, quarter = part[u] % 4;
             const size_t at = PLACE == kFragments
-                                  ? ((row[u] / 16) * (a.padded / 4) + block / 4) * 64 + block % 4 * 16 + row[u] % 16
+                                  ? (((row[u] / 16) * (a.padded / 8) + block / 8) * 2 + block % 2) * 64 + block % 8 / 2 * 16 + row[u] % 16
                                   : row[u] * a.padded + block;
             *reinterpret_cast<uint32_t*>(a.codes + at * 16 + quarter * 4) = c;
             if (leads) a.scales[PLACE == kFragments ? at : tile_scale_at(row[u], block, a.padded)] = (uint8_t)byte;
@@ -235,6 +235,26 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
     const uint32_t pair = code & 2 ? hi : lo;
     const uint32_t half = code & 1 ? pair >> 16 : pair & 0xFFFFu;
     return __builtin_bit_cast(float, (half << 16) | (code & 8) << 28);
+}
+
+// P values.  The hardware's conversion takes two at a time; scales near the
+// ends of the exponent's range, whose products are subnormal or overflow, are
+// multiplied out.
+template <int P>
+__device__ __forceinline__ void values_of(uint32_t c, uint32_t byte, float (&y)[P]) {
+    const float s = scale_value(byte);
+    if (byte - 4u < 244u) {
+        qar_float2 v[4];
+        v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+        v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+        v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+        v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = v[k / 2][k % 2];
+    } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] = e2m1_value(c >> (4 * k)) * s;
+    }
 }
 
 template <int OUT, bool FAST>
@@ -256,10 +276,8 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
     for (int u = 0; u < U; ++u) {
         const size_t i = first + (size_t)u * kThreads;
         if (i >= total) continue;
-        const float s = scale_value(byte[u]);
         float y[P];
-#pragma unroll
-        for (int k = 0; k < P; ++k) y[k] = e2m1_value(c[u] >> (4 * k)) * s;
+        values_of<P>(c[u], byte[u], y);
         size_t at = i * P;
         int count = P;
         if constexpr (!FAST) {
@@ -298,13 +316,13 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
 //
 // Bound by reading the weights, so these go from memory to registers once and
 // no tile of them waits in LDS: a wave takes 16 CT weight rows ("columns" of
-// the output) and every NW-th step of 128 k, and the waves' sums meet in LDS
-// at the end.  16x16x128 matrix instructions: lane l holds block l / 16 of the
-// step for row l % 16, which is 16 contiguous bytes of codes and one scale.
-// With FUSED a lane quantizes its own block of x (32 elements of one row) in
-// registers, in the layout the instruction wants: no pass over x before the
-// product and no exchange between lanes.
-
+// the output) and a run of the k axis, and the waves' sums meet in LDS at the
+// end.  16x16x128 matrix instructions: lane l = 16 g + r holds one block of
+// row r, 16 contiguous bytes of codes and one scale.  The two instructions of
+// a chunk of eight blocks (128 bytes of a row, a line) take blocks 2 g and
+// 2 g + 1 of lane group g, so that a lane's two loads are neighbours and one
+// 16-bit load brings both scales.
+//   FUSED: the waves quantize x themselves, each its run of k.
 struct LinearArgs {
     const void* x;
     const uint8_t *codes, *scales;     // weights
@@ -323,16 +341,7 @@ __device__ __forceinline__ mx_i32x8 operand(uint4 q) {
 }
 
 template <int IN>
-__device__ __forceinline__ void quantize_block(const void* x, size_t at, size_t left, bool aligned, uint4& codes,
-                                               uint32_t& byte) {
-    Eight<IN> v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (aligned && left >= 32)
-            v[i] = load8<IN>(x, at + 8 * i);
-        else
-            v[i] = load8_some<IN>(x, at + 8 * i, left > (size_t)(8 * i) ? (int)min((size_t)8, left - 8 * i) : 0);
-    }
+__device__ __forceinline__ void quantize_block(const Eight<IN> (&v)[4], uint4& codes, uint32_t& byte) {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = abs_max<IN>(v[i], m);
@@ -341,8 +350,48 @@ __device__ __forceinline__ void quantize_block(const void* x, size_t at, size_t 
     codes = make_uint4(codes8<IN>(v[0], s), codes8<IN>(v[1], s), codes8<IN>(v[2], s), codes8<IN>(v[3], s));
 }
 
+// Scale bytes of blocks b and b + 1 of a row, in the low bytes (of the last
+// block alone in the lowest).
+__device__ __forceinline__ uint32_t scale_pair(const uint8_t* scales, uint32_t b, uint32_t blocks) {
+    if (blocks == 1) return scales[0];
+    uint16_t pair;
+    __builtin_memcpy(&pair, scales + min(b, blocks - 2), 2);
+    return b == blocks - 1 ? pair >> 8 : pair;
+}
+
+// A wave quantizes 256 k of up to 16 rows of x into its own part of LDS: 32
+// lanes read 256 k of a row (whole lines, and no line twice), four neighbours
+// make a block's codes.  Rows behind the last are left out: what their lanes
+// then read from LDS reaches only sums that are not stored.
+template <int IN>
+struct RowsOfX {
+    Eight<IN> raw[8];
+    __device__ __forceinline__ void load(const LinearArgs& a, uint32_t chunk, uint32_t lane) {
+        const size_t k = (size_t)min(chunk * 8 + lane % 32 / 4, a.blocks - 1) * 32 + lane % 4 * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (2u * i >= a.rows) break;
+            raw[i] = load8<IN>(a.x, min((size_t)(2 * i + lane / 32), a.rows - 1) * a.inner + k);
+        }
+    }
+    __device__ __forceinline__ void quantize(const LinearArgs& a, uint32_t lane, uint32_t (&codes)[8][16][4],
+                                             uint8_t (&scales)[8][16]) const {
+        const uint32_t block = lane % 32 / 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (2u * i >= a.rows) break;
+            const uint32_t byte = scale_byte(quad_max(peak_of<IN>(abs_max<IN>(raw[i], 0))));
+            codes[block][2 * i + lane / 32][lane % 4] = codes8<IN>(raw[i], scale_value(byte));
+            if (lane % 4 == 0) scales[block][2 * i + lane / 32] = (uint8_t)byte;
+        }
+        // one wave writes and reads: its own order suffices
+        __builtin_amdgcn_wave_barrier();
+    }
+};
+
 template <int IN, int MT, int CT, int NW, bool FUSED>
 __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
+    static_assert(!FUSED || MT == 1, "rows of one tile");
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
     const size_t c0 = (size_t)blockIdx.x * (16 * CT);
     const size_t row_bytes = (size_t)a.blocks * 16;
@@ -354,66 +403,92 @@ __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
         wp[t] = a.codes + c * row_bytes;
         sp[t] = a.scales + c * a.blocks;
     }
-    const uint32_t steps = a.padded / 4;
-    const bool x_aligned = a.inner % (IN == kInBF16 ? 8 : 4) == 0;
+    const uint32_t chunks = a.padded / 8, run = (chunks + NW - 1) / NW;
+    const uint32_t first = wave * run, last = min(first + run, chunks);
     mx_f32x4 acc[MT][CT] = {};
 
-    uint4 w[CT];
-    uint32_t ws[CT];
-    auto load = [&](uint32_t s) {
-        const uint32_t block = s * 4 + g;
+    // the waves' sums, and before that the wave's own codes and scales of x
+    __shared__ union {
+        mx_f32x4 sums[NW][MT * CT][64];
+        struct {
+            uint32_t codes[8][16][4];
+            uint8_t scales[8][16];
+        } x[FUSED ? NW : 1];
+    } lds;
+
+    // the next chunk's loads are under way while this one's are used
+    RowsOfX<IN> raw;
+    uint4 w[CT][2], xq[FUSED ? 1 : MT][2];
+    uint32_t ws[CT], xs[FUSED ? 1 : MT][2];
+    auto load = [&](uint32_t c) {
+        if constexpr (FUSED) {
+            raw.load(a, c, lane);
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const size_t at = (((size_t)m * chunks + c) * 2 + e) * 64 + lane;
+                    xq[m][e] = *reinterpret_cast<const uint4*>(a.x_codes + at * 16);
+                    xs[m][e] = a.x_scales[at];
+                }
+        }
+        // behind the row's end its last blocks again, against zeros of x
+        const uint32_t b0 = min(c * 8 + 2 * g, a.blocks - 1), b1 = min(b0 + 1, a.blocks - 1);
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
-            w[t] = make_uint4(0, 0, 0, 0);
-            ws[t] = 127;
-            if (block < a.blocks) {
-                w[t] = load_b128(wp[t] + (size_t)block * 16);
-                ws[t] = sp[t][block];
-            }
+            w[t][0] = *reinterpret_cast<const uint4*>(wp[t] + (size_t)b0 * 16);
+            w[t][1] = *reinterpret_cast<const uint4*>(wp[t] + (size_t)b1 * 16);
+            ws[t] = scale_pair(sp[t], b0, a.blocks);
         }
     };
-    if (wave < steps) load(wave);
-    for (uint32_t s = wave; s < steps; s += NW) {
-        uint4 wc[CT];
-        uint32_t wsc[CT];
+    if (first < last) load(first);
+    for (uint32_t c = first; c < last; ++c) {
+        if constexpr (FUSED) raw.quantize(a, lane, lds.x[wave].codes, lds.x[wave].scales);
+        uint4 wc[CT][2], xc[MT][2];
+        uint32_t wsc[CT], xsc[MT][2];
 #pragma unroll
-        for (int t = 0; t < CT; ++t) wc[t] = w[t], wsc[t] = ws[t];
-        if (s + NW < steps) load(s + NW);
+        for (int t = 0; t < CT; ++t) wc[t][0] = w[t][0], wc[t][1] = w[t][1], wsc[t] = ws[t];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            uint4 xc = make_uint4(0, 0, 0, 0);
-            uint32_t xs = 127;
-            if constexpr (FUSED) {
-                const size_t row = m * 16 + r, e = (size_t)(s * 4 + g) * 32;
-                if (row < a.rows && e < a.inner)
-                    quantize_block<IN>(a.x, row * a.inner + e, a.inner - e, x_aligned, xc, xs);
-            } else {
-                const size_t at = ((size_t)m * steps + s) * 64 + lane;
-                xc = *reinterpret_cast<const uint4*>(a.x_codes + at * 16);
-                xs = a.x_scales[at];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (FUSED) {
+                    xc[m][e] = *reinterpret_cast<const uint4*>(lds.x[wave].codes[2 * g + e][r]);
+                    xsc[m][e] = lds.x[wave].scales[2 * g + e][r];
+                } else {
+                    xc[m][e] = xq[m][e];
+                    xsc[m][e] = xs[m][e];
+                }
+                if (c * 8 + 2 * g + e >= a.blocks) xc[m][e] = make_uint4(0, 0, 0, 0);
             }
+        if (c + 1 < last) load(c + 1);
 #pragma unroll
-            for (int t = 0; t < CT; ++t)
-                acc[m][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(wc[t]), operand(xc), acc[m][t], kE2M1,
-                                                                            kE2M1, 0, (int)wsc[t], 0, (int)xs);
-        }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < CT; ++t)
+                    acc[m][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        operand(wc[t][e]), operand(xc[m][e]), acc[m][t], kE2M1, kE2M1, 0, (int)(wsc[t] >> (8 * e)), 0,
+                        (int)xsc[m][e]);
     }
+    if (FUSED) __syncthreads();
 
     // lane l holds x row l % 16 and columns 4 (l / 16) .. + 3 of each 16 x 16 tile
-    __shared__ mx_f32x4 sums[NW][MT * CT][64];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < CT; ++t) sums[wave][m * CT + t][lane] = acc[m][t];
+        for (int t = 0; t < CT; ++t) lds.sums[wave][m * CT + t][lane] = acc[m][t];
     __syncthreads();
     // a thread adds up four columns of a row, in wave order
     for (uint32_t i = threadIdx.x; i < MT * CT * 64; i += NW * 64) {
         // neighbouring threads take neighbouring columns
         const uint32_t m = i / (CT * 64), rest = i % (CT * 64), row16 = rest / (CT * 4), quad = rest % (CT * 4);
         const uint32_t t = quad / 4, src = quad % 4 * 16 + row16;
-        mx_f32x4 y = sums[0][m * CT + t][src];
+        mx_f32x4 y = lds.sums[0][m * CT + t][src];
 #pragma unroll
-        for (int v = 1; v < NW; ++v) y += sums[v][m * CT + t][src];
+        for (int v = 1; v < NW; ++v) y += lds.sums[v][m * CT + t][src];
         const size_t row = m * 16 + row16, col = c0 + quad * 4;
         if (row >= a.rows) continue;
         const size_t at = row * a.cols + col;
@@ -433,17 +508,39 @@ __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
 // time through LDS in two buffers.  128 bytes of a row are eight blocks; they
 // arrive by direct loads to LDS, whose lanes write 16 bytes each one behind the
 // other, so the order in LDS is chosen by the addresses that the lanes read:
-// block b of row r lies in slot b ^ (r % 8), and the eight rows that a quarter
-// of a fragment read touches lie in eight different bank groups.
+// block b of row r lies in slot b ^ (r / 2 % 8), and the sixteen lanes that a
+// 16-byte read serves at once lie in sixteen different groups of four banks
+// (with r % 8 half of the reads' cycles were bank conflicts).
 // 32x32x64 matrix instructions: lane l holds block l / 32 of the step for row
 // l % 32.
+
+// N elements (16 bytes) of an output row from column `col`, as far as the row
+// goes; one store where it is aligned.
+template <int N, class T>
+__device__ __forceinline__ void store_row(T* out, size_t row_at, size_t col, size_t cols, uint4 v) {
+    if (col >= cols) return;
+    T* p = out + row_at + col;
+    if (cols % N == 0) {
+        *reinterpret_cast<uint4*>(p) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if (col + k >= cols) break;
+        if constexpr (sizeof(T) == 2)
+            p[k] = (T)(w[k / 2] >> (16 * (k % 2)));
+        else
+            p[k] = __builtin_bit_cast(T, w[k]);
+    }
+}
 
 template <int OUT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(LinearArgs a) {
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
     constexpr int TM = WM / 32, TN = WN / 32;
     __shared__ uint4 a0[BM * 8], a1[BM * 8], b0[BN * 8], b1[BN * 8];
-    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t wm = wave / (BN / WN), wn = wave % (BN / WN);
 
     // XCD x takes a contiguous range of tiles; within it bands of 8 row tiles,
@@ -455,7 +552,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     const size_t m0 = (size_t)(band * 8 + in_band % height) * BM, n0 = (size_t)(in_band / height) * BN;
 
     const uint32_t chunks = a.padded / 8;
-    const uint32_t slot_row = tid / 8, block = tid % 8 ^ slot_row % 8;
+    const uint32_t slot_row = tid / 8, block = tid % 8 ^ slot_row / 2 % 8;
     const uint8_t *ap[BM * 8 / NT], *bp[BN * 8 / NT];
 #pragma unroll
     for (int i = 0; i < BM * 8 / NT; ++i)
@@ -491,7 +588,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     auto step = [&](auto S, const uint4* as, const uint4* bs, const int (&ca)[TM], const int (&cb)[TN]) {
         constexpr int s = decltype(S)::value;
         mx_i32x8 fa[TM], fb[TN];
-        const uint32_t slot = (2 * s + half) ^ fr % 8;
+        const uint32_t slot = (2 * s + half) ^ fr / 2 % 8;
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[i] = operand(as[(wm * WM + i * 32 + fr) * 8 + slot]);
 #pragma unroll
@@ -500,8 +597,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], kE2M1, kE2M1, s, ca[i],
-                                                                           s, cb[j]);
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], kE2M1, kE2M1, s, cb[j],
+                                                                           s, ca[i]);
     };
     auto chunk = [&](uint32_t c, uint4* as, uint4* bs, uint4* an, uint4* bn) {
         __syncthreads();                            // this chunk has arrived; the other buffer is free
@@ -526,39 +623,46 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
         if (c + 1 < chunks) chunk(c + 1, a1, b1, a0, b0);
     }
 
-    // lane l holds column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4
-    const bool pairs = OUT == kOutBF16 && a.cols % 2 == 0;
+    // The weights are the first operand, so lane l = 32 h + r holds row r of a
+    // subtile and its columns 8 q + 4 h .. + 3 in registers 4 q .. + 3: for
+    // binary32 16 bytes as they are, for bf16 once the halves of the wave have
+    // traded quads (h takes columns 16 p + 8 h .. + 7).
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
+        const size_t row = m0 + wm * WM + i * 32 + fr;
+        if (row >= a.rows) continue;
+        const size_t at = row * a.cols;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const size_t col = n0 + wn * WN + j * 32 + fr;
-            const size_t row0 = m0 + wm * WM + i * 32 + half * 4;
-            if (pairs) {
-                // neighbouring lanes trade so that each stores two columns of every other row
-                const bool odd = lane % 2;
+            const size_t col = n0 + wn * WN + j * 32;
+            if constexpr (OUT == kOutBF16) {
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const float mine = odd ? acc[i][j][k + 1] : acc[i][j][k];
-                    const float theirs = dpp_move<kDppSwapAdjacent>(odd ? acc[i][j][k] : acc[i][j][k + 1]);
-                    const uint32_t w = odd ? pack_bf16x2(theirs, mine) : pack_bf16x2(mine, theirs);
-                    const size_t row = row0 + 8 * (k / 4) + k % 4 + odd;
-                    if (row < a.rows && col < a.cols)
-                        store_b32((uint16_t*)a.out + row * a.cols + (col - odd), w);
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float lo = acc[i][j][8 * p + 2 * k], hi = acc[i][j][8 * p + 2 * k + 1];
+                        w[k] = pack_bf16x2(lo, hi);
+                    }
+                    // quad 2 p (w[0], w[1]) of the upper half against quad 2 p + 1 of the lower
+                    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+                    const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+                    store_row<8>((uint16_t*)a.out, at, col + 16 * p + 8 * half, a.cols, make_uint4(x[0], y[0], x[1], y[1]));
                 }
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const size_t row = row0 + 8 * (k / 4) + k % 4;
-                    if (row >= a.rows || col >= a.cols) continue;
-                    const float y = acc[i][j][k];
-                    if constexpr (OUT == kOutBF16)
-                        ((uint16_t*)a.out)[row * a.cols + col] = (uint16_t)pack_bf16x2(y, 0.0f);
-                    else
-                        store_b32((float*)a.out + row * a.cols + col, __builtin_bit_cast(uint32_t, y));
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float v = acc[i][j][4 * q + k];
+                        w[k] = __builtin_bit_cast(uint32_t, v);
+                    }
+                    store_row<4>((float*)a.out, at, col + 8 * q + 4 * half, a.cols, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
         }
+    }
 }
 
 uint32_t groups_for(size_t items, size_t per_group) { return (uint32_t)((items + per_group - 1) / per_group); }
@@ -588,13 +692,17 @@ hipError_t quantize_call(QuantizeArgs a, int kind, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Two tiles of columns to a workgroup halve the reading of x, one gives twice
+// the workgroups.  Measured, two tiles against one: [5, 3840] x [3840, 15360]
+// 10.3 against 13.4 us, [1, 5376] x [5376, 5376] 8.9 against 7.4; for 32 rows
+// [32, 5376] x [5376, 5376] 12.5 against 14.2, [50, 8000] x [8000, 2880] 17.6
+// against 13.7.  Four tiles and four or sixteen waves were slower than the
+// better of these everywhere but once (2%).
 template <int IN, int MT, bool FUSED>
 void few_rows(const LinearArgs& a, hipStream_t st) {
     constexpr int NW = 8;
-    // 64 columns to a workgroup read x least often; fewer where that leaves CUs without work
-    constexpr int CT = MT == 1 ? 4 : MT == 2 ? 4 : 2;
-    if (a.cols >= (size_t)256 * 16 * CT)
-        mx4_few_rows_kernel<IN, MT, CT, NW, FUSED><<<groups_for(a.cols, 16 * CT), NW * 64, 0, st>>>(a);
+    if (groups_for(a.cols, 32) >= (MT == 1 ? 256u : 160u))
+        mx4_few_rows_kernel<IN, MT, 2, NW, FUSED><<<groups_for(a.cols, 32), NW * 64, 0, st>>>(a);
     else
         mx4_few_rows_kernel<IN, MT, 1, NW, FUSED><<<groups_for(a.cols, 16), NW * 64, 0, st>>>(a);
 }
@@ -607,7 +715,10 @@ void tiled(LinearArgs& a, hipStream_t st) {
         <<<a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
 }
 
-constexpr size_t kFusedRows = 16, kFewRows = 64;
+constexpr size_t kFewRows = 64;
+
+// One tile of rows of whole blocks is quantized inside the product.
+bool fused(size_t rows, size_t inner) { return rows <= 16 && inner % 32 == 0; }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -643,9 +754,9 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, si
 
 size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols) {
     const uint32_t blocks = groups_for(inner, 32);
-    if (rows <= kFusedRows) return 0;
+    if (fused(rows, inner)) return 0;
     if (rows <= kFewRows) {
-        const size_t fragments = (rows + 15) / 16 * round_up(blocks, 4) * 16;
+        const size_t fragments = (rows + 15) / 16 * round_up(blocks, 8) * 16;
         return align256(fragments * 16) + align256(fragments);
     }
     const size_t padded = round_up(blocks, 8);
@@ -659,8 +770,8 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     a.x = x, a.codes = codes, a.scales = scales, a.out = out, a.out_kind = out_kind;
     a.rows = rows, a.inner = inner, a.cols = cols;
     a.blocks = groups_for(inner, 32);
-    if (rows <= kFusedRows) {
-        a.padded = round_up(a.blocks, 4);
+    if (fused(rows, inner)) {
+        a.padded = round_up(a.blocks, 8);
         if (kind == kInBF16)
             few_rows<kInBF16, 1, true>(a, st);
         else
@@ -672,13 +783,15 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     q.codes = (uint8_t*)workspace;
     a.x_codes = q.codes;
     if (rows <= kFewRows) {
-        q.padded = a.padded = round_up(a.blocks, 4);
+        q.padded = a.padded = round_up(a.blocks, 8);
         const size_t fragments = (rows + 15) / 16 * a.padded * 16;
         q.scales = q.codes + align256(fragments * 16);
         a.x_scales = q.scales;
         const hipError_t e = quantize_call<kFragments>(q, kind, st);
         if (e != hipSuccess) return e;
-        if (rows <= 32)
+        if (rows <= 16)
+            kind == kInBF16 ? few_rows<kInBF16, 1, false>(a, st) : few_rows<kInF32, 1, false>(a, st);
+        else if (rows <= 32)
             kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
         else
             kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);

@@ -110,7 +110,8 @@ def declared_functions(header: str = HEADER) -> list[str]:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building the Stream object (2.8 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

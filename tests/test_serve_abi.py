@@ -58,7 +58,7 @@ def test_mx4_dequantize_refusals(L):
 
 def test_mx4_linear_refusals(L):
     f = L.qar_mx4_linear
-    good = dict(x=M, dtype=0, rows=4, inner=100, codes=2 * M, scales=3 * M, cols=50, out=4 * M, out_dtype=0, ws=None, size=0)
+    good = dict(x=M, dtype=0, rows=4, inner=96, codes=2 * M, scales=3 * M, cols=50, out=4 * M, out_dtype=0, ws=None, size=0)
 
     def call(**kw):
         return f(*{**good, **kw}.values(), None)
@@ -67,8 +67,8 @@ def test_mx4_linear_refusals(L):
         assert call(**{name: None}) == INV, name
     assert call(dtype=2) == UNS and call(out_dtype=7) == UNS
     assert call(x=M + 2) == MIS and call(codes=2 * M + 8) == MIS and call(out=4 * M + 4) == MIS
-    assert call(out=M + 784) == INV and call(out=2 * M) == INV and call(scales=4 * M + 399) == INV
-    need = L.qar_mx4_linear_workspace_bytes(40, 100, 50)
+    assert call(out=M + 752) == INV and call(out=2 * M) == INV and call(scales=4 * M + 399) == INV
+    need = L.qar_mx4_linear_workspace_bytes(40, 96, 50)
     assert need > 0
     assert call(rows=40) == INV                                      # no workspace
     assert call(rows=40, ws=8 * M, size=need - 1) == INV
@@ -83,8 +83,8 @@ def test_mx4_linear_refusals(L):
 def test_mx4_linear_workspace(L):
     size = L.qar_mx4_linear_workspace_bytes
     assert size(0, 1, 1) == size(1, 0, 1) == size(1, 1, 0) == 0
-    assert size(1, 5000, 5000) == 0                                  # few rows are quantized in registers
-    for rows in (17, 64, 65, 1000):
+    assert size(16, 4992, 5000) == 0                                 # few rows of whole blocks are quantized in registers
+    for rows in (1, 17, 64, 65, 1000):
         assert size(rows, 1000, 300) >= rows * 32 * 17               # the codes and scales of x
         assert size(rows, 1000, 300) % 256 == 0
     assert size(1 << 31, 64, 64) == 0
