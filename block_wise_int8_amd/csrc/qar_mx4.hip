@@ -11,6 +11,8 @@
 // (tests/test_gpu_mx4.py compares them with the definition).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "qar_device.h"
 #include "qar_launch.h"
 
@@ -535,11 +537,23 @@ __device__ __forceinline__ void store_row(T* out, size_t row_at, size_t col, siz
     }
 }
 
+// Waits until at most N of the wave's loads are under way (and no LDS read
+// is), then for the workgroup.  __syncthreads would wait for all of them.
+template <int N>
+__device__ __forceinline__ void arrive() {
+    static_assert(N < 64, "vmcnt");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 template <int OUT, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(LinearArgs a) {
+    static_assert(BM == BN, "one size of buffer");
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
-    constexpr int TM = WM / 32, TN = WN / 32;
-    __shared__ uint4 a0[BM * 8], a1[BM * 8], b0[BN * 8], b1[BN * 8];
+    constexpr int TM = WM / 32, TN = WN / 32, LOADS = BM * 8 / NT;
+    __shared__ uint4 s0[BM * 8], s1[BM * 8], s2[BM * 8], s3[BM * 8], s4[BM * 8];
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t wm = wave / (BN / WN), wn = wave % (BN / WN);
 
@@ -553,30 +567,32 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
 
     const uint32_t chunks = a.padded / 8;
     const uint32_t slot_row = tid / 8, block = tid % 8 ^ slot_row / 2 % 8;
-    const uint8_t *ap[BM * 8 / NT], *bp[BN * 8 / NT];
+    // offsets from the tile's first rows: 256 rows of 2^24 k at most are 2^31 bytes
+    const uint8_t *x_base = a.x_codes + m0 * a.padded * 16, *w_base = a.codes + n0 * a.blocks * 16;
+    uint32_t x_at[LOADS], w_at[LOADS];
 #pragma unroll
-    for (int i = 0; i < BM * 8 / NT; ++i)
-        ap[i] = a.x_codes + (min(m0 + i * (NT / 8) + slot_row, a.rows - 1) * a.padded + block) * 16;
-#pragma unroll
-    for (int i = 0; i < BN * 8 / NT; ++i)
-        bp[i] = a.codes + min(n0 + i * (NT / 8) + slot_row, a.cols - 1) * a.blocks * 16;
-    auto fetch = [&](uint32_t c, uint4* as, uint4* bs) {
+    for (int i = 0; i < LOADS; ++i) {
+        const uint32_t row = i * (NT / 8) + slot_row;
+        x_at[i] = (uint32_t)min((size_t)row, a.rows - 1 - m0) * a.padded * 16 + block * 16;
+        w_at[i] = (uint32_t)min((size_t)row, a.cols - 1 - n0) * a.blocks * 16;
+    }
+    // load i of the thread's LOADS
+    auto fetch_x = [&](uint32_t c, uint4* to, int i) {
+        const uint8_t* base = x_base + (size_t)min(c, chunks - 1) * 128;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(base + x_at[i]),
+                                         (__attribute__((address_space(3))) void*)(to + i * NT + wave * 64), 16, 0, 0);
+    };
+    auto fetch_w = [&](uint32_t c, uint4* to, int i) {
         // behind a row's last block x is padded with zeros, so any block of the weights will do there
-        const size_t bo = (size_t)min(c * 8 + block, a.blocks - 1) * 16;
-#pragma unroll
-        for (int i = 0; i < BM * 8 / NT; ++i)
-            __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) void*)(ap[i] + (size_t)c * 128),
-                (__attribute__((address_space(3))) void*)(as + i * NT + wave * 64), 16, 0, 0);
-#pragma unroll
-        for (int i = 0; i < BN * 8 / NT; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(bp[i] + bo),
-                                             (__attribute__((address_space(3))) void*)(bs + i * NT + wave * 64), 16, 0, 0);
+        const uint32_t at = min(c * 8 + block, a.blocks - 1) * 16;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(w_base + (w_at[i] + at)),
+                                         (__attribute__((address_space(3))) void*)(to + i * NT + wave * 64), 16, 0, 0);
     };
     const uint32_t* as_tile = reinterpret_cast<const uint32_t*>(a.x_scales) + (m0 + wm * WM) / 32 * chunks * 64 + lane;
     const uint32_t* bs_tile = reinterpret_cast<const uint32_t*>(a.w_tiles) + (n0 + wn * WN) / 32 * chunks * 64 + lane;
     int sa[TM], sb[TN];
-    auto fetch_scales = [&](uint32_t c) {
+    auto fetch_scales = [&](uint32_t chunk) {
+        const uint32_t c = min(chunk, chunks - 1);
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = (int)as_tile[((size_t)i * chunks + c) * 64];
 #pragma unroll
@@ -585,14 +601,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
 
     mx_f32x16 acc[TM][TN] = {};
     const uint32_t fr = lane % 32, half = lane / 32;
-    auto step = [&](auto S, const uint4* as, const uint4* bs, const int (&ca)[TM], const int (&cb)[TN]) {
+    // byte offset of a fragment for step 0; step s differs in bits 5 and 6 only
+    const uint32_t fx0 = (wm * WM + fr) * 128 + (half ^ fr / 2 % 8) * 16, fw0 = (wn * WN + fr) * 128 + (half ^ fr / 2 % 8) * 16;
+    auto step = [&](auto S, const uint4* xs, const uint4* ws, uint32_t fx, uint32_t fw, const int (&ca)[TM],
+                    const int (&cb)[TN], auto loads) {
         constexpr int s = decltype(S)::value;
         mx_i32x8 fa[TM], fb[TN];
-        const uint32_t slot = (2 * s + half) ^ fr / 2 % 8;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = operand(as[(wm * WM + i * 32 + fr) * 8 + slot]);
+        for (int i = 0; i < TM; ++i)
+            fa[i] = operand(*reinterpret_cast<const uint4*>((const char*)xs + (fx ^ (32 * s)) + i * 32 * 128));
 #pragma unroll
-        for (int j = 0; j < TN; ++j) fb[j] = operand(bs[(wn * WN + j * 32 + fr) * 8 + slot]);
+        for (int j = 0; j < TN; ++j)
+            fb[j] = operand(*reinterpret_cast<const uint4*>((const char*)ws + (fw ^ (32 * s)) + j * 32 * 128));
+        loads();
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -600,68 +621,109 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
                 acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], kE2M1, kE2M1, s, cb[j],
                                                                            s, ca[i]);
     };
-    auto chunk = [&](uint32_t c, uint4* as, uint4* bs, uint4* an, uint4* bn) {
-        __syncthreads();                            // this chunk has arrived; the other buffer is free
+    // Chunk c's x lies in buffer 2 c % 5 and its weights in (2 c + 1) % 5.
+    // When chunk c begins, the buffers of chunk c - 1 are free: the weights of
+    // chunk c + 1 and then x of chunk c + 2 are asked for, spread over the
+    // steps, because waves that all issue their loads first wait for the
+    // address units with the matrix units idle.  Behind the last chunk the
+    // last is asked for again, which keeps the counts.
+    auto chunk = [&](uint32_t c, uint4* xs, uint4* ws, uint4* w_next, uint4* x_after) {
+        arrive<LOADS>();                            // all but x of chunk c + 1
         int ca[TM], cb[TN];
 #pragma unroll
         for (int i = 0; i < TM; ++i) ca[i] = sa[i];
 #pragma unroll
         for (int j = 0; j < TN; ++j) cb[j] = sb[j];
-        if (c + 1 < chunks) {
-            fetch(c + 1, an, bn);
+        // the five buffers' fragment addresses would not fit the registers
+        uint32_t fx = fx0, fw = fw0;
+        asm volatile("" : "+v"(fx), "+v"(fw));
+        step(std::integral_constant<int, 0>{}, xs, ws, fx, fw, ca, cb, [&] {
+#pragma unroll
+            for (int i = 0; i < LOADS / 2; ++i) fetch_w(c + 1, w_next, i);
+        });
+        step(std::integral_constant<int, 1>{}, xs, ws, fx, fw, ca, cb, [&] {
+#pragma unroll
+            for (int i = LOADS / 2; i < LOADS; ++i) fetch_w(c + 1, w_next, i);
             fetch_scales(c + 1);
-        }
-        step(std::integral_constant<int, 0>{}, as, bs, ca, cb);
-        step(std::integral_constant<int, 1>{}, as, bs, ca, cb);
-        step(std::integral_constant<int, 2>{}, as, bs, ca, cb);
-        step(std::integral_constant<int, 3>{}, as, bs, ca, cb);
+            asm volatile("" ::: "memory");          // x last: what arrive() lets pass
+        });
+        step(std::integral_constant<int, 2>{}, xs, ws, fx, fw, ca, cb, [&] {
+#pragma unroll
+            for (int i = 0; i < LOADS / 2; ++i) fetch_x(c + 2, x_after, i);
+        });
+        step(std::integral_constant<int, 3>{}, xs, ws, fx, fw, ca, cb, [&] {
+#pragma unroll
+            for (int i = LOADS / 2; i < LOADS; ++i) fetch_x(c + 2, x_after, i);
+        });
     };
-    fetch(0, a0, b0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fetch_x(0, s0, i);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fetch_w(0, s1, i);
     fetch_scales(0);
-    for (uint32_t c = 0; c < chunks; c += 2) {
-        chunk(c, a0, b0, a1, b1);
-        if (c + 1 < chunks) chunk(c + 1, a1, b1, a0, b0);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) fetch_x(1, s2, i);
+    // Whole rounds of the buffers and then the rest, nested: where paths meet
+    // on which different loads are the last, the compiler would wait for all.
+    uint32_t c = 0;
+    for (; c + 5 <= chunks; c += 5) {
+        chunk(c, s0, s1, s3, s4);
+        chunk(c + 1, s2, s3, s0, s1);
+        chunk(c + 2, s4, s0, s2, s3);
+        chunk(c + 3, s1, s2, s4, s0);
+        chunk(c + 4, s3, s4, s1, s2);
     }
-
-    // The weights are the first operand, so lane l = 32 h + r holds row r of a
-    // subtile and its columns 8 q + 4 h .. + 3 in registers 4 q .. + 3: for
-    // binary32 16 bytes as they are, for bf16 once the halves of the wave have
-    // traded quads (h takes columns 16 p + 8 h .. + 7).
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const size_t row = m0 + wm * WM + i * 32 + fr;
-        if (row >= a.rows) continue;
-        const size_t at = row * a.cols;
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const size_t col = n0 + wn * WN + j * 32;
-            if constexpr (OUT == kOutBF16) {
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float lo = acc[i][j][8 * p + 2 * k], hi = acc[i][j][8 * p + 2 * k + 1];
-                        w[k] = pack_bf16x2(lo, hi);
-                    }
-                    // quad 2 p (w[0], w[1]) of the upper half against quad 2 p + 1 of the lower
-                    const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-                    const auto y = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-                    store_row<8>((uint16_t*)a.out, at, col + 16 * p + 8 * half, a.cols, make_uint4(x[0], y[0], x[1], y[1]));
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float v = acc[i][j][4 * q + k];
-                        w[k] = __builtin_bit_cast(uint32_t, v);
-                    }
-                    store_row<4>((float*)a.out, at, col + 8 * q + 4 * half, a.cols, make_uint4(w[0], w[1], w[2], w[3]));
-                }
+    if (c < chunks) {
+        chunk(c, s0, s1, s3, s4);
+        if (c + 1 < chunks) {
+            chunk(c + 1, s2, s3, s0, s1);
+            if (c + 2 < chunks) {
+                chunk(c + 2, s4, s0, s2, s3);
+                if (c + 3 < chunks) chunk(c + 3, s1, s2, s4, s0);
             }
         }
+    }
+    arrive<0>();                                    // nothing may write to LDS that is no longer this workgroup's
+
+    // The weights are the first operand, so lane l = 32 h + r holds row r of a
+    // subtile and its columns 8 q + 4 h .. + 3 in registers 4 q .. + 3.  They
+    // pass through the wave's own stretch of LDS, a few subtiles of rows at a
+    // time, so that a store writes whole lines: eight lanes a row of 128 bytes
+    // (straight from the registers a store touches 32 rows with 32 bytes each).
+    // 16-byte slot c of row r lies at c ^ (r % 8) of its group of eight.
+    using T = std::conditional_t<OUT == kOutBF16, uint16_t, float>;
+    // Half a buffer to a wave: every buffer is read out, and none is being written.
+    constexpr int ROW = WN * sizeof(T), HALF = BM * 64, NOW = std::min(HALF / (32 * ROW), TM);
+    static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
+    char* strip = reinterpret_cast<char*>(wave < 2 ? s0 : wave < 4 ? s1 : wave < 6 ? s2 : s3) + wave % 2 * HALF;
+#pragma unroll
+    for (int i0 = 0; i0 < TM; i0 += NOW) {
+#pragma unroll
+        for (int i = 0; i < NOW; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t row = i * 32 + fr, at = (j * 32 + 8 * q + 4 * half) * sizeof(T);
+                    char* to = strip + row * ROW + (at & ~127u) + ((at / 16 % 8 ^ row % 8) * 16) + at % 16;
+                    const float y0 = acc[i0 + i][j][4 * q], y1 = acc[i0 + i][j][4 * q + 1], y2 = acc[i0 + i][j][4 * q + 2],
+                                y3 = acc[i0 + i][j][4 * q + 3];
+                    if constexpr (OUT == kOutBF16)
+                        *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
+                    else
+                        *reinterpret_cast<mx_f32x4*>(to) = mx_f32x4{y0, y1, y2, y3};
+                }
+        __builtin_amdgcn_wave_barrier();
+        constexpr int PER = ROW / 16;               // lanes to a row
+#pragma unroll
+        for (int k = 0; k < NOW * 32 * PER / 64; ++k) {
+            const uint32_t row = k * (64 / PER) + lane / PER, c = lane % PER;
+            const uint4 v = *reinterpret_cast<const uint4*>(strip + row * ROW + (c & ~7u) * 16 + ((c % 8 ^ row % 8) * 16));
+            const size_t r = m0 + wm * WM + i0 * 32 + row;
+            if (r < a.rows) store_row<16 / sizeof(T)>((T*)a.out, r * a.cols, n0 + wn * WN + c * (16 / sizeof(T)), a.cols, v);
+        }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 

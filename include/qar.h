@@ -436,7 +436,7 @@ qar_status qar_dequantize_int4(const uint8_t* codes, const float* scales, size_t
  * may be 0 .. 254 (0 is 2^-127).
  */
 #define QAR_MX4_BLOCK 32
-#define QAR_MX4_MAX_DIM ((size_t)1 << 30) /* of rows and of columns */
+#define QAR_MX4_MAX_DIM ((size_t)1 << 24) /* of rows and of columns */
 
 /*
  *   x       [in]  rows * cols elements of `dtype`, 16-byte aligned.
