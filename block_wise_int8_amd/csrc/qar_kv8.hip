@@ -274,8 +274,40 @@ __global__ __launch_bounds__(kThreads) void kv8_read_kernel(ReadArgs a) {
 // element).  The softmax's numerators enter the second product multiplied by
 // 2^14, in one term (an error of 2^-12 of each, for outputs that are rounded
 // to 2^-9) or, for binary32, two.  Sums, maxima and outputs are binary32.
-
+//
+// A page's value scale enters with the numerators, as its ratio to the largest
+// scale so far (`Unit`), so that the second product adds to the outputs
+// directly; these are in that largest scale's units.  The ratio is at most 1
+// and costs nothing (its logarithm is part of the exponent); numerators times
+// ratio below 2^-28 of the row's largest are binary16 subnormals, off by up
+// to 2^-39 of the largest scale's values.
 constexpr float kLift = 14.0f;          // log2 of the numerators' factor
+
+struct Unit {
+    float unit = 0.0f;   // outputs are in units of this scale
+    float lift = kLift;  // log2 of the numerators' factor for this page ...
+    float drop = 1.0f;   // ... and what undoes the ratio in it
+    // The next page's scale; returns what the outputs so far are multiplied by.
+    __device__ __forceinline__ float next(float scale) {
+        float shrink = 1.0f;
+        if (scale > unit) {
+            shrink = unit / scale;
+            unit = scale;
+        }
+        // a ratio below 2^-60 leaves nothing of the page, but its numerators still count;
+        // hardware reciprocals and logarithms are good to a unit in the last place
+        const float ratio = unit > 0.0f ? fminf(fmaxf(scale * __builtin_amdgcn_rcpf(unit), 0x1p-60f), 1.0f) : 1.0f;
+        lift = kLift + __builtin_amdgcn_logf(ratio);
+        drop = __builtin_amdgcn_rcpf(ratio);
+        return shrink;
+    }
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
 
 struct AttendArgs {
     Kv8 c;
@@ -286,7 +318,8 @@ struct AttendArgs {
     float* lse;                         // log2 of each row's sum, for the weights; may be null
     float* weights;
     uint32_t queries, heads, group, rows, splits, pages_per_split, tiles;
-    float scale;                        // of the scores, times log2(e)
+    float scale;                        // of the scores, times log2(e), without its sign
+    bool negative;                      // its sign, which the queries take
 };
 
 // The maximum and the sum over lanes i, i + 32 and over lanes i, i + 16, ...:
@@ -375,13 +408,13 @@ struct Query {
     }
     // binary16 fragments of eight; returns what undoes the row's factor
     template <int OVER, int T>
-    __device__ __forceinline__ float convert(kv_half8 (&out)[N][T]) {
+    __device__ __forceinline__ float convert(bool negative, kv_half8 (&out)[N][T]) {
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) m = absmax4(x[i][1], absmax4(x[i][0], m));
         m = OVER == 16 ? max_over_16(m) : max_over_32(m);
         const int e = min(268 - (int)(__builtin_bit_cast(uint32_t, m) >> 23), 253);
-        const float f = __builtin_bit_cast(float, (uint32_t)e << 23);
+        const float f = __builtin_bit_cast(float, (uint32_t)e << 23 | (negative ? 0x80000000u : 0u));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             float y[8];
@@ -430,8 +463,10 @@ __device__ __forceinline__ void store1(void* x, size_t e, float v) {
 // tiles, which are the 16 contiguous bytes that it loads of each channel of
 // the values.
 
+// Two waves to a SIMD where the registers allow: the compiler then keeps the
+// products' results where the softmax can use them without a move.
 template <int DIM, int MT, int IN, int NW>
-__global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
+__global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_attend_few_kernel(AttendArgs a) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int KC = DIM / 64, VC = DIM / 16;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
@@ -455,6 +490,7 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
     const int32_t all_see = seq.n - seq.m + 1;               // every row sees the keys below
 
     kv_f32x4 o[MT][VC] = {};
+    Unit unit;
     float top[MT], total[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) top[i] = -FLT_MAX, total[i] = 0.0f;
@@ -493,7 +529,7 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
         load_v(id);
         if (base == first + wave) {
 #pragma unroll
-            for (int i = 0; i < MT; ++i) undo[i] = raw[i].template convert<16, T>(q[i]) * a.scale;
+            for (int i = 0; i < MT; ++i) undo[i] = raw[i].template convert<16, T>(a.negative, q[i]) * a.scale;
         }
         for (uint32_t i = 0; i < count; ++i) {
             const int32_t next = __builtin_amdgcn_readlane(my_id, min(i + 1, count - 1));
@@ -505,35 +541,43 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const kv_half8 lo = half_codes(kr[t][c].x, kr[t][c].y), hi = half_codes(kr[t][c].z, kr[t][c].w);
+                for (int u = 0; u < 2; ++u) {
+                    kv_half8 k[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        k[t] = u ? half_codes(kr[t][c].z, kr[t][c].w) : half_codes(kr[t][c].x, kr[t][c].y);
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
 #pragma unroll
-                        for (int e = 0; e < T; ++e) {
-                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[j][2 * c][e], s[j][t], 0, 0, 0);
-                            s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[j][2 * c + 1][e], s[j][t], 0, 0, 0);
-                        }
+                        for (int e = 0; e < T; ++e)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[t], q[j][2 * c + u][e], s[j][t], 0, 0, 0);
                 }
             if (i + 1 < count) load_k(next);
 
+            const float shrink_all = unit.next(vs);
+            if (shrink_all != 1.0f)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink_all;
             kv_half8 p[MT][2][T];
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
-                const float factor = ks * undo[j];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) s[j][t] *= factor;
+                float factor = ks * undo[j];
                 if (key0 + kPage > all_see || id < 0) {
                     const int32_t sees = (id < 0 ? 0 : limit[j]) - key0 - (int32_t)g * 16;
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) s[j][t][k] = 4 * t + k < sees ? s[j][t][k] : -INFINITY;
+                        for (int k = 0; k < 4; ++k) s[j][t][k] = 4 * t + k < sees ? s[j][t][k] * factor : -INFINITY;
+                    factor = 1.0f;
                 }
-                float m = -FLT_MAX;
+                float m = max3(s[j][0][0], s[j][0][1], s[j][0][2]);
 #pragma unroll
-                for (int t = 0; t < 4; ++t) m = fmaxf(fmaxf(fmaxf(m, s[j][t][0]), fmaxf(s[j][t][1], s[j][t][2])), s[j][t][3]);
-                m = fmaxf(max_over_16(m), top[j]);
+                for (int k = 3; k < 15; k += 2) m = max3(m, s[j][k / 4][k % 4], s[j][(k + 1) / 4][(k + 1) % 4]);
+                m = fmaxf(max_over_16(fmaxf(m, s[j][3][3])) * factor, top[j]);
                 if (__any(m > top[j])) {
                     const float shrink = __builtin_amdgcn_exp2f(top[j] - m);
                     total[j] *= shrink;
@@ -541,30 +585,33 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
                     for (int c = 0; c < VC; ++c) o[j][c] *= shrink;
                     top[j] = m;
                 }
-                const float off = kLift - m;
+                const float off = unit.lift - m;
+                float sum = 0.0f;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float x[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = __builtin_amdgcn_exp2f(s[j][2 * u + k / 4][k % 4] + off);
-                    total[j] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                    for (int k = 0; k < 8; ++k)
+                        x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][2 * u + k / 4][k % 4], factor, off));
+                    sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
                     half_terms<T>(x, p[j][u]);
                 }
+                total[j] = __builtin_fmaf(sum, unit.drop, total[j]);
             }
+            // two tiles at a time, so that neighbouring products add to different ones
 #pragma unroll
-            for (int c = 0; c < VC; ++c) {
-                const kv_half8 lo = half_codes(vr[c].x, vr[c].y), hi = half_codes(vr[c].z, vr[c].w);
+            for (int c = 0; c < VC; c += 2) {
+                const kv_half8 v[2][2] = {{half_codes(vr[c].x, vr[c].y), half_codes(vr[c + 1].x, vr[c + 1].y)},
+                                          {half_codes(vr[c].z, vr[c].w), half_codes(vr[c + 1].z, vr[c + 1].w)}};
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    kv_f32x4 y = {};
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int e = 0; e < T; ++e) {
-                        y = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, p[j][0][e], y, 0, 0, 0);
-                        y = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, p[j][1][e], y, 0, 0, 0);
-                    }
+                    for (int e = 0; e < T; ++e)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) o[j][c][k] = __builtin_fmaf(y[k], vs, o[j][c][k]);
-                }
+                        for (int j = 0; j < MT; ++j)
+#pragma unroll
+                            for (int d = 0; d < 2; ++d)
+                                o[j][c + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u][d], p[j][u][e], o[j][c + d], 0, 0, 0);
             }
             if (i + 1 < count) load_v(next);
             id = next;
@@ -581,7 +628,7 @@ __global__ __launch_bounds__(NW * 64) void kv8_attend_few_kernel(AttendArgs a) {
             total[j] = sum_over_16(total[j]);
             if (g == 0) tops[wave][r] = top[j], totals[wave][r] = total[j];
 #pragma unroll
-            for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[j][c];
+            for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[j][c] * unit.unit;
         }
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < 16 * DIM; i += NW * 64) {
@@ -665,13 +712,19 @@ __global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendA
 
 // --- many rows: four waves of 32 rows share a page in LDS, converted to
 // binary16 once for all of them, in two buffers; the page behind it is on its
-// way to registers meanwhile.  32x32x16 products: lane l = 32 g + r.  Row m of
-// a tile of 32 keys is given the key with bits 2 and 3 of m exchanged: lane
-// half g then receives keys 16 a + 8 g .. + 7, the eight contiguous keys of
-// the values' fragment for step a.  LDS rows are eight 16-byte slots (128 bytes)
-// or a multiple; slot c of row r lies at c ^ (r / 2 % 8), in longer rows at
-// c ^ (r % 16), so that the sixteen lanes that a 16-byte read serves at once
-// lie in different banks.
+// way to registers meanwhile.  Bound by the two products and the softmax's
+// arithmetic together (0.6 of the binary16 rate that a large matrix product
+// reaches, of it 0.5 for causal prompts).  Measured and left out: the next
+// page's scores formed beside this page's exponentials, eight waves with half
+// the keys each, raised priorities for the longest tiles: each within 4% or
+// slower.
+//
+// 32x32x16 products: lane l = 32 g + r.  Row m of a tile of 32 keys is given
+// the key with bits 2 and 3 of m exchanged: lane half g then receives keys 16
+// a + 8 g .. + 7, the eight contiguous keys of the values' fragment for step
+// a.  LDS rows are eight 16-byte slots (128 bytes) or a multiple; slot c of
+// row r lies at c ^ (r / 2 % 8), in longer rows at c ^ (r % 16), so that the
+// sixteen lanes that a 16-byte read serves at once lie in different banks.
 
 constexpr int kTileRows = 128;
 
@@ -679,84 +732,115 @@ __device__ __forceinline__ uint32_t exchange_bits_2_3(uint32_t v) {
     return (v & ~12u) | (v & 4u) << 1 | (v & 8u) >> 1;
 }
 
+// A barrier for LDS alone: __syncthreads would also wait for the loads from
+// memory that are under way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 template <int DIM, int IN>
-__global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void kv8_attend_many_kernel(AttendArgs a) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
     constexpr int KR = DIM / 8;                        // slots of a row of keys
     const auto k_swizzle = [](uint32_t row) { return DIM == 64 ? row / 2 % 8 : row % 16; };
     __shared__ kv_half8 k_tile[2][kPage * KR], v_tile[2][DIM * 8];
-    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, r = lane % 32, g = lane / 32;
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), r = lane % 32,
+                   g = lane / 32;
     // the last tiles see the most keys: first
     const uint32_t split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
     const uint32_t bh = rest % (a.c.heads * a.c.batch), tile = a.tiles - 1 - rest / (a.c.heads * a.c.batch);
     const uint32_t h = bh % a.c.heads, b = bh / a.c.heads;
-    const Sequence seq(a, b);
-    const uint32_t row = tile * kTileRows + wave * 32 + r;
-    const bool there = seq.counts(row);
+    const uint32_t first_row = tile * kTileRows + wave * 32, row = first_row + r;
 
-    // pages that the tile's last row and the wave's last row see
-    const auto pages_of = [&](uint32_t last_row) {
-        const int32_t i = min((int32_t)(min(last_row, seq.rows - 1) / seq.group), seq.m - 1);
-        const int32_t keys = seq.m > 0 && (int32_t)(tile * kTileRows / seq.group) < seq.m ? seq.n - seq.m + i + 1 : 0;
-        return keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u;
-    };
-    const uint32_t first = split * a.pages_per_split;
-    const uint32_t last = min(first + a.pages_per_split, pages_of(tile * kTileRows + kTileRows - 1));
-    const uint32_t my_last = tile * kTileRows + wave * 32 < seq.rows ? pages_of(tile * kTileRows + wave * 32 + 31) : 0;
-
-    kv_half8 q[DIM / 16][T];
+    // Loads that depend on no other come first: a row of queries whatever the
+    // sequence's length, and the first pages, which are used if they count.
     Query<IN, DIM, 8, 16> raw;
-    raw.load(a.q, there ? query_row(a, b, h, row) : 0, g * 8, there);
-    const float undo = raw.template convert<32, T>(q) * a.scale;
-    const int32_t limit = there ? seq.limit(row) : INT32_MAX;
-    // every row of the wave sees the keys below (rows without a query see all)
-    const int32_t all_see = seq.n - seq.m + (int32_t)((tile * kTileRows + wave * 32) / seq.group) + 1;
-
-    kv_f32x16 o[DIM / 32] = {};
-    float top = -FLT_MAX, total = 0.0f;
-
-    uint4 kr[U], vr[U];
-    int32_t id = -1, next_id = -1;
-    float ks = 0.0f, vs = 0.0f, next_ks = 0.0f, next_vs = 0.0f;
+    raw.load(a.q, query_row(a, b, h, min(row, a.rows - 1)), g * 8, true);
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
-    auto load_page = [&](uint32_t p) {
-        next_id = valid_page(table[p], a.c.pages);
-        const size_t at = (size_t)max(next_id, 0) * a.c.heads + h;
-        next_ks = next_id < 0 ? 0.0f : a.c.k_scales[at];    // what page 0 holds must not matter
-        next_vs = next_id < 0 ? 0.0f : a.c.v_scales[at];
-        const int8_t* k = a.c.k + at * (kPage * DIM) + tid * 16;
-        const int8_t* v = a.c.v + at * (kPage * DIM) + tid * 16;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            kr[u] = *reinterpret_cast<const uint4*>(k + u * kThreads * 16);
-            vr[u] = *reinterpret_cast<const uint4*>(v + u * kThreads * 16);
-        }
+    const uint32_t first = split * a.pages_per_split, limit_page = min(first + a.pages_per_split, a.c.width);
+    uint4 kr[U], vr[U];
+    // The pages' numbers and scales come 64 at a time, one in each lane: looked
+    // up one by one, every page would wait for a scalar load, and with it for
+    // the wave's LDS reads.  Asked for in ascending order; pages behind
+    // `limit_page` are read as the one before it and not used.
+    struct Page {
+        int32_t id;
+        float ks, vs;          // 0 for a page that is not there: what page 0 holds must not matter
     };
-    auto put_page = [&](int buffer) {
+    uint32_t base = first;
+    int32_t my_id;
+    float my_ks, my_vs;
+    auto look_up = [&] {
+        my_id = valid_page(table[min(base + lane, limit_page - 1)], a.c.pages);
+        const size_t at = (size_t)max(my_id, 0) * a.c.heads + h;
+        my_ks = my_id < 0 ? 0.0f : a.c.k_scales[at];
+        my_vs = my_id < 0 ? 0.0f : a.c.v_scales[at];
+    };
+    auto page_at = [&](uint32_t page) {
+        if (page - base >= 64) {
+            base = page;
+            look_up();
+        }
+        const uint32_t i = page - base;
+        return Page{__builtin_amdgcn_readlane(my_id, i),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i)),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i))};
+    };
+    auto load_k = [&](int32_t id) {
+        const int8_t* k = a.c.k + ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) kr[u] = *reinterpret_cast<const uint4*>(k + u * kThreads * 16);
+    };
+    auto load_v = [&](int32_t id) {
+        const int8_t* v = a.c.v + ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) vr[u] = *reinterpret_cast<const uint4*>(v + u * kThreads * 16);
+    };
+    auto put_k = [&](int buffer) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const uint32_t i = u * kThreads + tid;
             const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
             k_tile[buffer][lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
             k_tile[buffer][lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
-            const uint32_t d = i / 4, e = i % 4 * 2;
+        }
+    };
+    auto put_v = [&](int buffer) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid, d = i / 4, e = i % 4 * 2;
             v_tile[buffer][d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
             v_tile[buffer][d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
         }
     };
+    look_up();
+    Page now = page_at(first), next = page_at(first + 1);
+    load_k(now.id);
+    load_v(now.id);
 
-    if (first < last) load_page(first);
-    for (uint32_t page = first; page < last; ++page) {
-        const int buffer = (page - first) % 2;
-        put_page(buffer);
-        id = next_id, ks = next_ks, vs = next_vs;
-        __syncthreads();                    // the page before last is no longer read
-        if (page + 1 < last) load_page(page + 1);
-        if (page >= my_last) continue;
-        const int32_t key0 = (int32_t)(page * kPage);
+    const Sequence seq(a, b);
+    const bool there = seq.counts(row);
+    // pages that the tile's last row and the wave's last row see
+    const auto pages_of = [&](uint32_t last_row) {
+        const int32_t i = min((int32_t)(min(last_row, seq.rows - 1) / seq.group), seq.m - 1);
+        const int32_t keys = seq.m > 0 && (int32_t)(tile * kTileRows / seq.group) < seq.m ? seq.n - seq.m + i + 1 : 0;
+        return keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u;
+    };
+    const uint32_t last = min(limit_page, pages_of(tile * kTileRows + kTileRows - 1));
+    const uint32_t my_last = first_row < seq.rows ? min(last, pages_of(first_row + 31)) : 0;
+    const int32_t limit = there ? seq.limit(row) : INT32_MAX;
+    // every row of the wave sees the keys below (rows without a query see all)
+    const int32_t all_see = seq.n - seq.m + (int32_t)(first_row / seq.group) + 1;
 
-        kv_f32x16 s[2] = {};
+    kv_half8 q[DIM / 16][T];
+    const float undo = raw.template convert<32, T>(a.negative, q) * a.scale;
+
+    kv_f32x16 o[DIM / 32] = {};
+    Unit unit;
+    float top = -FLT_MAX, total = 0.0f;
+    auto scores = [&](int buffer, kv_f32x16 (&s)[2]) {
+        s[0] = s[1] = kv_f32x16{};
 #pragma unroll
         for (int c = 0; c < DIM / 16; ++c)
 #pragma unroll
@@ -766,81 +850,112 @@ __global__ __launch_bounds__(kThreads) void kv8_attend_many_kernel(AttendArgs a)
 #pragma unroll
                 for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
             }
+    };
 
-        const float factor = ks * undo;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) s[t] *= factor;
-        if (key0 + kPage > all_see || id < 0) {
-            // register k of tile t is key 32 t + 16 (k / 8) + 8 g + k % 8
-            const int32_t sees = (id < 0 ? 0 : limit) - key0 - (int32_t)g * 8;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int k = 0; k < 16; ++k) s[t][k] = 32 * t + 16 * (k / 8) + k % 8 < sees ? s[t][k] : -INFINITY;
+    if (first < last) {
+        put_k(0);
+        put_v(0);
+        load_k(next.id);
+        load_v(next.id);
+    }
+    // At a page's beginning: its codes are in LDS (behind the barrier), the
+    // next page's in registers or on their way there.
+    for (uint32_t page = first; page < last; ++page) {
+        const int even = (page - first) % 2;
+        lds_barrier();
+        const Page after = page_at(page + 2);
+        if (page + 1 < last) {
+            put_k(even ^ 1);
+            put_v(even ^ 1);
+            load_k(after.id);
+            load_v(after.id);
         }
-        float m = -FLT_MAX;
+        if (page < my_last && now.id >= 0) {
+            kv_f32x16 s[2];
+            scores(even, s);
+            const int32_t key0 = (int32_t)(page * kPage);
+            const float shrink_all = unit.next(now.vs);
+            if (shrink_all != 1.0f)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+                for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink_all;
+            float factor = now.ks * undo;
+            if (key0 + kPage > all_see) {
+                // register k of tile t is key 32 t + 16 (k / 8) + 8 g + k % 8
+                const int32_t sees = limit - key0 - (int32_t)g * 8;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) m = fmaxf(m, s[t][k]);
-        m = fmaxf(max_over_32(m), top);
-        if (__any(m > top)) {
-            const float shrink = __builtin_amdgcn_exp2f(top - m);
-            total *= shrink;
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink;
-            top = m;
-        }
-        const float off = kLift - m;
-        kv_half8 p[4][T];
+                    for (int k = 0; k < 16; ++k)
+                        s[t][k] = 32 * t + 16 * (k / 8) + k % 8 < sees ? s[t][k] * factor : -INFINITY;
+                factor = 1.0f;
+            }
+            float m = max3(s[0][15], s[1][15], s[0][14]);
+            float m1 = max3(s[1][14], s[0][13], s[1][13]);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            float x[8];
+            for (int k = 0; k < 12; k += 2) {
+                m = max3(m, s[0][k], s[0][k + 1]);
+                m1 = max3(m1, s[1][k], s[1][k + 1]);
+            }
+            m = max3(m, s[0][12], s[1][12]);
+            m = fmaxf(max_over_32(fmaxf(m, m1)) * factor, top);
+            // outputs and sums are taken to the new maximum when it has grown by
+            // 2^1.5, which the numerators' type has room for
+            if (__any(m > top + 1.5f)) {
+                const float shrink = __builtin_amdgcn_exp2f(top - m);
+                total *= shrink;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __builtin_amdgcn_exp2f(s[u / 2][u % 2 * 8 + k] + off);
-            total += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-            half_terms<T>(x, p[u]);
-        }
-#pragma unroll
-        for (int d = 0; d < DIM / 32; ++d) {
-            kv_f32x16 y = {};
-            const uint32_t lr = d * 32 + r;
+                for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink;
+                top = m;
+            }
+            const float off = unit.lift - top;
+            kv_half8 p[4][T];
+            float sum = 0.0f;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const kv_half8 v = v_tile[buffer][lr * 8 + ((u * 2 + g) ^ lr / 2 % 8)];
+                float x[8];
 #pragma unroll
-                for (int e = 0; e < T; ++e) y = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], y, 0, 0, 0);
+                for (int k = 0; k < 8; ++k)
+                    x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][u % 2 * 8 + k], factor, off));
+                sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                half_terms<T>(x, p[u]);
             }
+            total = __builtin_fmaf(sum, unit.drop, total);
+            // neighbouring products add to different tiles: none waits for the one before it
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[d][k] = __builtin_fmaf(y[k], vs, o[d][k]);
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int d = 0; d < DIM / 32; ++d) {
+                    const uint32_t lr = d * 32 + r;
+                    const kv_half8 v = v_tile[even][lr * 8 + ((u * 2 + g) ^ lr / 2 % 8)];
+#pragma unroll
+                    for (int e = 0; e < T; ++e) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], o[d], 0, 0, 0);
+                }
         }
+        now = next, next = after;
     }
 
     total = sum_over_32(total);
     if (row >= a.rows) return;
+    const bool seen = there && total > 0.0f;
+    const float f = a.splits > 1 ? unit.unit : seen ? unit.unit / total : 0.0f;
+    const size_t at = a.splits > 1 ? (((size_t)bh * a.splits + split) * a.rows + row) * DIM : query_row(a, b, h, row) * DIM;
     // register k of tile d is channel 32 d + 8 (k / 4) + 4 g + k % 4
-    if (a.splits == 1) {
-        const bool seen = there && total > 0.0f;
-        const float f = seen ? 1.0f / total : 0.0f;
-        const size_t at = query_row(a, b, h, row) * DIM + g * 4;
 #pragma unroll
-        for (int d = 0; d < DIM / 32; ++d)
+    for (int d = 0; d < DIM / 32; ++d)
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                const kv_f32x4 y = {o[d][k] * f, o[d][k + 1] * f, o[d][k + 2] * f, o[d][k + 3] * f};
-                store4<IN>(a.out, at + d * 32 + k * 2, seen ? y : kv_f32x4{});
-            }
-        if (a.lse && g == 0) a.lse[(size_t)bh * a.rows + row] = seen ? top - kLift + __builtin_amdgcn_logf(total) : INFINITY;
-    } else {
-        const size_t at = ((size_t)bh * a.splits + split) * a.rows + row;
-#pragma unroll
-        for (int d = 0; d < DIM / 32; ++d)
-#pragma unroll
-            for (int k = 0; k < 16; k += 4)
-                *reinterpret_cast<kv_f32x4*>(a.part + at * DIM + d * 32 + k * 2 + g * 4) =
-                    kv_f32x4{o[d][k], o[d][k + 1], o[d][k + 2], o[d][k + 3]};
-        if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
-    }
+        for (int k = 0; k < 16; k += 4) {
+            const kv_f32x4 y = {o[d][k] * f, o[d][k + 1] * f, o[d][k + 2] * f, o[d][k + 3] * f};
+            const size_t to = at + d * 32 + k * 2 + g * 4;
+            if (a.splits > 1)
+                *reinterpret_cast<kv_f32x4*>(a.part + to) = y;
+            else
+                store4<IN>(a.out, to, seen ? y : kv_f32x4{});
+        }
+    if (g) return;
+    if (a.splits > 1)
+        a.stats[at / DIM * 2] = top, a.stats[at / DIM * 2 + 1] = total;
+    else if (a.lse)
+        a.lse[(size_t)bh * a.rows + row] = seen ? top - kLift + __builtin_amdgcn_logf(total) : INFINITY;
 }
 
 // --- the weights that the keys received: with every row's log2 sum known, a
@@ -893,7 +1008,7 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                 kr[t][c] = *reinterpret_cast<const uint4*>(a.c.k + at * (kPage * DIM) + k_at + t * 4 * DIM + c * 64);
     };
     load_page(first);
-    if (ONE) undo = raw.template convert<16, T>(q) * a.scale;
+    if (ONE) undo = raw.template convert<16, T>(a.negative, q) * a.scale;
     for (uint32_t page = first; page < last; ++page) {
         id = next_id, ks = next_ks, old = next_old;
         kv_f32x4 sum[4] = {};
@@ -904,7 +1019,7 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                 // a tile whose last query ends before this page adds nothing
                 if (seq.limit(min(tile * 16 + 15, a.rows - 1)) <= (int32_t)(page * kPage)) continue;
                 load_rows(tile);
-                undo = raw.template convert<16, T>(q) * a.scale;
+                undo = raw.template convert<16, T>(a.negative, q) * a.scale;
             }
             kv_f32x4 s[4] = {};
 #pragma unroll
@@ -1260,7 +1375,8 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
     AttendArgs a = {};
     a.c = c, a.q = q, a.q_lens = q_lens, a.out = out, a.weights = weights;
     a.queries = queries, a.heads = heads, a.group = heads / c.heads, a.rows = queries * a.group;
-    a.scale = scale * 1.44269504088896340736f;
+    a.scale = (scale < 0 ? -scale : scale) * 1.44269504088896340736f;
+    a.negative = scale < 0;
     const Plan p = plan_for(c.batch, c.heads, a.rows, c.dim, c.width);
     a.tiles = p.tiles, a.splits = p.splits, a.pages_per_split = p.pages_per_split;
     const size_t items = (size_t)c.batch * c.heads * a.rows;
