@@ -1026,16 +1026,17 @@ static bool kv8_rows_ok(uint32_t batch, uint32_t queries, uint32_t heads, uint32
     // tiles of 16 rows or more, at most 2048 + width workgroups for the cuts of one
     return queries <= (1u << 30) && rows <= (1u << 30) &&
            (size_t)batch * kv_heads <= kMaxGroups / ((rows + 15) / 16 + 2048 + width) &&
-           (size_t)batch * kv_heads * rows <= kMaxGroups;
+           (size_t)batch * kv_heads * rows <= kMaxGroups &&
+           (size_t)batch * kv_heads <= kMaxGroups / (width * (size_t)QAR_KV8_PAGE);
 }
 
 size_t qar_kv8_attention_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
-                                         uint32_t dim, uint32_t table_width, int with_weights) {
-    if (batch == 0 || queries == 0 || table_width == 0 || (dim != 64 && dim != 128 && dim != 256) ||
+                                         uint32_t dim, uint32_t table_width, qar_dtype dtype, int with_weights) {
+    if (!dtype_ok(dtype) || batch == 0 || queries == 0 || table_width == 0 || (dim != 64 && dim != 128 && dim != 256) ||
         !kv8_rows_ok(batch, queries, heads, kv_heads, table_width))
         return 0;
     return qar::kv8_attention_workspace(batch, kv_heads, queries * (heads / kv_heads), (int)dim, table_width,
-                                        with_weights != 0);
+                                        dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, with_weights != 0);
 }
 
 qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
@@ -1050,7 +1051,8 @@ qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtyp
     if (!aligned(q, 16) || !aligned(out, 16) || (q_lens && !aligned(q_lens, 4)) || (weights && !aligned(weights, 4)))
         return QAR_ERR_MISALIGNED;
     const size_t need = qar::kv8_attention_workspace(cache->batch, cache->kv_heads, queries * (heads / cache->kv_heads),
-                                                     (int)cache->dim, cache->table_width, weights != nullptr);
+                                                     (int)cache->dim, cache->table_width,
+                                                     dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, weights != nullptr);
     if (need && (!workspace || workspace_bytes < need)) return QAR_ERR_INVALID_ARG;
     if (need && !aligned(workspace, 256)) return QAR_ERR_MISALIGNED;
     const size_t bytes = (size_t)cache->batch * queries * heads * cache->dim * dtype_bytes(dtype);

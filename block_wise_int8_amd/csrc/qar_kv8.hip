@@ -961,10 +961,10 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
 // --- the weights that the keys received: with every row's log2 sum known, a
 // wave forms a page's scores again (reading its keys only), and adds up their
 // exponentials over the rows.  Each weight belongs to one wave, which adds in
-// one order: no atomics.  ONE: 16 rows at most, whose queries stay in
-// registers over the wave's pages.
+// one order: no atomics.  16 rows at most: their queries stay in registers
+// over the wave's pages.
 
-template <int DIM, int IN, bool ONE>
+template <int DIM, int IN>
 __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int KC = DIM / 64;
@@ -982,14 +982,13 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
     kv_half8 q[DIM / 32][T];
     float undo = 0.0f, lse = INFINITY;
     int32_t limit = 0;
-    auto load_rows = [&](uint32_t tile) {
-        const uint32_t row = tile * 16 + r;
-        const bool there = seq.counts(row);
-        raw.load(a.q, there ? query_row(a, b, h, row) : 0, g * 16, there);
-        lse = there ? a.lse[(size_t)bh * a.rows + row] : INFINITY;
-        limit = there ? seq.limit(row) : 0;
-    };
-    if (ONE) load_rows(0);
+    if (seq.counts(r)) {
+        raw.load(a.q, query_row(a, b, h, r), g * 16, true);
+        lse = a.lse[(size_t)bh * a.rows + r];
+        limit = seq.limit(r);
+    } else {
+        raw.load(a.q, 0, 0, false);
+    }
     const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16;
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     float* weights = a.weights + (size_t)bh * a.c.width * kPage;
@@ -1008,41 +1007,31 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                 kr[t][c] = *reinterpret_cast<const uint4*>(a.c.k + at * (kPage * DIM) + k_at + t * 4 * DIM + c * 64);
     };
     load_page(first);
-    if (ONE) undo = raw.template convert<16, T>(a.negative, q) * a.scale;
+    undo = raw.template convert<16, T>(a.negative, q) * a.scale;
     for (uint32_t page = first; page < last; ++page) {
         id = next_id, ks = next_ks, old = next_old;
         kv_f32x4 sum[4] = {};
         const int32_t key0 = (int32_t)(page * kPage + g * 16);
-        const uint32_t tiles = ONE ? 1 : (a.rows + 15) / 16;
-        for (uint32_t tile = 0; tile < tiles; ++tile) {
-            if (!ONE) {
-                // a tile whose last query ends before this page adds nothing
-                if (seq.limit(min(tile * 16 + 15, a.rows - 1)) <= (int32_t)(page * kPage)) continue;
-                load_rows(tile);
-                undo = raw.template convert<16, T>(a.negative, q) * a.scale;
-            }
-            kv_f32x4 s[4] = {};
+        kv_f32x4 s[4] = {};
 #pragma unroll
-            for (int c = 0; c < KC; ++c)
+        for (int c = 0; c < KC; ++c)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const kv_half8 lo = half_codes(kr[t][c].x, kr[t][c].y), hi = half_codes(kr[t][c].z, kr[t][c].w);
+                    const kv_half8 k = u ? half_codes(kr[t][c].z, kr[t][c].w) : half_codes(kr[t][c].x, kr[t][c].y);
 #pragma unroll
-                    for (int e = 0; e < T; ++e) {
-                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo, q[2 * c][e], s[t], 0, 0, 0);
-                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi, q[2 * c + 1][e], s[t], 0, 0, 0);
-                    }
+                    for (int e = 0; e < T; ++e)
+                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[2 * c + u][e], s[t], 0, 0, 0);
                 }
-            if (ONE && page + 1 < last) load_page(page + 1);
-            const float factor = ks * undo;
-            const int32_t sees = id < 0 ? 0 : limit - key0;
+        if (page + 1 < last) load_page(page + 1);
+        const float factor = ks * undo;
+        const int32_t sees = id < 0 ? 0 : limit - key0;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sum[t][k] += 4 * t + k < sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k], factor, -lse)) : 0.0f;
-        }
-        if (!ONE && page + 1 < last) load_page(page + 1);
+            for (int k = 0; k < 4; ++k)
+                sum[t][k] = 4 * t + k < sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k], factor, -lse)) : 0.0f;
         // over the 16 lanes of a row; lane r of them adds key 16 g + r
         float mine = 0.0f;
 #pragma unroll
@@ -1059,6 +1048,146 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
         const int32_t key = key0 + (int32_t)r;
         if (key < seq.n && id >= 0) weights[key] = old + mine;
     }
+}
+
+// The same for more rows.  Their queries are converted once, into fragments
+// that a wave of the second kernel reads whole lines of; a wave there has 32
+// keys in registers and runs over a share of the row tiles, whose sums are
+// added in order by the third kernel where there are several shares.
+
+constexpr int kShareThreads = 256, kShareKeys = kShareThreads / 64 * 32;
+
+struct Row {
+    float factor, lse;     // log2 sum: infinite for rows without a query
+    int32_t limit;
+};
+
+struct ShareArgs {
+    AttendArgs a;
+    kv_half8* fragments;   // [sequence and head][tile of 32 rows][dim / 16][term][lane]
+    Row* rows;             // [sequence and head][tiles * 32]
+    float* sums;           // [share][sequence and head][width * kPage], where shares > 1
+    uint32_t row_tiles, shares, key_groups;
+};
+
+template <int DIM, int IN>
+__global__ __launch_bounds__(kShareThreads) void kv8_fragments_kernel(ShareArgs s) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    const AttendArgs& a = s.a;
+    const uint32_t lane = threadIdx.x % 64, r = lane % 32, g = lane / 32;
+    const size_t unit = (size_t)blockIdx.x * (kShareThreads / 64) + threadIdx.x / 64;
+    if (unit >= (size_t)a.c.batch * a.c.heads * s.row_tiles) return;
+    const uint32_t tile = unit % s.row_tiles, bh = unit / s.row_tiles, h = bh % a.c.heads, b = bh / a.c.heads;
+    const Sequence seq(a, b);
+    const uint32_t row = tile * 32 + r;
+    const bool there = seq.counts(row);
+    Query<IN, DIM, 8, 16> raw;
+    raw.load(a.q, there ? query_row(a, b, h, row) : 0, g * 8, there);
+    kv_half8 q[DIM / 16][T];
+    const float undo = raw.template convert<32, T>(a.negative, q) * a.scale;
+#pragma unroll
+    for (int c = 0; c < DIM / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < T; ++e) s.fragments[((unit * (DIM / 16) + c) * T + e) * 64 + lane] = q[c][e];
+    if (g == 0)
+        s.rows[unit * 32 + r] = Row{undo, there ? a.lse[(size_t)bh * a.rows + row] : INFINITY, there ? seq.limit(row) : 0};
+}
+
+template <int DIM, int IN>
+__global__ __launch_bounds__(kShareThreads) void kv8_shares_kernel(ShareArgs s) {
+    constexpr int T = IN == kInBF16 ? 1 : 2, N = DIM / 16;
+    const AttendArgs& a = s.a;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 32, g = lane / 32;
+    const uint32_t share = blockIdx.x % s.shares, rest = blockIdx.x / s.shares;
+    const uint32_t bh = rest / s.key_groups, h = bh % a.c.heads, b = bh / a.c.heads;
+    const uint32_t key0 = rest % s.key_groups * kShareKeys + wave * 32, page = key0 / kPage;
+    if (page >= a.c.width) return;
+    const Sequence seq(a, b);
+    const int32_t id = valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages);
+    const size_t tokens = (size_t)a.c.width * kPage;
+    float* out = (s.shares > 1 ? s.sums + ((size_t)share * a.c.batch * a.c.heads + bh) * tokens : a.weights + bh * tokens) + key0;
+
+    float mine = 0.0f;
+    if ((int32_t)key0 < seq.n && seq.m > 0 && id >= 0) {
+        // row m of the products is the key with bits 2 and 3 exchanged, as above
+        const size_t at = (size_t)id * a.c.heads + h;
+        const float ks = a.c.k_scales[at];
+        const int8_t* codes = a.c.k + at * (kPage * DIM) + (key0 % kPage + exchange_bits_2_3(r)) * DIM + g * 8;
+        kv_half8 k[N];
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const uint2 w = *reinterpret_cast<const uint2*>(codes + c * 16);
+            k[c] = half_codes(w.x, w.y);
+        }
+        // the first tile with a row that sees key0, and this share of the tiles from there on
+        const int32_t before = (int32_t)key0 - (seq.n - seq.m);
+        const uint32_t first_tile = before > 0 ? (uint32_t)((size_t)before * seq.group / 32) : 0;
+        const uint32_t end_tile = min(s.row_tiles, (uint32_t)(((size_t)seq.m * seq.group + 31) / 32));
+        const uint32_t count = end_tile > first_tile ? end_tile - first_tile : 0, per = (count + s.shares - 1) / s.shares;
+        const uint32_t from = first_tile + min(share * per, count), to = first_tile + min((share + 1) * per, count);
+        kv_f32x16 sum = {};
+        kv_half8 q[N][T];
+        Row row;
+        auto load = [&](uint32_t tile) {
+            const size_t unit = (size_t)bh * s.row_tiles + tile;
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+                for (int e = 0; e < T; ++e) q[c][e] = s.fragments[((unit * N + c) * T + e) * 64 + lane];
+            row = s.rows[unit * 32 + r];
+        };
+        if (from < to) load(from);
+        for (uint32_t tile = from; tile < to; ++tile) {
+            // two sums, so that neighbouring products do not wait for each other
+            kv_f32x16 even = {}, odd = {};
+#pragma unroll
+            for (int c = 0; c < N; ++c)
+#pragma unroll
+                for (int e = 0; e < T; ++e) {
+                    if ((c * T + e) % 2)
+                        odd = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[c], q[c][e], odd, 0, 0, 0);
+                    else
+                        even = __builtin_amdgcn_mfma_f32_32x32x16_f16(k[c], q[c][e], even, 0, 0, 0);
+                }
+            const Row now = row;
+            if (tile + 1 < to) load(tile + 1);
+            const float factor = ks * now.factor;
+            const int32_t sees = now.limit - (int32_t)key0 - (int32_t)g * 8;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(even[i] + odd[i], factor, -now.lse));
+                sum[i] += 16 * (i / 8) + i % 8 < sees ? x : 0.0f;
+            }
+        }
+        // over the 32 lanes of a half; lane r < 16 of it keeps register r's key
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float v = sum[i];
+            v += dpp_move<kDppSwapAdjacent>(v);
+            v += dpp_move<kDppSwapPairs>(v);
+            v += dpp_move<kDppRowHalfMirror>(v);
+            v += dpp_move<kDppRowMirror>(v);
+            const Pair p = with_lane_16(v);
+            v = p.a + p.b;
+            if (r == (uint32_t)i) mine = v;
+        }
+    }
+    if (r >= 16) return;
+    const uint32_t key = 16 * (r / 8) + 8 * g + r % 8;
+    if (s.shares > 1)
+        out[key] = mine;
+    else if ((int32_t)(key0 + key) < seq.n)
+        out[key] += mine;
+}
+
+__global__ __launch_bounds__(kShareThreads) void kv8_add_shares_kernel(ShareArgs s) {
+    const AttendArgs& a = s.a;
+    const size_t tokens = (size_t)a.c.width * kPage, all = (size_t)a.c.batch * a.c.heads * tokens;
+    const size_t i = (size_t)blockIdx.x * kShareThreads + threadIdx.x;
+    if (i >= all || (int32_t)(i % tokens) >= clamp_length(a.c.lengths[i / tokens / a.c.heads], a.c.width * kPage)) return;
+    float y = 0.0f;
+    for (uint32_t share = 0; share < s.shares; ++share) y += s.sums[share * all + i];
+    a.weights[i] += y;
 }
 
 // ---------------------------------------------------------------------------
@@ -1361,12 +1490,52 @@ hipError_t launch_kv8_read(const Kv8& c, const int32_t* starts, uint32_t tokens,
     return hipGetLastError();
 }
 
-size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, bool weights) {
+namespace {
+
+// Where a call's scratch lies in its workspace.
+struct Layout {
+    size_t lse, stats, part, fragments, rows, sums, end;
+    uint32_t row_tiles, shares, key_groups;
+};
+
+// Rows whose queries one tile of the few-row weights kernel holds.
+constexpr uint32_t kOneTile = 16;
+
+Layout layout_for(const Plan& p, uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, int terms,
+                  bool weights) {
+    Layout l = {};
+    const size_t heads = (size_t)batch * kv_heads, items = heads * rows;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align256(bytes);
+        return here;
+    };
+    if (weights) l.lse = take(items * 4);
+    if (p.splits > 1) {
+        l.stats = take(items * p.splits * 8);
+        l.part = take(items * p.splits * dim * 4);
+    }
+    if (weights && rows > kOneTile) {
+        l.row_tiles = (rows + 31) / 32;
+        l.key_groups = (width * kPage + kShareKeys - 1) / kShareKeys;
+        // enough workgroups for the chip, at least four row tiles to each
+        const size_t units = heads * l.key_groups, want = (1536 + units - 1) / units, most = (l.row_tiles + 3) / 4;
+        l.shares = (uint32_t)(want < most ? want : most);
+        l.fragments = take(heads * l.row_tiles * 32 * dim * 2 * terms);
+        l.rows = take(heads * l.row_tiles * 32 * sizeof(Row));
+        if (l.shares > 1) l.sums = take(l.shares * heads * width * kPage * 4);
+    }
+    l.end = at;
+    return l;
+}
+
+} // namespace
+
+size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, int kind,
+                               bool weights) {
     const Plan p = plan_for(batch, kv_heads, rows, dim, width);
-    const size_t items = (size_t)batch * kv_heads * rows;
-    size_t bytes = weights ? align256(items * 4) : 0;
-    if (p.splits > 1) bytes += align256(items * p.splits * 8) + align256(items * p.splits * dim * 4);
-    return bytes;
+    return layout_for(p, batch, kv_heads, rows, dim, width, kind == kInBF16 ? 1 : 2, weights).end;
 }
 
 hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads,
@@ -1378,53 +1547,53 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
     a.scale = (scale < 0 ? -scale : scale) * 1.44269504088896340736f;
     a.negative = scale < 0;
     const Plan p = plan_for(c.batch, c.heads, a.rows, c.dim, c.width);
+    const Layout l = layout_for(p, c.batch, c.heads, a.rows, c.dim, c.width, kind == kInBF16 ? 1 : 2, weights != nullptr);
     a.tiles = p.tiles, a.splits = p.splits, a.pages_per_split = p.pages_per_split;
     const size_t items = (size_t)c.batch * c.heads * a.rows;
-    uint8_t* at = (uint8_t*)workspace;
-    if (weights) {
-        a.lse = (float*)at;
-        at += align256(items * 4);
-    }
+    uint8_t* scratch = (uint8_t*)workspace;
+    if (weights) a.lse = (float*)(scratch + l.lse);
     if (a.splits > 1) {
-        a.stats = (float*)at;
-        a.part = (float*)(at + align256(items * a.splits * 8));
+        a.stats = (float*)(scratch + l.stats);
+        a.part = (float*)(scratch + l.part);
     }
-    const uint32_t groups = c.batch * c.heads * a.tiles * a.splits;
+    hipError_t e = hipSuccess;
     with_dim(c.dim, [&](auto D) {
         with_kind(kind, [&](auto K) {
+            auto launched = [&] { return (e = hipGetLastError()) == hipSuccess; };
+            const uint32_t groups = c.batch * c.heads * a.tiles * a.splits;
             if (!p.few)
                 kv8_attend_many_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a);
             else if (a.rows <= 16)
                 kv8_attend_few_kernel<D(), 1, K(), 4><<<groups, kThreads, 0, st>>>(a);
             else if constexpr (few_rows_of(D()) > 16)
                 kv8_attend_few_kernel<D(), 2, K(), 4><<<groups, kThreads, 0, st>>>(a);
+            if (!launched()) return;
+            if (a.splits > 1) {
+                kv8_join_kernel<D(), K()><<<(uint32_t)items, kJoinGroups * D() / 4, 0, st>>>(a);
+                if (!launched()) return;
+            }
+            if (!weights) return;
+            if (a.rows <= kOneTile) {
+                // about eight pages to a wave
+                a.splits = (c.width + 31) / 32;
+                kv8_weights_kernel<D(), K()><<<c.batch * c.heads * a.splits, kThreads, 0, st>>>(a);
+                (void)launched();
+                return;
+            }
+            ShareArgs s = {a, (kv_half8*)(scratch + l.fragments), (Row*)(scratch + l.rows), (float*)(scratch + l.sums),
+                           l.row_tiles, l.shares, l.key_groups};
+            const size_t heads_all = (size_t)c.batch * c.heads;
+            constexpr int waves = kShareThreads / 64;
+            kv8_fragments_kernel<D(), K()>
+                <<<(uint32_t)((heads_all * l.row_tiles + waves - 1) / waves), kShareThreads, 0, st>>>(s);
+            if (!launched()) return;
+            kv8_shares_kernel<D(), K()><<<(uint32_t)(heads_all * l.key_groups * l.shares), kShareThreads, 0, st>>>(s);
+            if (!launched() || l.shares == 1) return;
+            kv8_add_shares_kernel<<<(uint32_t)((heads_all * c.width * kPage + kShareThreads - 1) / kShareThreads),
+                                    kShareThreads, 0, st>>>(s);
+            (void)launched();
         });
     });
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.splits > 1) {
-        with_dim(c.dim, [&](auto D) {
-            with_kind(kind, [&](auto K) {
-                kv8_join_kernel<D(), K()><<<(uint32_t)items, kJoinGroups * D() / 4, 0, st>>>(a);
-            });
-        });
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    if (weights) {
-        // about eight pages to a wave
-        a.splits = (c.width + 31) / 32;
-        with_dim(c.dim, [&](auto D) {
-            with_kind(kind, [&](auto K) {
-                const uint32_t g = c.batch * c.heads * a.splits;
-                if (a.rows <= 16)
-                    kv8_weights_kernel<D(), K(), true><<<g, kThreads, 0, st>>>(a);
-                else
-                    kv8_weights_kernel<D(), K(), false><<<g, kThreads, 0, st>>>(a);
-            });
-        });
-        e = hipGetLastError();
-    }
     return e;
 }
 

@@ -106,7 +106,8 @@ hipError_t launch_kv8_append(const Kv8& c, const int32_t* starts, const void* k_
                              uint32_t tokens, hipStream_t st);
 hipError_t launch_kv8_read(const Kv8& c, const int32_t* starts, uint32_t tokens, void* k_out, void* v_out, int kind,
                            hipStream_t st);
-size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, bool weights);
+size_t kv8_attention_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, int kind,
+                               bool weights);
 hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads,
                                 const int32_t* q_lens, float scale, float* weights, void* out, void* workspace,
                                 hipStream_t st);

@@ -61,7 +61,7 @@ _SIGNATURES = {
     "qar_mx4_linear": [_vp, _int, _sz, _sz, _vp, _vp, _sz, _vp, _int, _vp, _sz, _vp],
     "qar_kv8_append": [_vp, _vp, _vp, _vp, _int, _u32, _vp],
     "qar_kv8_read": [_vp, _vp, _u32, _vp, _vp, _int, _vp],
-    "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int],
+    "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int, _int],
     "qar_kv8_attention": [_vp, _vp, _int, _u32, _u32, _vp, ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
     "qar_kv8_evict": [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp],
     "qar_status_string": [_int],
@@ -843,7 +843,7 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
         _shaped(out, "out", shape, (q.dtype,), dev)
     L = lib()
     ws, size, keep = _workspace(workspace, L.qar_kv8_attention_workspace_bytes(
-        c.batch, queries, heads, c.kv_heads, c.dim, c.table_width, weights is not None), dev)
+        c.batch, queries, heads, c.kv_heads, c.dim, c.table_width, _dtype_code(q.dtype), weights is not None), dev)
     _check(L.qar_kv8_attention(ctypes.byref(c), q.data_ptr(), _dtype_code(q.dtype), queries, heads,
                                None if q_lens is None else q_lens.data_ptr(), c.dim ** -0.5 if scale is None else scale,
                                None if weights is None else weights.data_ptr(), out.data_ptr(), ws, size,

@@ -540,7 +540,7 @@ qar_status qar_kv8_read(const qar_kv8_cache* cache, const int32_t* starts, uint3
  *              whether weights are passed.
  */
 size_t qar_kv8_attention_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
-                                         uint32_t dim, uint32_t table_width, int with_weights);
+                                         uint32_t dim, uint32_t table_width, qar_dtype dtype, int with_weights);
 qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
                              uint32_t heads, const int32_t* q_lens, float scale, float* weights, void* out,
                              void* workspace, size_t workspace_bytes, void* stream);

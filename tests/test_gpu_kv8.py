@@ -230,7 +230,7 @@ def test_attention_repeats_bit_for_bit_on_any_workspace():
     cache = ref.to_cache(c)
     for queries in (1, 50):
         q, _ = ref.data(rng, (2, queries, 8, 128), torch.bfloat16)
-        need = qar.lib().qar_kv8_attention_workspace_bytes(2, queries, 8, 2, 128, 24, 1)
+        need = qar.lib().qar_kv8_attention_workspace_bytes(2, queries, 8, 2, 128, 24, 0, 1)
         assert need > 0
         outs, sums = [], []
         for fill in (0, 255, 127):
@@ -312,7 +312,7 @@ def test_a_step_on_a_stream_and_in_a_graph():
     d = ref.make_cache(rng, 2, 2, 64, [128, 128], 2)
     k, _ = ref.data(rng, (2, 1, 2, 64), torch.bfloat16)
     q, _ = ref.data(rng, (2, 1, 4, 64), torch.bfloat16)
-    need = qar.lib().qar_kv8_attention_workspace_bytes(2, 1, 4, 2, 64, 4, 1)
+    need = qar.lib().qar_kv8_attention_workspace_bytes(2, 1, 4, 2, 64, 4, 0, 1)
     ws = torch.empty(max(256, need), dtype=torch.uint8, device=DEV)
     starts = _ints(199, 130)
 

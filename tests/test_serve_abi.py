@@ -175,7 +175,7 @@ def test_attention_refusals(L):
     assert attend(c, weights=900 * M + 1) == MIS
     assert attend(c, out=600 * M) == INV and attend(c, out=200 * M) == INV and attend(c, q_lens=700 * M) == INV
     size = L.qar_kv8_attention_workspace_bytes
-    need = size(3, 1, 4, 2, 64, 4, 1)
+    need = size(3, 1, 4, 2, 64, 4, 0, 1)
     assert need > 0
     assert attend(c, weights=900 * M) == INV                                             # no workspace
     assert attend(c, weights=900 * M, ws=950 * M, size=need - 1) == INV
@@ -183,7 +183,8 @@ def test_attention_refusals(L):
     assert attend(c, weights=900 * M, ws=900 * M, size=need) == INV                      # over the weights
     assert attend(c, weights=700 * M, ws=950 * M, size=need) == INV                      # over the output
     assert attend(c, weights=M, ws=950 * M, size=need) == INV
-    assert size(0, 1, 4, 2, 64, 4, 1) == size(3, 1, 3, 2, 64, 4, 1) == size(3, 1, 4, 2, 80, 4, 1) == 0
+    assert size(0, 1, 4, 2, 64, 4, 0, 1) == size(3, 1, 3, 2, 64, 4, 0, 1) == size(3, 1, 4, 2, 80, 4, 0, 1) == 0
+    assert size(3, 1, 4, 2, 64, 4, 2, 1) == 0 and size(3, 40, 4, 2, 64, 4, 1, 1) > size(3, 40, 4, 2, 64, 4, 0, 1)
 
 
 def test_evict_refusals(L):
