@@ -1083,7 +1083,7 @@ qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, 
         return QAR_ERR_INVALID_ARG;
     if (!weights || !kept || !moved || keep == 0 || keep > (size_t)into->table_width * QAR_KV8_PAGE)
         return QAR_ERR_INVALID_ARG;
-    if (!aligned(weights, 4) || !aligned(kept, 4) || !aligned(moved, 4)) return QAR_ERR_MISALIGNED;
+    if (!aligned(weights, 16) || !aligned(kept, 4) || !aligned(moved, 4)) return QAR_ERR_MISALIGNED;
     const size_t items = (size_t)cache->batch * cache->kv_heads;
     if (items * 2 > kMaxGroups / (keep / QAR_KV8_PAGE + 1)) return QAR_ERR_INVALID_ARG;
     const Range wi = range(weights, items * cache->table_width * QAR_KV8_PAGE * 4);

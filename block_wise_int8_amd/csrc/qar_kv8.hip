@@ -471,9 +471,24 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
     constexpr int KC = DIM / 64, VC = DIM / 16;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
     const uint32_t split = blockIdx.x % a.splits, bh = blockIdx.x / a.splits, h = bh % a.c.heads, b = bh / a.c.heads;
+    // The wave's first 64 pages are looked up at once, one in each lane, while
+    // the sequence's length is on its way: entries behind it are not used.
+    const uint32_t first = split * a.pages_per_split, limit_page = min(first + a.pages_per_split, a.c.width);
+    int32_t my_id;
+    float my_ks, my_vs;
+    auto look_up = [&](uint32_t page) {
+        my_id = -1, my_ks = my_vs = 0.0f;
+        if (page < limit_page) {
+            my_id = valid_page(a.c.table[(size_t)b * a.c.width + page], a.c.pages);
+            if (my_id >= 0) {
+                my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
+                my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
+            }
+        }
+    };
+    look_up(first + wave + lane * NW);
     const Sequence seq(a, b);
-    const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
-    const uint32_t first = split * a.pages_per_split, last = min(first + a.pages_per_split, pages);
+    const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage, last = min(limit_page, pages);
     if (first >= last && split) return;
 
     Query<IN, DIM, 16, 64> raw[MT];
@@ -496,6 +511,8 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
     for (int i = 0; i < MT; ++i) top[i] = -FLT_MAX, total[i] = 0.0f;
 
     const size_t head_bytes = (size_t)kPage * DIM;
+    // values are read once, keys once more where weights are wanted: these may
+    // stay in the caches (125 against 130 us for 64 sequences of 8,000 tokens)
     const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16, v_at = r * kPage + g * 16;
     uint4 kr[4][KC], vr[VC];
     auto load_k = [&](int32_t id) {
@@ -503,7 +520,7 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) kr[t][c] = load_b128(p + t * 4 * DIM + c * 64);
+            for (int c = 0; c < KC; ++c) kr[t][c] = *reinterpret_cast<const uint4*>(p + t * 4 * DIM + c * 64);
     };
     auto load_v = [&](int32_t id) {
         const int8_t* p = a.c.v + ((size_t)max(id, 0) * a.c.heads + h) * head_bytes + v_at;
@@ -511,18 +528,8 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
         for (int c = 0; c < VC; ++c) vr[c] = load_b128(p + c * 16 * kPage);
     };
 
-    // up to 64 of the wave's pages at a time, one in each lane
     for (uint32_t base = first + wave; base < last; base += 64 * NW) {
-        const uint32_t mine = base + lane * NW;
-        int32_t my_id = -1;
-        float my_ks = 0.0f, my_vs = 0.0f;
-        if (mine < last) {
-            my_id = valid_page(a.c.table[(size_t)b * a.c.width + mine], a.c.pages);
-            if (my_id >= 0) {
-                my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
-                my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
-            }
-        }
+        if (base != first + wave) look_up(base + lane * NW);
         const uint32_t count = min(64u, (last - base + NW - 1) / NW);
         int32_t id = __builtin_amdgcn_readlane(my_id, 0);
         load_k(id);
@@ -964,6 +971,19 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
 // one order: no atomics.  16 rows at most: their queries stay in registers
 // over the wave's pages.
 
+constexpr int kDppRowRotate8 = 0x128;   // lane i <-> i ^ 8 within each 16
+
+// Of 2 N values a lane keeps the upper N if it is `upper`, else the lower, and
+// adds what its partner has of them.
+template <int CTRL, int N>
+__device__ __forceinline__ void halve(float (&v)[16], bool upper) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float keep = upper ? v[i + N] : v[i], give = upper ? v[i] : v[i + N];
+        v[i] = keep + dpp_move<CTRL>(give);
+    }
+}
+
 template <int DIM, int IN>
 __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
@@ -974,9 +994,11 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
     const uint32_t wave = blockIdx.x % a.splits * (kThreads / 64) + threadIdx.x / 64;
     const Sequence seq(a, b);
     const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
-    // a wave has a run of pages
+    // a wave has a run of pages, at most 64, whose numbers and scales its lanes hold
     const uint32_t run = (pages + waves - 1) / waves, first = wave * run, last = min(first + run, pages);
     if (first >= last || seq.m == 0) return;
+    const int32_t my_id = valid_page(a.c.table[(size_t)b * a.c.width + min(first + lane, last - 1)], a.c.pages);
+    const float my_ks = my_id < 0 ? 0.0f : a.c.k_scales[(size_t)my_id * a.c.heads + h];
 
     Query<IN, DIM, 16, 64> raw;
     kv_half8 q[DIM / 32][T];
@@ -990,26 +1012,25 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
         raw.load(a.q, 0, 0, false);
     }
     const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16;
-    const int32_t* table = a.c.table + (size_t)b * a.c.width;
     float* weights = a.weights + (size_t)bh * a.c.width * kPage;
     uint4 kr[4][KC];
-    int32_t id = -1, next_id = -1;
-    float ks = 0.0f, next_ks = 0.0f, old = 0.0f, next_old = 0.0f;
-    auto load_page = [&](uint32_t page) {
-        next_id = valid_page(table[page], a.c.pages);
-        const size_t at = (size_t)max(next_id, 0) * a.c.heads + h;
-        next_ks = a.c.k_scales[at];
+    float next_old = 0.0f;
+    auto load_page = [&](uint32_t page, int32_t page_id) {
+        const int8_t* k = a.c.k + ((size_t)max(page_id, 0) * a.c.heads + h) * (kPage * DIM) + k_at;
         next_old = weights[page * kPage + lane];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int c = 0; c < KC; ++c)
-                kr[t][c] = *reinterpret_cast<const uint4*>(a.c.k + at * (kPage * DIM) + k_at + t * 4 * DIM + c * 64);
+            for (int c = 0; c < KC; ++c) kr[t][c] = *reinterpret_cast<const uint4*>(k + t * 4 * DIM + c * 64);
     };
-    load_page(first);
+    int32_t id = __builtin_amdgcn_readlane(my_id, 0);
+    load_page(first, id);
     undo = raw.template convert<16, T>(a.negative, q) * a.scale;
     for (uint32_t page = first; page < last; ++page) {
-        id = next_id, ks = next_ks, old = next_old;
+        const uint32_t i = page - first;
+        const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i));
+        const float old = next_old;
+        const int32_t next_id = __builtin_amdgcn_readlane(my_id, min(i + 1, last - first - 1));
         kv_f32x4 sum[4] = {};
         const int32_t key0 = (int32_t)(page * kPage + g * 16);
         kv_f32x4 s[4] = {};
@@ -1024,7 +1045,7 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
                     for (int e = 0; e < T; ++e)
                         s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[2 * c + u][e], s[t], 0, 0, 0);
                 }
-        if (page + 1 < last) load_page(page + 1);
+        if (page + 1 < last) load_page(page + 1, next_id);
         const float factor = ks * undo;
         const int32_t sees = id < 0 ? 0 : limit - key0;
 #pragma unroll
@@ -1032,21 +1053,21 @@ __global__ __launch_bounds__(kThreads) void kv8_weights_kernel(AttendArgs a) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 sum[t][k] = 4 * t + k < sees ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k], factor, -lse)) : 0.0f;
-        // over the 16 lanes of a row; lane r of them adds key 16 g + r
-        float mine = 0.0f;
+        // over the 16 lanes of a row: each exchange halves the keys that a lane
+        // still sums, and lane r is left with key 16 g + r
+        float v[16];
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float v = sum[t][k];
-                v += dpp_move<kDppSwapAdjacent>(v);
-                v += dpp_move<kDppSwapPairs>(v);
-                v += dpp_move<kDppRowHalfMirror>(v);
-                v += dpp_move<kDppRowMirror>(v);
-                if (r == (uint32_t)(4 * t + k)) mine = v;
-            }
+            for (int k = 0; k < 4; ++k) v[4 * t + k] = sum[t][k];
+        halve<kDppRowRotate8, 8>(v, r & 8);
+        halve<kDppRowHalfMirror, 4>(v, r & 4);
+        halve<kDppSwapPairs, 2>(v, r & 2);
+        halve<kDppSwapAdjacent, 1>(v, r & 1);
+        const float mine = v[0];
         const int32_t key = key0 + (int32_t)r;
         if (key < seq.n && id >= 0) weights[key] = old + mine;
+        id = next_id;
     }
 }
 
@@ -1194,8 +1215,8 @@ __global__ __launch_bounds__(kShareThreads) void kv8_add_shares_kernel(ShareArgs
 // evict.  First the choice: one workgroup for each sequence and head finds the
 // weight of the last token that stays by three histograms (11, 11 and 10 bits
 // of the weights' order-preserving bit patterns), then writes the kept
-// indexes in order: each wave counts what it keeps of its stretch of tokens,
-// and then places it.  The lower index stays where weights are equal.
+// indexes in order: each thread counts what it keeps of its own tokens, and
+// then places it.  The lower index stays where weights are equal.
 
 constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64, kBins = 2048;
 
@@ -1213,6 +1234,41 @@ __device__ __forceinline__ uint32_t order_of(float w) {
     const uint32_t bits = __builtin_bit_cast(uint32_t, w + 0.0f);
     return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
+
+// A thread has `own` consecutive tokens (a multiple of four).  The order of
+// the first HELD stays in registers; tokens behind them are read again where
+// needed.  0 stands for no token: no weight's order is that low.
+template <int HELD>
+struct Tokens {
+    const float* w;
+    uint32_t first, end;
+    uint32_t held[HELD];
+    __device__ __forceinline__ Tokens(const float* weights, uint32_t all, uint32_t own) : w(weights) {
+        first = min((uint32_t)threadIdx.x * own, all);
+        end = min(first + own, all);
+#pragma unroll
+        for (int j = 0; j < HELD; j += 4) {
+            mine4(first + j, held + j);
+        }
+    }
+    __device__ __forceinline__ void mine4(uint32_t i, uint32_t* o) const {
+        kv_f32x4 x = {};
+        if (i + 4 <= end)
+            x = *reinterpret_cast<const kv_f32x4*>(w + i);
+        else
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i + k < end) x[k] = w[i + k];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = i + k < end ? order_of(x[k]) : 0;
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) f(first + j, held[j]);
+        for (uint32_t i = first + HELD; i < end; ++i) f(i, order_of(w[i]));
+    }
+};
 
 template <int HELD>
 __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a) {
@@ -1234,25 +1290,12 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
         return;
     }
     const uint32_t free = n - recent, need = a.keep - recent;      // `need` of the first `free` tokens stay
+    const Tokens<HELD> tokens(w, free, (free + 4 * kSelectThreads - 1) / (4 * kSelectThreads) * 4);
     for (uint32_t i = tid; i < recent; i += kSelectThreads) {
         kept[need + i] = (int32_t)(free + i);
         moved[need + i] = w[free + i];
     }
     if (need == 0) return;
-
-    // wave v has a stretch of tokens, lane i of it every 64th; the first HELD
-    // of a lane stay in registers, those behind are read again where needed
-    const uint32_t stretch = ((free + kSelectThreads - 1) / kSelectThreads) * 64;
-    const uint32_t from = min(wave * stretch, free), to = min(from + stretch, free);
-    float held[HELD];
-#pragma unroll
-    for (int j = 0; j < HELD; ++j) held[j] = from + j * 64 + lane < to ? w[from + j * 64 + lane] : 0.0f;
-    auto each = [&](auto f) {
-#pragma unroll
-        for (int j = 0; j < HELD; ++j)
-            if (from + j * 64 < to) f(from + j * 64 + lane, held[j]);
-        for (uint32_t base = from + HELD * 64; base < to; base += 64) f(base + lane, base + lane < to ? w[base + lane] : 0.0f);
-    };
 
     uint32_t prefix = 0, mask = 0, left = need;        // the threshold's bits so far, and which they are
     for (int pass = 0; pass < 3; ++pass) {
@@ -1260,9 +1303,8 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
         const uint32_t top = pass == 2 ? 1023 : 2047;
         for (uint32_t i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
         __syncthreads();
-        each([&](uint32_t i, float weight) {
-            const uint32_t o = order_of(weight);
-            if (i < to && (o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
+        tokens.each([&](uint32_t, uint32_t o) {
+            if (o != 0 && (o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
         });
         __syncthreads();
         // tokens in this thread's two bins and in all above them
@@ -1275,7 +1317,8 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
         if (lane == 0) wave_sum[wave] = suffix;
         __syncthreads();
         uint32_t above = suffix - hi - lo;
-        for (uint32_t v = wave + 1; v < kSelectWaves; ++v) above += wave_sum[v];
+#pragma unroll
+        for (uint32_t v = 1; v < kSelectWaves; ++v) above += v > wave ? wave_sum[v] : 0;
         if (above < left && above + hi >= left) {
             found_bin = 2 * tid + 1;
             found_above = above;
@@ -1291,31 +1334,34 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
 
     // all above the threshold stay, and the first `left` equal to it
     uint32_t more = 0, equal = 0;
-    each([&](uint32_t i, float weight) {
-        const uint32_t o = order_of(weight);
-        more += i < to && o > prefix;
-        equal += i < to && o == prefix;
+    tokens.each([&](uint32_t, uint32_t o) {
+        more += o > prefix;
+        equal += o == prefix;
     });
-    for (int d = 32; d; d /= 2) {
-        more += __shfl_xor(more, d);
-        equal += __shfl_xor(equal, d);
+    // what the threads before this one have
+    uint32_t more_before = more, equal_before = equal;
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t m = __shfl_up(more_before, d), e = __shfl_up(equal_before, d);
+        if (lane >= (uint32_t)d) more_before += m, equal_before += e;
     }
-    if (lane == 0) wave_more[wave] = more, wave_equal[wave] = equal;
+    if (lane == 63) wave_more[wave] = more_before, wave_equal[wave] = equal_before;
     __syncthreads();
-    uint32_t more_before = 0, equal_before = 0;
-    for (uint32_t v = 0; v < wave; ++v) more_before += wave_more[v], equal_before += wave_equal[v];
-    const uint64_t below = ((uint64_t)1 << lane) - 1;
-    each([&](uint32_t i, float weight) {
-        const uint32_t o = order_of(weight);
-        const uint64_t m = __ballot(i < to && o > prefix), e = __ballot(i < to && o == prefix);
-        const uint32_t my_more = more_before + __popcll(m & below), my_equal = equal_before + __popcll(e & below);
-        if ((m >> lane & 1) || ((e >> lane & 1) && my_equal < left)) {
-            const uint32_t at = my_more + min(my_equal, left);
+    more_before -= more;
+    equal_before -= equal;
+#pragma unroll
+    for (uint32_t v = 0; v + 1 < kSelectWaves; ++v) {
+        more_before += v < wave ? wave_more[v] : 0;
+        equal_before += v < wave ? wave_equal[v] : 0;
+    }
+    tokens.each([&](uint32_t i, uint32_t o) {
+        const bool is_more = o > prefix, is_equal = o == prefix;
+        if (is_more || (is_equal && equal_before < left)) {
+            const uint32_t at = more_before + min(equal_before, left);
             kept[at] = (int32_t)i;
-            moved[at] = weight;
+            moved[at] = w[i];
         }
-        more_before += __popcll(m);
-        equal_before += __popcll(e);
+        more_before += is_more;
+        equal_before += is_equal;
     });
 }
 
@@ -1600,7 +1646,7 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st) {
     EvictArgs a = {c, into, weights, recent, keep, kept, moved};
-    // the table's width bounds the tokens: weights in registers up to 24,576
+    // the table's width bounds the tokens: their order stays in registers up to 24,576
     if (c.width * kPage <= kSelectThreads * 8)
         kv8_select_kernel<8><<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
     else

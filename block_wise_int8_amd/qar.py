@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -638,6 +639,16 @@ def qar_dequantize_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, ro
 # serving: microscaled 4-bit floating point
 
 
+# These calls are short enough for their checks to count: each asks first
+# whether everything fits (`_fits`), and only if not finds out what does not
+# and says so.
+
+
+def _fits(t, shape, dtype, index):
+    """A contiguous tensor of this shape and type on GPU `index` (which is at least 0)."""
+    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
 def _workspace(given, need, device):
     """(pointer, bytes) of the caller's workspace, or of a new one (torch's
     allocator reuses its memory only behind the work already on this stream)."""
@@ -670,11 +681,11 @@ def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales:
     rows, cols = _matrix(x, "x").shape
     dev, nb = x.device, _mx4_blocks(cols)
     if codes is None:
-        codes = torch.empty((rows, nb * 16), dtype=torch.uint8, device=dev)
+        codes = x.new_empty((rows, nb * 16), dtype=torch.uint8)
     else:
         _expect(codes, "codes", rows * nb * 16, (torch.uint8,), dev)
     if scales is None:
-        scales = torch.empty((rows, nb), dtype=torch.uint8, device=dev)
+        scales = x.new_empty((rows, nb), dtype=torch.uint8)
     else:
         _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
     _check(lib().qar_mx4_quantize(x.data_ptr(), _dtype_code(x.dtype), rows, cols, codes.data_ptr(), scales.data_ptr(),
@@ -685,12 +696,14 @@ def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales:
 def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """codes uint8[rows, nb * 16], scales uint8[rows, nb] -> out [rows, cols] (bf16 or fp32)."""
-    rows = _matrix(codes, "codes").shape[0]
-    dev, nb = codes.device, _mx4_blocks(cols)
-    _expect(codes, "codes", rows * nb * 16, (torch.uint8,), dev)
-    _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
+    rows, nb, index = codes.shape[0], _mx4_blocks(cols), codes.get_device()
+    if index < 0 or not (_fits(codes, (rows, nb * 16), torch.uint8, index) and
+                         _fits(scales, (rows, nb), torch.uint8, index)):
+        _expect(_matrix(codes, "codes"), "codes", rows * nb * 16, (torch.uint8,), codes.device)
+        _expect(scales, "scales", rows * nb, (torch.uint8,), codes.device)
+    dev = codes.device
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        out = codes.new_empty((rows, cols), dtype=out_dtype)
     else:
         _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
     _check(lib().qar_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
@@ -707,12 +720,14 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
     lib().qar_mx4_linear_workspace_bytes(rows, inner, cols) bytes) is allocated
     with torch when not given."""
     rows, inner = _matrix(x, "x").shape
-    cols = _matrix(codes, "codes").shape[0]
-    dev, nb = x.device, _mx4_blocks(inner)
-    _expect(codes, "codes", cols * nb * 16, (torch.uint8,), dev)
-    _expect(scales, "scales", cols * nb, (torch.uint8,), dev)
+    cols, nb, index = codes.shape[0], _mx4_blocks(inner), x.get_device()
+    dev = x.device
+    if index < 0 or not (_fits(codes, (cols, nb * 16), torch.uint8, index) and
+                         _fits(scales, (cols, nb), torch.uint8, index)):
+        _expect(_matrix(codes, "codes"), "codes", cols * nb * 16, (torch.uint8,), dev)
+        _expect(scales, "scales", cols * nb, (torch.uint8,), dev)
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype or x.dtype, device=dev)
+        out = x.new_empty((rows, cols), dtype=out_dtype or x.dtype)
     else:
         _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
     L = lib()
@@ -726,9 +741,9 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
 # serving: the 8-bit paged cache
 
 
-class _KvStruct(ctypes.Structure):
-    _fields_ = [("k", _vp), ("k_scales", _vp), ("v", _vp), ("v_scales", _vp), ("page_table", _vp), ("lengths", _vp),
-                ("pages", _u32), ("kv_heads", _u32), ("dim", _u32), ("batch", _u32), ("table_width", _u32)]
+# qar_kv8_cache of include/qar.h as bytes: six pointers, five 32-bit numbers and
+# the padding behind them
+_KV_PACK = struct.Struct("=6Q5I4x").pack
 
 
 class KvCache:
@@ -753,22 +768,29 @@ class KvCache:
                    torch.zeros(batch, dtype=torch.int32, device=device))
 
     def _struct(self, what="cache"):
-        k, table, dev = self.k, self.page_table, self.k.device
+        """(the C struct as bytes, GPU index, batch, kv_heads, dim, table_width)"""
+        k, v, ks, vs, table, lengths = self.k, self.v, self.k_scales, self.v_scales, self.page_table, self.lengths
+        index = k.get_device()
         if k.dim() != 4 or k.shape[2] != QAR_KV8_PAGE or table.dim() != 2:
             raise ValueError(f"{what}.k must be [pages, kv_heads, {QAR_KV8_PAGE}, dim] and {what}.page_table [batch, width]")
-        pages, heads, _, dim = k.shape
+        pages, heads, page, dim = k.shape
         batch, width = table.shape
-        if tuple(self.v.shape) != (pages, heads, dim, QAR_KV8_PAGE):
-            raise ValueError(f"{what}.v must be {(pages, heads, dim, QAR_KV8_PAGE)}, not {tuple(self.v.shape)}")
-        for name, t, numel, dt in (("k", k, k.numel(), torch.int8), ("v", self.v, k.numel(), torch.int8),
-                                   ("k_scales", self.k_scales, pages * heads, torch.float32),
-                                   ("v_scales", self.v_scales, pages * heads, torch.float32),
-                                   ("page_table", table, batch * width, torch.int32),
-                                   ("lengths", self.lengths, batch, torch.int32)):
-            if t.dtype is not dt or not t.is_cuda or not t.is_contiguous() or t.numel() != numel or t.device != dev:
-                _expect(t, f"{what}.{name}", numel, (dt,), dev)
-        return _KvStruct(k.data_ptr(), self.k_scales.data_ptr(), self.v.data_ptr(), self.v_scales.data_ptr(),
-                         table.data_ptr(), self.lengths.data_ptr(), pages, heads, dim, batch, width)
+        flat = (pages, heads)
+        if index < 0 or not (k.dtype is torch.int8 and k.is_contiguous() and
+                             _fits(v, (pages, heads, dim, page), torch.int8, index) and
+                             _fits(ks, flat, torch.float32, index) and _fits(vs, flat, torch.float32, index) and
+                             table.dtype is torch.int32 and table.is_contiguous() and table.get_device() == index and
+                             _fits(lengths, (batch,), torch.int32, index)):
+            dev = k.device
+            if tuple(v.shape) != (pages, heads, dim, QAR_KV8_PAGE):
+                raise ValueError(f"{what}.v must be {(pages, heads, dim, QAR_KV8_PAGE)}, not {tuple(v.shape)}")
+            for name, numel, dt in (("k", k.numel(), torch.int8), ("v", k.numel(), torch.int8),
+                                    ("k_scales", pages * heads, torch.float32),
+                                    ("v_scales", pages * heads, torch.float32), ("page_table", batch * width, torch.int32),
+                                    ("lengths", batch, torch.int32)):
+                _expect(getattr(self, name), f"{what}.{name}", numel, (dt,), dev)
+        return _KV_PACK(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), table.data_ptr(), lengths.data_ptr(),
+                        pages, heads, dim, batch, width), index, batch, heads, dim, width
 
 
 def _shaped(t, what, shape, dtypes, device):
@@ -787,14 +809,17 @@ _INT32, _F32 = (torch.int32,), (torch.float32,)
 def qar_kv8_append(cache: KvCache, starts: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
     """k_new, v_new [batch, tokens, kv_heads, dim] (bf16/fp32) enter the cache at
     positions starts[b] (int32[batch]) of every sequence.  ``cache.lengths`` stays as it is."""
-    c = cache._struct()
-    dev, tokens = cache.k.device, k_new.shape[1] if k_new.dim() == 4 else -1
-    shape = (c.batch, tokens, c.kv_heads, c.dim)
-    _shaped(k_new, "k_new", shape, _DATA_DTYPES, dev)
-    _shaped(v_new, "v_new", shape, (k_new.dtype,), dev)
-    _shaped(starts, "starts", (c.batch,), _INT32, dev)
-    _check(lib().qar_kv8_append(ctypes.byref(c), starts.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                                _dtype_code(k_new.dtype), tokens, _stream(stream)), "qar_kv8_append")
+    c, index, batch, heads, dim, _ = cache._struct()
+    tokens = k_new.shape[1] if k_new.dim() == 4 else -1
+    shape, dtype = (batch, tokens, heads, dim), k_new.dtype
+    if index < 0 or not (dtype in _DATA_DTYPES and _fits(k_new, shape, dtype, index) and
+                         _fits(v_new, shape, dtype, index) and _fits(starts, (batch,), torch.int32, index)):
+        dev = cache.k.device
+        _shaped(k_new, "k_new", shape, _DATA_DTYPES, dev)
+        _shaped(v_new, "v_new", shape, (dtype,), dev)
+        _shaped(starts, "starts", (batch,), _INT32, dev)
+    _check(lib().qar_kv8_append(c, starts.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype_code(dtype), tokens,
+                                _stream(stream)), "qar_kv8_append")
 
 
 def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: torch.dtype = torch.bfloat16,
@@ -802,18 +827,18 @@ def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: t
     """Tokens starts[b] .. starts[b] + tokens - 1 of every sequence as values
     (k, v), each [batch, tokens, kv_heads, dim]; zeros behind its length.
     ``out`` = (k, v) receives them instead of new tensors."""
-    c = cache._struct()
-    dev = cache.k.device
-    shape = (c.batch, tokens, c.kv_heads, c.dim)
-    _shaped(starts, "starts", (c.batch,), _INT32, dev)
+    c, index, batch, heads, dim, _ = cache._struct()
+    shape = (batch, tokens, heads, dim)
+    if index < 0 or not _fits(starts, (batch,), torch.int32, index):
+        _shaped(starts, "starts", (batch,), _INT32, cache.k.device)
     if out is None:
-        k, v = torch.empty(shape, dtype=out_dtype, device=dev), torch.empty(shape, dtype=out_dtype, device=dev)
+        k, v = cache.k.new_empty(shape, dtype=out_dtype), cache.k.new_empty(shape, dtype=out_dtype)
     else:
         k, v = out
-        _shaped(k, "out[0]", shape, _DATA_DTYPES, dev)
-        _shaped(v, "out[1]", shape, (k.dtype,), dev)
-    _check(lib().qar_kv8_read(ctypes.byref(c), starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(),
-                              _dtype_code(k.dtype), _stream(stream)), "qar_kv8_read")
+        _shaped(k, "out[0]", shape, _DATA_DTYPES, cache.k.device)
+        _shaped(v, "out[1]", shape, (k.dtype,), cache.k.device)
+    _check(lib().qar_kv8_read(c, starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype),
+                              _stream(stream)), "qar_kv8_read")
     return k, v
 
 
@@ -826,28 +851,32 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
     when given, has the weight that each token received added.  ``workspace`` (at
     least lib().qar_kv8_attention_workspace_bytes(...) bytes) is allocated with
     torch when not given."""
-    c = cache._struct()
-    dev = cache.k.device
+    c, index, batch, kv_heads, dim, width = cache._struct()
     if q.dim() != 4:
         raise ValueError(f"q must be [batch, queries, heads, dim], not {list(q.shape)}")
     _, queries, heads, _ = q.shape
-    shape = (c.batch, queries, heads, c.dim)
-    _shaped(q, "q", shape, _DATA_DTYPES, dev)
-    if q_lens is not None:
-        _shaped(q_lens, "q_lens", (c.batch,), _INT32, dev)
-    if weights is not None:
-        _shaped(weights, "weights", (c.batch, c.kv_heads, c.table_width * QAR_KV8_PAGE), _F32, dev)
+    shape, dtype = (batch, queries, heads, dim), q.dtype
+    summed = (batch, kv_heads, width * QAR_KV8_PAGE)
+    if index < 0 or not (dtype in _DATA_DTYPES and _fits(q, shape, dtype, index) and
+                         (q_lens is None or _fits(q_lens, (batch,), torch.int32, index)) and
+                         (weights is None or _fits(weights, summed, torch.float32, index)) and
+                         (out is None or _fits(out, shape, dtype, index))):
+        dev = cache.k.device
+        _shaped(q, "q", shape, _DATA_DTYPES, dev)
+        if q_lens is not None:
+            _shaped(q_lens, "q_lens", (batch,), _INT32, dev)
+        if weights is not None:
+            _shaped(weights, "weights", summed, _F32, dev)
+        if out is not None:
+            _shaped(out, "out", shape, (dtype,), dev)
     if out is None:
         out = torch.empty_like(q)
-    else:
-        _shaped(out, "out", shape, (q.dtype,), dev)
-    L = lib()
+    L, code = lib(), _dtype_code(dtype)
     ws, size, keep = _workspace(workspace, L.qar_kv8_attention_workspace_bytes(
-        c.batch, queries, heads, c.kv_heads, c.dim, c.table_width, _dtype_code(q.dtype), weights is not None), dev)
-    _check(L.qar_kv8_attention(ctypes.byref(c), q.data_ptr(), _dtype_code(q.dtype), queries, heads,
-                               None if q_lens is None else q_lens.data_ptr(), c.dim ** -0.5 if scale is None else scale,
-                               None if weights is None else weights.data_ptr(), out.data_ptr(), ws, size,
-                               _stream(stream)), "qar_kv8_attention")
+        batch, queries, heads, kv_heads, dim, width, code, weights is not None), q.device)
+    _check(L.qar_kv8_attention(c, q.data_ptr(), code, queries, heads, None if q_lens is None else q_lens.data_ptr(),
+                               dim ** -0.5 if scale is None else scale, None if weights is None else weights.data_ptr(),
+                               out.data_ptr(), ws, size, _stream(stream)), "qar_kv8_attention")
     return out
 
 
@@ -856,22 +885,26 @@ def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: 
     """``into`` receives, of every sequence and head, the last min(recent, keep)
     tokens of ``cache`` and the heaviest others, ``keep`` in all, and its lengths
     -> (kept positions int32[batch, kv_heads, keep], -1 behind them; their weights, 0 behind them)."""
-    c, d = cache._struct(), into._struct("into")
-    dev = cache.k.device
-    if into.k.device != dev:
-        raise ValueError(f"into is on {into.k.device}, cache on {dev}")
+    c, index, batch, heads, _, width = cache._struct()
+    d, other = into._struct("into")[:2]
+    if other != index:
+        raise ValueError(f"into is on {into.k.device}, cache on {cache.k.device}")
     if not 0 <= recent < 1 << 32 or not 1 <= keep < 1 << 31:
         raise ValueError(f"recent must be at least 0 and keep at least 1, not {recent} and {keep}")
-    _shaped(weights, "weights", (c.batch, c.kv_heads, c.table_width * QAR_KV8_PAGE), _F32, dev)
-    shape = (c.batch, c.kv_heads, keep)
+    summed, shape = (batch, heads, width * QAR_KV8_PAGE), (batch, heads, keep)
+    if index < 0 or not (_fits(weights, summed, torch.float32, index) and
+                         (kept is None or _fits(kept, shape, torch.int32, index)) and
+                         (moved is None or _fits(moved, shape, torch.float32, index))):
+        dev = cache.k.device
+        _shaped(weights, "weights", summed, _F32, dev)
+        if kept is not None:
+            _shaped(kept, "kept", shape, _INT32, dev)
+        if moved is not None:
+            _shaped(moved, "moved", shape, _F32, dev)
     if kept is None:
-        kept = torch.empty(shape, dtype=torch.int32, device=dev)
-    else:
-        _shaped(kept, "kept", shape, _INT32, dev)
+        kept = weights.new_empty(shape, dtype=torch.int32)
     if moved is None:
-        moved = torch.empty(shape, dtype=torch.float32, device=dev)
-    else:
-        _shaped(moved, "moved", shape, _F32, dev)
-    _check(lib().qar_kv8_evict(ctypes.byref(c), ctypes.byref(d), weights.data_ptr(), recent, keep, kept.data_ptr(),
-                               moved.data_ptr(), _stream(stream)), "qar_kv8_evict")
+        moved = weights.new_empty(shape)
+    _check(lib().qar_kv8_evict(c, d, weights.data_ptr(), recent, keep, kept.data_ptr(), moved.data_ptr(),
+                               _stream(stream)), "qar_kv8_evict")
     return kept, moved

@@ -555,7 +555,8 @@ qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtyp
  *   cache, into  equal batch, kv_heads and dim.  Their pages must be disjoint
  *                (one pool may hold both); tables and lengths are their own;
  *                into->table_width * QAR_KV8_PAGE >= keep.
- *   weights  [in]  float[batch][kv_heads][table_width * QAR_KV8_PAGE] (cache's).
+ *   weights  [in]  float[batch][kv_heads][table_width * QAR_KV8_PAGE] (cache's),
+ *                  16-byte aligned.
  *   kept     [out] int32[batch][kv_heads][keep]: the kept positions, ascending; -1 behind them.
  *   moved    [out] float[batch][kv_heads][keep]: their weights; 0 behind them.
  */

@@ -94,10 +94,21 @@ def test_mx4_linear_workspace(L):
 # the cache
 
 
+class _Kv(ctypes.Structure):
+    """qar_kv8_cache"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "k_scales", "v", "v_scales", "page_table", "lengths")] + \
+        [(n, ctypes.c_uint32) for n in ("pages", "kv_heads", "dim", "batch", "table_width")]
+
+
+def test_the_binding_packs_the_struct():
+    c = _Kv(*[i << 40 for i in range(1, 7)], 7, 8, 9, 10, 11)
+    assert bytes(c) == qar._KV_PACK(*[i << 40 for i in range(1, 7)], 7, 8, 9, 10, 11)
+
+
 def _struct(**kw):
     good = dict(k=M, k_scales=100 * M, v=200 * M, v_scales=300 * M, page_table=400 * M, lengths=500 * M, pages=10,
                 kv_heads=2, dim=64, batch=3, table_width=4)
-    return qar._KvStruct(*{**good, **kw}.values())
+    return _Kv(*{**good, **kw}.values())
 
 
 BAD_CACHES = [(dict(dim=96), UNS), (dict(dim=0), UNS), (dict(k=None), INV), (dict(k_scales=None), INV), (dict(v=None), INV),
