@@ -971,8 +971,6 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
 // one order: no atomics.  16 rows at most: their queries stay in registers
 // over the wave's pages.
 
-constexpr int kDppRowRotate8 = 0x128;   // lane i <-> i ^ 8 within each 16
-
 // Of 2 N values a lane keeps the upper N if it is `upper`, else the lower, and
 // adds what its partner has of them.
 template <int CTRL, int N>

@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(QuantizeArgs a) 
     for (int u = 0; u < U; ++u) {
         const size_t i = first + (size_t)u * kThreads;
         const uint32_t byte = scale_byte(quad_max(peak_of<IN>(abs_max<IN>(v[u], 0))));
-        if (i >= total) continue;
+        if (i >= total) continue;                 // whole blocks, and whole chunks where they matter
         const uint32_t c = codes8<IN>(v[u], scale_value(byte));
         const bool leads = threadIdx.x % 4 == 0;
         if constexpr (PLACE == kRows) {
@@ -221,7 +221,16 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(QuantizeArgs a) 
                                   ? (((row[u] / 16) * (a.padded / 8) + block / 8) * 2 + block % 2) * 64 + block % 8 / 2 * 16 + row[u] % 16
                                   : row[u] * a.padded + block;
             *reinterpret_cast<uint32_t*>(a.codes + at * 16 + quarter * 4) = c;
-            if (leads) a.scales[PLACE == kFragments ? at : tile_scale_at(row[u], block, a.padded)] = (uint8_t)byte;
+            if constexpr (PLACE == kFragments) {
+                if (leads) a.scales[at] = (uint8_t)byte;
+            } else {
+                // 32 lanes have a row's chunk of eight blocks: every other block's byte makes a word
+                uint32_t word = byte << (block % 8 / 2 * 8);
+                word |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)word, kDppRowRotate8, 0xF, 0xF, false);
+                word |= (uint32_t)__shfl_xor((int)word, 16);
+                if (leads && block % 8 < 2)
+                    *reinterpret_cast<uint32_t*>(a.scales + tile_scale_at(row[u], block, a.padded)) = word;
+            }
         }
     }
 }
@@ -693,10 +702,12 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     // (straight from the registers a store touches 32 rows with 32 bytes each).
     // 16-byte slot c of row r lies at c ^ (r % 8) of its group of eight.
     using T = std::conditional_t<OUT == kOutBF16, uint16_t, float>;
-    // Half a buffer to a wave: every buffer is read out, and none is being written.
-    constexpr int ROW = WN * sizeof(T), HALF = BM * 64, NOW = std::min(HALF / (32 * ROW), TM);
+    // A buffer to a wave, or half of one: all are read out, and none is being written.
+    constexpr int ROW = WN * sizeof(T), SHARE = NT / 64 > 4 ? 2 : 1, STRIP = BM * 128 / SHARE;
+    constexpr int NOW = std::min(STRIP / (32 * ROW), TM);
     static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
-    char* strip = reinterpret_cast<char*>(wave < 2 ? s0 : wave < 4 ? s1 : wave < 6 ? s2 : s3) + wave % 2 * HALF;
+    const uint32_t home = wave / SHARE;
+    char* strip = reinterpret_cast<char*>(home == 0 ? s0 : home == 1 ? s1 : home == 2 ? s2 : s3) + wave % SHARE * STRIP;
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += NOW) {
 #pragma unroll
@@ -777,6 +788,9 @@ void tiled(LinearArgs& a, hipStream_t st) {
         <<<a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
 }
 
+// The few-row kernel, which reads x again for every 16 or 32 columns, against
+// tiles of 64: for 40 rows of 5376 x 5376 13.1 against 16.6 us, for 64 rows of
+// 1152 x 1152 6.9 against 7.7, of 3840 x 15360 19.4 against 16.0 to 19.0.
 constexpr size_t kFewRows = 64;
 
 // One tile of rows of whole blocks is quantized inside the product.
@@ -868,19 +882,24 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     a.w_tiles = q.w_tiles;
     const hipError_t e = quantize_call<kTiles>(q, kind, st);
     if (e != hipSuccess) return e;
-    // the large tile where it gives every CU at least one
-    const size_t large = (size_t)groups_for(rows, 256) * groups_for(cols, 256);
-    if (large >= 256) {
-        if (out_kind == kOutBF16)
-            tiled<kOutBF16, 256, 256, 128, 64>(a, st);
+    // The largest tile that gives every CU one.  Tiles of 64 against 128: 500
+    // rows of 3840 x 3840 15.2 against 17.5 us, 1000 of 2880 x 9000 37.1 against
+    // 33.5; 128 against 256: 2000 rows of 5376 x 5376 48.9 against 51.4, 8192 of
+    // 5376 x 21504 1.3 times the time.
+    const auto tiles = [&](size_t size) { return (size_t)groups_for(rows, size) * groups_for(cols, size); };
+    const auto go = [&](auto OUT) {
+        constexpr int out = decltype(OUT)::value;
+        if (tiles(256) >= 256)
+            tiled<out, 256, 256, 128, 64>(a, st);
+        else if (tiles(128) >= 256)
+            tiled<out, 128, 128, 64, 64>(a, st);
         else
-            tiled<kOutF32, 256, 256, 128, 64>(a, st);
-    } else {
-        if (out_kind == kOutBF16)
-            tiled<kOutBF16, 128, 128, 64, 64>(a, st);
-        else
-            tiled<kOutF32, 128, 128, 64, 64>(a, st);
-    }
+            tiled<out, 64, 64, 32, 64>(a, st);
+    };
+    if (out_kind == kOutBF16)
+        go(std::integral_constant<int, kOutBF16>{});
+    else
+        go(std::integral_constant<int, kOutF32>{});
     return hipGetLastError();
 }
 

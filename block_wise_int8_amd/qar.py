@@ -644,13 +644,30 @@ def qar_dequantize_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, ro
 # and says so.
 
 
+def _as_current(stream):
+    """A context in which ``stream`` (a Stream or a handle) is the current one.  A call on a stream
+    other than the current one is made inside it, so that what it allocates (outputs, workspaces)
+    belongs to that stream and is not handed out again while the call runs."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _current(index):
+    """The current stream's handle, for tensors on GPU ``index``."""
+    device = torch.cuda.current_device()
+    if index != device:
+        raise ValueError(f"the tensors are on GPU {index}, the current device is {device}")
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _fits(t, shape, dtype, index):
     """A contiguous tensor of this shape and type on GPU `index` (which is at least 0)."""
     return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _workspace(given, need, device):
-    """(pointer, bytes) of the caller's workspace, or of a new one (torch's
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one (torch's
     allocator reuses its memory only behind the work already on this stream)."""
     if given is None:
         if not need:
@@ -678,6 +695,9 @@ def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales:
                      stream=None):
     """x [rows, cols] (bf16/fp32) -> (E2M1 codes, two per byte, uint8[rows, nb * 16];
     power-of-two scales uint8[rows, nb]) with nb = ceil(cols / 32)."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_mx4_quantize(x, codes, scales)
     rows, cols = _matrix(x, "x").shape
     dev, nb = x.device, _mx4_blocks(cols)
     if codes is None:
@@ -689,13 +709,16 @@ def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales:
     else:
         _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
     _check(lib().qar_mx4_quantize(x.data_ptr(), _dtype_code(x.dtype), rows, cols, codes.data_ptr(), scales.data_ptr(),
-                                  _stream(stream)), "qar_mx4_quantize")
+                                  _current(x.get_device())), "qar_mx4_quantize")
     return codes, scales
 
 
 def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out: torch.Tensor | None = None,
                        out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """codes uint8[rows, nb * 16], scales uint8[rows, nb] -> out [rows, cols] (bf16 or fp32)."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_mx4_dequantize(codes, scales, cols, out, out_dtype)
     rows, nb, index = codes.shape[0], _mx4_blocks(cols), codes.get_device()
     if index < 0 or not (_fits(codes, (rows, nb * 16), torch.uint8, index) and
                          _fits(scales, (rows, nb), torch.uint8, index)):
@@ -707,7 +730,7 @@ def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out
     else:
         _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
     _check(lib().qar_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                    _dtype_code(out.dtype), _stream(stream)), "qar_mx4_dequantize")
+                                    _dtype_code(out.dtype), _current(index)), "qar_mx4_dequantize")
     return out
 
 
@@ -719,6 +742,9 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
     (x's type unless out or out_dtype says otherwise).  ``workspace`` (at least
     lib().qar_mx4_linear_workspace_bytes(rows, inner, cols) bytes) is allocated
     with torch when not given."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_mx4_linear(x, codes, scales, out, out_dtype, workspace)
     rows, inner = _matrix(x, "x").shape
     cols, nb, index = codes.shape[0], _mx4_blocks(inner), x.get_device()
     dev = x.device
@@ -733,7 +759,7 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
     L = lib()
     ws, size, keep = _workspace(workspace, L.qar_mx4_linear_workspace_bytes(rows, inner, cols), dev)
     _check(L.qar_mx4_linear(x.data_ptr(), _dtype_code(x.dtype), rows, inner, codes.data_ptr(), scales.data_ptr(), cols,
-                            out.data_ptr(), _dtype_code(out.dtype), ws, size, _stream(stream)), "qar_mx4_linear")
+                            out.data_ptr(), _dtype_code(out.dtype), ws, size, _current(index)), "qar_mx4_linear")
     return out
 
 
@@ -809,6 +835,9 @@ _INT32, _F32 = (torch.int32,), (torch.float32,)
 def qar_kv8_append(cache: KvCache, starts: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
     """k_new, v_new [batch, tokens, kv_heads, dim] (bf16/fp32) enter the cache at
     positions starts[b] (int32[batch]) of every sequence.  ``cache.lengths`` stays as it is."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_append(cache, starts, k_new, v_new)
     c, index, batch, heads, dim, _ = cache._struct()
     tokens = k_new.shape[1] if k_new.dim() == 4 else -1
     shape, dtype = (batch, tokens, heads, dim), k_new.dtype
@@ -819,7 +848,7 @@ def qar_kv8_append(cache: KvCache, starts: torch.Tensor, k_new: torch.Tensor, v_
         _shaped(v_new, "v_new", shape, (dtype,), dev)
         _shaped(starts, "starts", (batch,), _INT32, dev)
     _check(lib().qar_kv8_append(c, starts.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype_code(dtype), tokens,
-                                _stream(stream)), "qar_kv8_append")
+                                _current(index)), "qar_kv8_append")
 
 
 def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: torch.dtype = torch.bfloat16,
@@ -827,6 +856,9 @@ def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: t
     """Tokens starts[b] .. starts[b] + tokens - 1 of every sequence as values
     (k, v), each [batch, tokens, kv_heads, dim]; zeros behind its length.
     ``out`` = (k, v) receives them instead of new tensors."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_read(cache, starts, tokens, out_dtype, out)
     c, index, batch, heads, dim, _ = cache._struct()
     shape = (batch, tokens, heads, dim)
     if index < 0 or not _fits(starts, (batch,), torch.int32, index):
@@ -838,7 +870,7 @@ def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: t
         _shaped(k, "out[0]", shape, _DATA_DTYPES, cache.k.device)
         _shaped(v, "out[1]", shape, (k.dtype,), cache.k.device)
     _check(lib().qar_kv8_read(c, starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype),
-                              _stream(stream)), "qar_kv8_read")
+                              _current(index)), "qar_kv8_read")
     return k, v
 
 
@@ -851,6 +883,9 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
     when given, has the weight that each token received added.  ``workspace`` (at
     least lib().qar_kv8_attention_workspace_bytes(...) bytes) is allocated with
     torch when not given."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_attention(cache, q, q_lens, scale, weights, out, workspace)
     c, index, batch, kv_heads, dim, width = cache._struct()
     if q.dim() != 4:
         raise ValueError(f"q must be [batch, queries, heads, dim], not {list(q.shape)}")
@@ -876,7 +911,7 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
         batch, queries, heads, kv_heads, dim, width, code, weights is not None), q.device)
     _check(L.qar_kv8_attention(c, q.data_ptr(), code, queries, heads, None if q_lens is None else q_lens.data_ptr(),
                                dim ** -0.5 if scale is None else scale, None if weights is None else weights.data_ptr(),
-                               out.data_ptr(), ws, size, _stream(stream)), "qar_kv8_attention")
+                               out.data_ptr(), ws, size, _current(index)), "qar_kv8_attention")
     return out
 
 
@@ -885,6 +920,9 @@ def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: 
     """``into`` receives, of every sequence and head, the last min(recent, keep)
     tokens of ``cache`` and the heaviest others, ``keep`` in all, and its lengths
     -> (kept positions int32[batch, kv_heads, keep], -1 behind them; their weights, 0 behind them)."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_evict(cache, into, weights, recent, keep, kept, moved)
     c, index, batch, heads, _, width = cache._struct()
     d, other = into._struct("into")[:2]
     if other != index:
@@ -906,5 +944,5 @@ def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: 
     if moved is None:
         moved = weights.new_empty(shape)
     _check(lib().qar_kv8_evict(c, d, weights.data_ptr(), recent, keep, kept.data_ptr(), moved.data_ptr(),
-                               _stream(stream)), "qar_kv8_evict")
+                               _current(index)), "qar_kv8_evict")
     return kept, moved

@@ -51,9 +51,10 @@ def encode(x, scale):
     return np.where(scale > 0, np.clip(q, -127, 127), 0).astype(np.int8)
 
 
-def make_cache(rng, batch, kv_heads, dim, lengths, width, spare=3, absent=()):
+def make_cache(rng, batch, kv_heads, dim, lengths, width, spare=3, absent=(), ahead=False):
     """A filled cache: scattered pages, garbage behind every sequence's end, NaN scales in pages that no table names.
-    `absent`: (sequence, page) entries that point outside the pool."""
+    `absent`: (sequence, page) entries that point outside the pool.  `ahead`: entries behind a sequence's end name pages that
+    were given to it but hold nothing yet."""
     pages = batch * width + spare
     k = rng.integers(-127, 128, (pages, kv_heads, PAGE, dim)).astype(np.int8)
     v = rng.integers(-127, 128, (pages, kv_heads, dim, PAGE)).astype(np.int8)
@@ -64,7 +65,8 @@ def make_cache(rng, batch, kv_heads, dim, lengths, width, spare=3, absent=()):
     for b, n in enumerate(lengths):
         used = -(-n // PAGE)
         unused[table[b, :used]] = False
-        table[b, used:] = -1
+        if not ahead:
+            table[b, used:] = -1
     ks[unused], vs[unused] = np.nan, np.nan
     for b, p in absent:
         table[b, p] = [pages, -7, 2 ** 31 - 1, -2 ** 31][(b + p) % 4]

@@ -188,6 +188,16 @@ def test_attention_rows_that_see_nothing(queries, dtype):
     assert (out[0] == 0).all() and (out[1] == 0).all() and (out[3] == 0).all()
 
 
+@pytest.mark.parametrize("queries", [1, 40])
+def test_pages_given_ahead_do_not_matter(queries):
+    """Table entries behind a sequence's end may name pages that hold nothing yet (NaN scales)."""
+    rng = np.random.default_rng(14)
+    c = ref.make_cache(rng, 4, 2, 128, [0, 1, 64, 300], 9, ahead=True)
+    _check_attention(c, 4, queries, 4, torch.bfloat16, [0, 1, min(queries, 64), queries], True, seed=7)
+    k, v = qar.qar_kv8_read(ref.to_cache(c), _ints(0, 0, 0, 0), 400, out_dtype=torch.float32)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_lengths_out_of_range(dtype):
     """Lengths beyond the table and below zero are clipped, q_lens likewise."""
@@ -351,6 +361,26 @@ def test_a_step_on_a_stream_and_in_a_graph():
         equal(eager, graphed)
         if i == 0:
             equal(eager, sided)
+
+
+def test_memory_of_a_call_on_another_stream_is_not_reused_under_it():
+    """Workspace and outputs that a call on a side stream allocates belong to that stream: work on the main stream that asks
+    for memory of the same sizes meanwhile does not get it."""
+    rng = np.random.default_rng(32)
+    cache = ref.to_cache(ref.make_cache(rng, 1, 1, 64, [30000], 469))
+    q, _ = ref.data(rng, (1, 2, 4, 64), torch.bfloat16)
+    want = qar.qar_kv8_attention(cache, q)
+    need = qar.lib().qar_kv8_attention_workspace_bytes(1, 2, 4, 1, 64, 469, 0, 0)
+    assert need > 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for handle in (side, side.cuda_stream):
+        for _ in range(20):
+            got = qar.qar_kv8_attention(cache, q, stream=handle)
+            for _ in range(4):
+                torch.empty(need, dtype=torch.uint8, device=DEV).fill_(255)
+            side.synchronize()
+            assert torch.equal(got, want)
 
 
 def test_empty_calls():
