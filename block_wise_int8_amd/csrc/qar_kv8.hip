@@ -1477,9 +1477,14 @@ void with_kind(int kind, F f) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// How an attention call is cut.  Few rows: a workgroup's four waves take a
-// page each in turn.  The cache's lengths are on the device, so cuts follow
-// the page table's width; workgroups behind a sequence's end leave at once.
+// How an attention call is cut.  The cache's lengths are on the device, so cuts
+// follow the page table's width; workgroups behind a sequence's end leave at
+// once.  Few rows: a workgroup's four waves take a page each in turn; about
+// two workgroups to a CU, unless that leaves a wave fewer than four pages
+// (2,048 workgroups against 512: 64 sequences of 8,000 tokens with weights
+// 109.6 against 104.3 us, 64 x 12 heads of 2,000 tokens 32.1 against 27.9, 4 x
+// 16 heads of 20,000 tokens 50.1 against 50.9), and at least one to a CU while
+// a wave has one page.  Many rows: cut only where the tiles leave CUs idle.
 // Two tiles of 16 rows at 256 channels would not fit a wave's registers.
 constexpr uint32_t few_rows_of(int dim) { return dim == 256 ? 16 : 32; }
 
@@ -1499,7 +1504,7 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
     };
     uint32_t splits;
     if (p.few) {
-        splits = cut(2048, 16);
+        splits = cut(512, 16);
         if (units * splits < 256) splits = cut(256, 4);
     } else {
         splits = units >= 256 ? 1 : cut(512, 4);
