@@ -651,7 +651,7 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
                 y = __builtin_fmaf(os[w][row16][d], f, y);
             }
             if (a.splits == 1) {
-                const bool seen = seq.counts(row) && l > 0.0f;
+                const bool seen = seq.counts(row) && l != 0.0f;
                 store1<IN>(a.out, query_row(a, b, h, row) * DIM + d, seen ? y / l : 0.0f);
                 if (a.lse && d == 0) a.lse[(size_t)bh * a.rows + row] = seen ? m - kLift + __builtin_amdgcn_logf(l) : INFINITY;
             } else {
@@ -710,7 +710,7 @@ __global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendA
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(ys[s][q][k], f, y[k]);
     }
-    const bool seen = l > 0.0f;
+    const bool seen = l != 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = seen ? y[k] / l : 0.0f;
     store4<OUT>(a.out, query_row(a, b, h, row) * DIM + q * 4, y);
@@ -943,7 +943,7 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
 
     total = sum_over_32(total);
     if (row >= a.rows) return;
-    const bool seen = there && total > 0.0f;
+    const bool seen = there && total != 0.0f;
     const float f = a.splits > 1 ? unit.unit : seen ? unit.unit / total : 0.0f;
     const size_t at = a.splits > 1 ? (((size_t)bh * a.splits + split) * a.rows + row) * DIM : query_row(a, b, h, row) * DIM;
     // register k of tile d is channel 32 d + 8 (k / 4) + 4 g + k % 4
@@ -1458,21 +1458,13 @@ template <int D>
 using Dim = std::integral_constant<int, D>;
 
 template <class F>
-void with_dim(int dim, F f) {
-    if (dim == 64)
-        f(Dim<64>{});
-    else if (dim == 128)
-        f(Dim<128>{});
-    else
-        f(Dim<256>{});
+hipError_t with_dim(int dim, F f) {
+    return dim == 64 ? f(Dim<64>{}) : dim == 128 ? f(Dim<128>{}) : f(Dim<256>{});
 }
 
 template <class F>
-void with_kind(int kind, F f) {
-    if (kind == kInBF16)
-        f(std::integral_constant<int, kInBF16>{});
-    else
-        f(std::integral_constant<int, kInF32>{});
+hipError_t with_kind(int kind, F f) {
+    return kind == kInBF16 ? f(std::integral_constant<int, kInBF16>{}) : f(std::integral_constant<int, kInF32>{});
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -1523,20 +1515,18 @@ hipError_t launch_kv8_append(const Kv8& c, const int32_t* starts, const void* k_
                              uint32_t tokens, hipStream_t st) {
     AppendArgs a = {c, starts, k_new, v_new, tokens, (tokens + kPage - 2) / kPage + 1};
     const uint32_t groups = c.batch * a.touched * c.heads * 2;
-    with_dim(c.dim, [&](auto D) {
-        with_kind(kind, [&](auto K) { kv8_append_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a); });
+    return with_dim(c.dim, [&](auto D) {
+        return with_kind(kind, [&](auto K) { return launch_threads(kv8_append_kernel<D(), K()>, groups, kThreads, st, a); });
     });
-    return hipGetLastError();
 }
 
 hipError_t launch_kv8_read(const Kv8& c, const int32_t* starts, uint32_t tokens, void* k_out, void* v_out, int kind,
                            hipStream_t st) {
     ReadArgs a = {c, starts, k_out, v_out, tokens, (tokens + kPage - 2) / kPage + 1};
     const uint32_t groups = c.batch * a.touched * c.heads * 2;
-    with_dim(c.dim, [&](auto D) {
-        with_kind(kind, [&](auto K) { kv8_read_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a); });
+    return with_dim(c.dim, [&](auto D) {
+        return with_kind(kind, [&](auto K) { return launch_threads(kv8_read_kernel<D(), K()>, groups, kThreads, st, a); });
     });
-    return hipGetLastError();
 }
 
 namespace {
@@ -1605,62 +1595,54 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
         a.stats = (float*)(scratch + l.stats);
         a.part = (float*)(scratch + l.part);
     }
-    hipError_t e = hipSuccess;
-    with_dim(c.dim, [&](auto D) {
-        with_kind(kind, [&](auto K) {
-            auto launched = [&] { return (e = hipGetLastError()) == hipSuccess; };
+    return with_dim(c.dim, [&](auto D) {
+        return with_kind(kind, [&](auto K) {
             const uint32_t groups = c.batch * c.heads * a.tiles * a.splits;
+            hipError_t e;
             if (!p.few)
-                kv8_attend_many_kernel<D(), K()><<<groups, kThreads, 0, st>>>(a);
-            else if (a.rows <= 16)
-                kv8_attend_few_kernel<D(), 1, K(), 4><<<groups, kThreads, 0, st>>>(a);
-            else if constexpr (few_rows_of(D()) > 16)
-                kv8_attend_few_kernel<D(), 2, K(), 4><<<groups, kThreads, 0, st>>>(a);
-            if (!launched()) return;
-            if (a.splits > 1) {
-                kv8_join_kernel<D(), K()><<<(uint32_t)items, kJoinGroups * D() / 4, 0, st>>>(a);
-                if (!launched()) return;
-            }
-            if (!weights) return;
+                e = launch_threads(kv8_attend_many_kernel<D(), K()>, groups, kThreads, st, a);
+            else if (few_rows_of(D()) == 16 || a.rows <= 16)
+                e = launch_threads(kv8_attend_few_kernel<D(), 1, K(), 4>, groups, kThreads, st, a);
+            else
+                e = launch_threads(kv8_attend_few_kernel<D(), few_rows_of(D()) / 16, K(), 4>, groups, kThreads, st, a);
+            if (e == hipSuccess && a.splits > 1)
+                e = launch_threads(kv8_join_kernel<D(), K()>, (uint32_t)items, kJoinGroups * D() / 4, st, a);
+            if (e != hipSuccess || !weights) return e;
             if (a.rows <= kOneTile) {
                 // about eight pages to a wave
                 a.splits = (c.width + 31) / 32;
-                kv8_weights_kernel<D(), K()><<<c.batch * c.heads * a.splits, kThreads, 0, st>>>(a);
-                (void)launched();
-                return;
+                return launch_threads(kv8_weights_kernel<D(), K()>, c.batch * c.heads * a.splits, kThreads, st, a);
             }
             ShareArgs s = {a, (kv_half8*)(scratch + l.fragments), (Row*)(scratch + l.rows), (float*)(scratch + l.sums),
                            l.row_tiles, l.shares, l.key_groups};
             const size_t heads_all = (size_t)c.batch * c.heads;
             constexpr int waves = kShareThreads / 64;
-            kv8_fragments_kernel<D(), K()>
-                <<<(uint32_t)((heads_all * l.row_tiles + waves - 1) / waves), kShareThreads, 0, st>>>(s);
-            if (!launched()) return;
-            kv8_shares_kernel<D(), K()><<<(uint32_t)(heads_all * l.key_groups * l.shares), kShareThreads, 0, st>>>(s);
-            if (!launched() || l.shares == 1) return;
-            kv8_add_shares_kernel<<<(uint32_t)((heads_all * c.width * kPage + kShareThreads - 1) / kShareThreads),
-                                    kShareThreads, 0, st>>>(s);
-            (void)launched();
+            e = launch_threads(kv8_fragments_kernel<D(), K()>, (uint32_t)((heads_all * l.row_tiles + waves - 1) / waves),
+                               kShareThreads, st, s);
+            if (e == hipSuccess)
+                e = launch_threads(kv8_shares_kernel<D(), K()>, (uint32_t)(heads_all * l.key_groups * l.shares),
+                                   kShareThreads, st, s);
+            if (e == hipSuccess && l.shares > 1)
+                e = launch_threads(kv8_add_shares_kernel,
+                                   (uint32_t)((heads_all * c.width * kPage + kShareThreads - 1) / kShareThreads),
+                                   kShareThreads, st, s);
+            return e;
         });
     });
-    return e;
 }
 
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st) {
     EvictArgs a = {c, into, weights, recent, keep, kept, moved};
     // the table's width bounds the tokens: their order stays in registers up to 24,576
-    if (c.width * kPage <= kSelectThreads * 8)
-        kv8_select_kernel<8><<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
-    else
-        kv8_select_kernel<24><<<c.batch * c.heads, kSelectThreads, 0, st>>>(a);
-    hipError_t e = hipGetLastError();
+    const hipError_t e =
+        launch_threads(c.width * kPage <= kSelectThreads * 8 ? kv8_select_kernel<8> : kv8_select_kernel<24>,
+                       c.batch * c.heads, kSelectThreads, st, a);
     if (e != hipSuccess) return e;
     const uint32_t out_pages = (keep + kPage - 1) / kPage;
-    with_dim(c.dim, [&](auto D) {
-        kv8_move_kernel<D()><<<c.batch * c.heads * out_pages, kThreads, 0, st>>>(a, out_pages);
+    return with_dim(c.dim, [&](auto D) {
+        return launch_threads(kv8_move_kernel<D()>, c.batch * c.heads * out_pages, kThreads, st, a, out_pages);
     });
-    return hipGetLastError();
 }
 
 } // namespace qar

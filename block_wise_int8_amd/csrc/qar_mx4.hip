@@ -743,14 +743,12 @@ uint32_t groups_for(size_t items, size_t per_group) { return (uint32_t)((items +
 uint32_t round_up(uint32_t v, uint32_t to) { return (v + to - 1) / to * to; }
 
 template <int IN, int PLACE>
-void quantize_into(const QuantizeArgs& a, uint32_t extra_groups, hipStream_t st) {
+hipError_t quantize_into(const QuantizeArgs& a, uint32_t extra_groups, hipStream_t st) {
     const uint32_t groups = a.quantize_groups + extra_groups;
     // whole 16-byte loads: rows start aligned; one flat range: rows of whole blocks
     const bool fast = PLACE == kRows ? a.cols % 32 == 0 : a.cols % 8 == 0;
-    if (fast)
-        mx4_quantize_kernel<IN, PLACE, true><<<groups, kThreads, 0, st>>>(a);
-    else
-        mx4_quantize_kernel<IN, PLACE, false><<<groups, kThreads, 0, st>>>(a);
+    return launch_threads(fast ? mx4_quantize_kernel<IN, PLACE, true> : mx4_quantize_kernel<IN, PLACE, false>, groups,
+                          kThreads, st, a);
 }
 
 template <int PLACE>
@@ -758,11 +756,7 @@ hipError_t quantize_call(QuantizeArgs a, int kind, hipStream_t st) {
     a.quantize_groups = groups_for(a.rows * a.padded * 4, 4 * kThreads);
     const uint32_t extra =
         PLACE == kTiles ? groups_for((a.w_rows + 31) / 32 * (a.padded / 8) * 64, kThreads) : 0;
-    if (kind == kInBF16)
-        quantize_into<kInBF16, PLACE>(a, extra, st);
-    else
-        quantize_into<kInF32, PLACE>(a, extra, st);
-    return hipGetLastError();
+    return kind == kInBF16 ? quantize_into<kInBF16, PLACE>(a, extra, st) : quantize_into<kInF32, PLACE>(a, extra, st);
 }
 
 // Two tiles of columns to a workgroup halve the reading of x, one gives twice
@@ -772,20 +766,18 @@ hipError_t quantize_call(QuantizeArgs a, int kind, hipStream_t st) {
 // against 13.7.  Four tiles and four or sixteen waves were slower than the
 // better of these everywhere but once (2%).
 template <int IN, int MT, bool FUSED>
-void few_rows(const LinearArgs& a, hipStream_t st) {
+hipError_t few_rows(const LinearArgs& a, hipStream_t st) {
     constexpr int NW = 8;
     if (groups_for(a.cols, 32) >= (MT == 1 ? 256u : 160u))
-        mx4_few_rows_kernel<IN, MT, 2, NW, FUSED><<<groups_for(a.cols, 32), NW * 64, 0, st>>>(a);
-    else
-        mx4_few_rows_kernel<IN, MT, 1, NW, FUSED><<<groups_for(a.cols, 16), NW * 64, 0, st>>>(a);
+        return launch_threads(mx4_few_rows_kernel<IN, MT, 2, NW, FUSED>, groups_for(a.cols, 32), NW * 64, st, a);
+    return launch_threads(mx4_few_rows_kernel<IN, MT, 1, NW, FUSED>, groups_for(a.cols, 16), NW * 64, st, a);
 }
 
 template <int IN, int BM, int BN, int WM, int WN>
-void tiled(LinearArgs& a, hipStream_t st) {
+hipError_t tiled(LinearArgs& a, hipStream_t st) {
     a.row_tiles = groups_for(a.rows, BM);
     a.col_tiles = groups_for(a.cols, BN);
-    mx4_tiled_kernel<IN, BM, BN, WM, WN>
-        <<<a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, 0, st>>>(a);
+    return launch_threads(mx4_tiled_kernel<IN, BM, BN, WM, WN>, a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, st, a);
 }
 
 // The few-row kernel, which reads x again for every 16 or 32 columns, against
@@ -812,20 +804,13 @@ hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, si
                                  hipStream_t st) {
     const uint32_t blocks = groups_for(cols, 32);
     const bool fast = cols % 32 == 0;
-    if (kind == kOutBF16) {
-        const uint32_t groups = groups_for(rows * blocks * 4, 4 * kThreads);
-        if (fast)
-            mx4_dequantize_kernel<kOutBF16, true><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
-        else
-            mx4_dequantize_kernel<kOutBF16, false><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
-    } else {
-        const uint32_t groups = groups_for(rows * blocks * 8, 4 * kThreads);
-        if (fast)
-            mx4_dequantize_kernel<kOutF32, true><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
-        else
-            mx4_dequantize_kernel<kOutF32, false><<<groups, kThreads, 0, st>>>(codes, scales, rows, cols, blocks, out);
-    }
-    return hipGetLastError();
+    const auto go = [&](auto OUT, uint32_t lanes) {
+        constexpr int O = decltype(OUT)::value;
+        return launch_threads(fast ? mx4_dequantize_kernel<O, true> : mx4_dequantize_kernel<O, false>,
+                              groups_for(rows * blocks * lanes, 4 * kThreads), kThreads, st, codes, scales, rows, cols, blocks,
+                              out);
+    };
+    return kind == kOutBF16 ? go(std::integral_constant<int, kOutBF16>{}, 4) : go(std::integral_constant<int, kOutF32>{}, 8);
 }
 
 size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols) {
@@ -848,11 +833,7 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     a.blocks = groups_for(inner, 32);
     if (fused(rows, inner)) {
         a.padded = round_up(a.blocks, 8);
-        if (kind == kInBF16)
-            few_rows<kInBF16, 1, true>(a, st);
-        else
-            few_rows<kInF32, 1, true>(a, st);
-        return hipGetLastError();
+        return kind == kInBF16 ? few_rows<kInBF16, 1, true>(a, st) : few_rows<kInF32, 1, true>(a, st);
     }
     QuantizeArgs q = {};
     q.x = x, q.rows = rows, q.cols = inner, q.blocks = a.blocks;
@@ -866,12 +847,10 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
         const hipError_t e = quantize_call<kFragments>(q, kind, st);
         if (e != hipSuccess) return e;
         if (rows <= 16)
-            kind == kInBF16 ? few_rows<kInBF16, 1, false>(a, st) : few_rows<kInF32, 1, false>(a, st);
-        else if (rows <= 32)
-            kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
-        else
-            kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);
-        return hipGetLastError();
+            return kind == kInBF16 ? few_rows<kInBF16, 1, false>(a, st) : few_rows<kInF32, 1, false>(a, st);
+        if (rows <= 32)
+            return kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
+        return kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);
     }
     q.padded = a.padded = round_up(a.blocks, 8);
     q.scales = q.codes + align256(rows * q.padded * 16);
@@ -889,18 +868,11 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     const auto tiles = [&](size_t size) { return (size_t)groups_for(rows, size) * groups_for(cols, size); };
     const auto go = [&](auto OUT) {
         constexpr int out = decltype(OUT)::value;
-        if (tiles(256) >= 256)
-            tiled<out, 256, 256, 128, 64>(a, st);
-        else if (tiles(128) >= 256)
-            tiled<out, 128, 128, 64, 64>(a, st);
-        else
-            tiled<out, 64, 64, 32, 64>(a, st);
+        if (tiles(256) >= 256) return tiled<out, 256, 256, 128, 64>(a, st);
+        if (tiles(128) >= 256) return tiled<out, 128, 128, 64, 64>(a, st);
+        return tiled<out, 64, 64, 32, 64>(a, st);
     };
-    if (out_kind == kOutBF16)
-        go(std::integral_constant<int, kOutBF16>{});
-    else
-        go(std::integral_constant<int, kOutF32>{});
-    return hipGetLastError();
+    return out_kind == kOutBF16 ? go(std::integral_constant<int, kOutBF16>{}) : go(std::integral_constant<int, kOutF32>{});
 }
 
 } // namespace qar

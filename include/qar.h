@@ -524,7 +524,8 @@ qar_status qar_kv8_read(const qar_kv8_cache* cache, const int32_t* starts, uint3
  * lengths[b] - q_lens[b] + i + 1 tokens.
  *   out[b][i][j] = sum over t of p_t v_t,  p = softmax(scale * q . k_t)
  * with key head j / (heads / kv_heads) for query head j.  A row that sees no
- * token gives zeros, and so do rows i >= q_lens[b].  Scores, maxima, sums and
+ * token gives zeros, and so do rows i >= q_lens[b].  A NaN in a query makes
+ * its row NaN and no other.  Scores, maxima, sums and
  * outputs are binary32; the softmax's numerators enter the second product in
  * binary16 (bf16 queries) or as two binary16 terms (binary32 queries).
  *   q, out     [batch][queries][heads][dim] of `dtype`, 16-byte aligned;

@@ -225,6 +225,21 @@ def test_attention_scales_far_apart(queries, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("queries,heads,n", [(1, 4, 70), (2, 4, 6000), (40, 4, 200), (70, 2, 3000)])
+def test_attention_keeps_a_nan_to_its_row(queries, heads, n, dtype):
+    rng = np.random.default_rng(15)
+    c = ref.make_cache(rng, 1, 2, 128, [n], -(-n // PAGE))
+    q, values = ref.data(rng, (1, queries, heads, 128), dtype)
+    want = ref.attend(c, values, [queries], 128 ** -0.5)
+    tol, _ = _attention_tolerance(want, q, dtype, 128, n)
+    q[0, -1, 1, 77] = float("nan")
+    got = qar.qar_kv8_attention(ref.to_cache(c), q).double().cpu().numpy()
+    assert np.isnan(got[0, -1, 1]).all()
+    got[0, -1, 1] = want["out"][0, -1, 1]
+    assert (np.abs(got - want["out"]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("batch,kv_heads,heads,dim,queries,n", [(1, 1, 1, 64, 1, 20000), (1, 2, 16, 64, 3, 9000),
                                                                (1, 1, 8, 128, 60, 5000), (40, 8, 8, 64, 1, 300)])
 def test_attention_split_over_long_caches(batch, kv_heads, heads, dim, queries, n, dtype):
@@ -390,3 +405,43 @@ def test_empty_calls():
     qar.qar_kv8_append(cache, _ints(0, 0), x, x)
     assert qar.qar_kv8_read(cache, _ints(0, 0), 0)[0].shape == (2, 0, 1, 64)
     assert qar.qar_kv8_attention(cache, x).shape == (2, 0, 1, 64)
+
+
+def test_stale_runtime_error_does_not_fail_a_good_call():
+    """A launch reports its own status: an error that an unrelated HIP call left on the thread (an invalid hipSetDevice) must
+    not turn a valid call into QAR_ERR_HIP."""
+    import ctypes
+    maps = open("/proc/self/maps").read().split()
+    hip = ctypes.CDLL(next(p for p in maps if "libamdhip64.so" in p))
+    hip.hipSetDevice.argtypes = [ctypes.c_int]
+    rng = np.random.default_rng(33)
+    c = ref.make_cache(rng, 2, 2, 64, [200, 131], 4)
+    cache, into = ref.to_cache(c), ref.to_cache(ref.make_cache(rng, 2, 2, 64, [128, 128], 2))
+    k, _ = ref.data(rng, (2, 1, 2, 64), torch.bfloat16)
+    outs = qar.qar_kv8_read(cache, _ints(0, 0), 100)
+    starts, kept = _ints(199, 130), torch.empty((2, 2, 100), dtype=torch.int32, device=DEV)
+    moved, summed = torch.empty((2, 2, 100), device=DEV), torch.zeros((2, 2, 256), device=DEV)
+    x, _ = ref.data(rng, (90, 200), torch.bfloat16)
+    w, s = qar.qar_mx4_quantize(x)
+    calls = [lambda: qar.qar_kv8_append(cache, starts, k, k), lambda: qar.qar_kv8_read(cache, starts, 100, out=outs),
+             lambda: qar.qar_kv8_evict(cache, into, summed, 16, 100, kept=kept, moved=moved),
+             lambda: qar.qar_mx4_quantize(x, codes=w, scales=s)]
+    for queries in (1, 50):
+        q, _ = ref.data(rng, (2, queries, 4, 64), torch.bfloat16)
+        need = qar.lib().qar_kv8_attention_workspace_bytes(2, queries, 4, 2, 64, 4, 0, 1)
+        ws, out = torch.empty(max(256, need), dtype=torch.uint8, device=DEV), torch.empty_like(q)
+        calls.append(lambda q=q, ws=ws, out=out: qar.qar_kv8_attention(cache, q, weights=summed, out=out, workspace=ws))
+    for rows in (4, 20, 90):
+        ws = torch.empty(max(256, qar.lib().qar_mx4_linear_workspace_bytes(rows, 200, 90)), dtype=torch.uint8, device=DEV)
+        y = torch.empty((rows, 90), dtype=torch.bfloat16, device=DEV)
+        calls.append(lambda a=x[:rows], y=y, ws=ws: qar.qar_mx4_linear(a, w, s, out=y, workspace=ws))
+    y = torch.empty_like(x)
+    calls.append(lambda: qar.qar_mx4_dequantize(w, s, 200, out=y))
+    torch.cuda.synchronize()
+    for call in calls:
+        assert hip.hipSetDevice(1 << 20) != 0                # hipErrorInvalidDevice, left on the thread
+        try:
+            call()
+        finally:
+            hip.hipGetLastError()                            # clear what the test left behind
+    torch.cuda.synchronize()
