@@ -1,9 +1,11 @@
-"""ctypes binding of libqar (include/qar.h): argument marshalling only.
+"""Binding of libqar (include/qar.h): argument marshalling only.
 
 Every computation runs in libqar's HIP kernels; this module turns torch
 tensors into device pointers, HIP streams into handles, allocates outputs
 with torch when the caller passes none, and raises ``QarError`` on a
-non-OK status.  A missing library raises; there is no fallback.
+non-OK status.  The AllReduce's calls go through ctypes, the serving calls,
+where the host's part counts, through an extension (csrc/qar_torch.cpp).  A
+missing library raises; there is no fallback.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(HERE, "libqar.so")
+EXTENSION = os.path.join(HERE, "_qar_torch.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "qar.h")
 
 QAR_OK, QAR_ERR_INVALID_ARG, QAR_ERR_MISALIGNED, QAR_ERR_UNSUPPORTED, QAR_ERR_HIP, QAR_ERR_CAPACITY = range(6)
@@ -639,9 +642,45 @@ def qar_dequantize_rows(codes: torch.Tensor, scales: torch.Tensor, rows: int, ro
 # serving: microscaled 4-bit floating point
 
 
-# These calls are short enough for their checks to count: each asks first
-# whether everything fits (`_fits`), and only if not finds out what does not
-# and says so.
+# These calls are short enough for the host's part to count, so an extension
+# (csrc/qar_torch.cpp) checks the arguments, allocates and calls the library.
+# It returns None where something does not fit; `_why_*` then find out what and
+# raise.
+
+_extension = None
+
+
+def _serve():
+    """The loaded extension (raises if it has not been built)."""
+    global _extension
+    if _extension is None:
+        lib()
+        try:
+            from . import _qar_torch
+        except ImportError as e:
+            raise RuntimeError(f"{EXTENSION} does not load (build it with __graft_entry__.build() or "
+                               f"block_wise_int8_amd/build.py): {e}") from e
+        _extension = _qar_torch
+    return _extension
+
+
+def _done(result, where):
+    """What the extension returned: a status or the call's tensors."""
+    if type(result) is int:
+        _check(result, where)
+        return None
+    return result
+
+
+def _on_current(index):
+    device = torch.cuda.current_device()
+    if index != device:
+        raise ValueError(f"the tensors are on GPU {index}, the current device is {device}")
+
+
+def _whole(v, what, lo, hi):
+    if isinstance(v, bool) or not isinstance(v, int) or not lo <= v < hi:
+        raise ValueError(f"{what} must be a whole number of at least {lo} and below {hi}, not {v}")
 
 
 def _as_current(stream):
@@ -651,33 +690,6 @@ def _as_current(stream):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
-
-
-def _current(index):
-    """The current stream's handle, for tensors on GPU ``index``."""
-    device = torch.cuda.current_device()
-    if index != device:
-        raise ValueError(f"the tensors are on GPU {index}, the current device is {device}")
-    return torch._C._cuda_getCurrentRawStream(device)
-
-
-def _fits(t, shape, dtype, index):
-    """A contiguous tensor of this shape and type on GPU `index` (which is at least 0)."""
-    return t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
-def _workspace(given, need, device):
-    """(pointer, bytes, tensor) of the caller's workspace, or of a new one (torch's
-    allocator reuses its memory only behind the work already on this stream)."""
-    if given is None:
-        if not need:
-            return None, 0, None
-        given = torch.empty(need, dtype=torch.uint8, device=device)
-    else:
-        _dev(given, "workspace")
-        if given.device != device:
-            raise ValueError(f"workspace is on {given.device}, the call's other tensors on {device}")
-    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def _matrix(t, what):
@@ -698,19 +710,23 @@ def qar_mx4_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales:
     if stream is not None:
         with _as_current(stream):
             return qar_mx4_quantize(x, codes, scales)
+    made = _serve().mx4_quantize(x, codes, scales)
+    return _done(made, "qar_mx4_quantize") if made is not None else _why_mx4_quantize(x, codes, scales)
+
+
+def _why_mx4_quantize(x, codes, scales):
     rows, cols = _matrix(x, "x").shape
-    dev, nb = x.device, _mx4_blocks(cols)
-    if codes is None:
-        codes = x.new_empty((rows, nb * 16), dtype=torch.uint8)
-    else:
-        _expect(codes, "codes", rows * nb * 16, (torch.uint8,), dev)
-    if scales is None:
-        scales = x.new_empty((rows, nb), dtype=torch.uint8)
-    else:
-        _expect(scales, "scales", rows * nb, (torch.uint8,), dev)
-    _check(lib().qar_mx4_quantize(x.data_ptr(), _dtype_code(x.dtype), rows, cols, codes.data_ptr(), scales.data_ptr(),
-                                  _current(x.get_device())), "qar_mx4_quantize")
-    return codes, scales
+    _dtype_code(x.dtype)
+    _why_mx4(codes, scales, rows, _mx4_blocks(cols), x.device)
+    _on_current(x.get_device())
+    raise ValueError("qar_mx4_quantize: the arguments do not fit")
+
+
+def _why_mx4(codes, scales, rows, nb, device):
+    if codes is not None:
+        _expect(codes, "codes", rows * nb * 16, (torch.uint8,), device)
+    if scales is not None:
+        _expect(scales, "scales", rows * nb, (torch.uint8,), device)
 
 
 def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out: torch.Tensor | None = None,
@@ -719,19 +735,25 @@ def qar_mx4_dequantize(codes: torch.Tensor, scales: torch.Tensor, cols: int, out
     if stream is not None:
         with _as_current(stream):
             return qar_mx4_dequantize(codes, scales, cols, out, out_dtype)
-    rows, nb, index = codes.shape[0], _mx4_blocks(cols), codes.get_device()
-    if index < 0 or not (_fits(codes, (rows, nb * 16), torch.uint8, index) and
-                         _fits(scales, (rows, nb), torch.uint8, index)):
-        _expect(_matrix(codes, "codes"), "codes", rows * nb * 16, (torch.uint8,), codes.device)
-        _expect(scales, "scales", rows * nb, (torch.uint8,), codes.device)
-    dev = codes.device
-    if out is None:
-        out = codes.new_empty((rows, cols), dtype=out_dtype)
-    else:
-        _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
-    _check(lib().qar_mx4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-                                    _dtype_code(out.dtype), _current(index)), "qar_mx4_dequantize")
-    return out
+    made = _serve().mx4_dequantize(codes, scales, cols, out, out_dtype)
+    return _done(made, "qar_mx4_dequantize") if made is not None else _why_mx4_dequantize(codes, scales, cols, out, out_dtype)
+
+
+def _why_mx4_dequantize(codes, scales, cols, out, out_dtype):
+    _whole(cols, "cols", 0, 1 << 63)
+    rows = _matrix(codes, "codes").shape[0]
+    _dev(scales, "scales")
+    _why_mx4(codes, scales, rows, _mx4_blocks(cols), codes.device)
+    _why_out(out, out_dtype, rows * cols, codes.device)
+    _on_current(codes.get_device())
+    raise ValueError("qar_mx4_dequantize: the arguments do not fit")
+
+
+def _why_out(out, out_dtype, numel, device):
+    if out is not None:
+        _expect(out, "out", numel, _DATA_DTYPES, device)
+    elif out_dtype is not None:
+        _dtype_code(out_dtype)
 
 
 def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, out: torch.Tensor | None = None,
@@ -745,22 +767,27 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
     if stream is not None:
         with _as_current(stream):
             return qar_mx4_linear(x, codes, scales, out, out_dtype, workspace)
+    made = _serve().mx4_linear(x, codes, scales, out, out_dtype, workspace)
+    if made is not None:
+        return _done(made, "qar_mx4_linear")
+    return _why_mx4_linear(x, codes, scales, out, out_dtype, workspace)
+
+
+def _why_mx4_linear(x, codes, scales, out, out_dtype, workspace):
     rows, inner = _matrix(x, "x").shape
-    cols, nb, index = codes.shape[0], _mx4_blocks(inner), x.get_device()
-    dev = x.device
-    if index < 0 or not (_fits(codes, (cols, nb * 16), torch.uint8, index) and
-                         _fits(scales, (cols, nb), torch.uint8, index)):
-        _expect(_matrix(codes, "codes"), "codes", cols * nb * 16, (torch.uint8,), dev)
-        _expect(scales, "scales", cols * nb, (torch.uint8,), dev)
-    if out is None:
-        out = x.new_empty((rows, cols), dtype=out_dtype or x.dtype)
-    else:
-        _expect(out, "out", rows * cols, _DATA_DTYPES, dev)
-    L = lib()
-    ws, size, keep = _workspace(workspace, L.qar_mx4_linear_workspace_bytes(rows, inner, cols), dev)
-    _check(L.qar_mx4_linear(x.data_ptr(), _dtype_code(x.dtype), rows, inner, codes.data_ptr(), scales.data_ptr(), cols,
-                            out.data_ptr(), _dtype_code(out.dtype), ws, size, _current(index)), "qar_mx4_linear")
-    return out
+    cols = _matrix(codes, "codes").shape[0]
+    _dev(scales, "scales")
+    _why_mx4(codes, scales, cols, _mx4_blocks(inner), x.device)
+    _dtype_code(x.dtype)
+    _why_out(out, out_dtype, rows * cols, x.device)
+    _why_workspace(workspace, x.device)
+    _on_current(x.get_device())
+    raise ValueError("qar_mx4_linear: the arguments do not fit")
+
+
+def _why_workspace(workspace, device):
+    if workspace is not None and _dev(workspace, "workspace").device != device:
+        raise ValueError(f"workspace is on {workspace.device}, the call's other tensors on {device}")
 
 
 # ----------------------------------------------------------------------------
@@ -794,29 +821,23 @@ class KvCache:
                    torch.zeros(batch, dtype=torch.int32, device=device))
 
     def _struct(self, what="cache"):
-        """(the C struct as bytes, GPU index, batch, kv_heads, dim, table_width)"""
+        """(the C struct as bytes, for calls of lib() itself, GPU index, batch, kv_heads, dim, table_width)"""
         k, v, ks, vs, table, lengths = self.k, self.v, self.k_scales, self.v_scales, self.page_table, self.lengths
-        index = k.get_device()
+        for name in self.__slots__:
+            if not isinstance(getattr(self, name), torch.Tensor):
+                raise TypeError(f"{what}.{name} must be a CUDA (HIP) tensor")
         if k.dim() != 4 or k.shape[2] != QAR_KV8_PAGE or table.dim() != 2:
             raise ValueError(f"{what}.k must be [pages, kv_heads, {QAR_KV8_PAGE}, dim] and {what}.page_table [batch, width]")
         pages, heads, page, dim = k.shape
         batch, width = table.shape
-        flat = (pages, heads)
-        if index < 0 or not (k.dtype is torch.int8 and k.is_contiguous() and
-                             _fits(v, (pages, heads, dim, page), torch.int8, index) and
-                             _fits(ks, flat, torch.float32, index) and _fits(vs, flat, torch.float32, index) and
-                             table.dtype is torch.int32 and table.is_contiguous() and table.get_device() == index and
-                             _fits(lengths, (batch,), torch.int32, index)):
-            dev = k.device
-            if tuple(v.shape) != (pages, heads, dim, QAR_KV8_PAGE):
-                raise ValueError(f"{what}.v must be {(pages, heads, dim, QAR_KV8_PAGE)}, not {tuple(v.shape)}")
-            for name, numel, dt in (("k", k.numel(), torch.int8), ("v", k.numel(), torch.int8),
-                                    ("k_scales", pages * heads, torch.float32),
-                                    ("v_scales", pages * heads, torch.float32), ("page_table", batch * width, torch.int32),
-                                    ("lengths", batch, torch.int32)):
-                _expect(getattr(self, name), f"{what}.{name}", numel, (dt,), dev)
+        if tuple(v.shape) != (pages, heads, dim, page):
+            raise ValueError(f"{what}.v must be {(pages, heads, dim, page)}, not {tuple(v.shape)}")
+        for name, numel, dt in (("k", k.numel(), torch.int8), ("v", k.numel(), torch.int8),
+                                ("k_scales", pages * heads, torch.float32), ("v_scales", pages * heads, torch.float32),
+                                ("page_table", batch * width, torch.int32), ("lengths", batch, torch.int32)):
+            _expect(getattr(self, name), f"{what}.{name}", numel, (dt,), k.device)
         return _KV_PACK(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), table.data_ptr(), lengths.data_ptr(),
-                        pages, heads, dim, batch, width), index, batch, heads, dim, width
+                        pages, heads, dim, batch, width), k.get_device(), batch, heads, dim, width
 
 
 def _shaped(t, what, shape, dtypes, device):
@@ -838,17 +859,18 @@ def qar_kv8_append(cache: KvCache, starts: torch.Tensor, k_new: torch.Tensor, v_
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_append(cache, starts, k_new, v_new)
-    c, index, batch, heads, dim, _ = cache._struct()
-    tokens = k_new.shape[1] if k_new.dim() == 4 else -1
-    shape, dtype = (batch, tokens, heads, dim), k_new.dtype
-    if index < 0 or not (dtype in _DATA_DTYPES and _fits(k_new, shape, dtype, index) and
-                         _fits(v_new, shape, dtype, index) and _fits(starts, (batch,), torch.int32, index)):
-        dev = cache.k.device
-        _shaped(k_new, "k_new", shape, _DATA_DTYPES, dev)
-        _shaped(v_new, "v_new", shape, (dtype,), dev)
-        _shaped(starts, "starts", (batch,), _INT32, dev)
-    _check(lib().qar_kv8_append(c, starts.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _dtype_code(dtype), tokens,
-                                _current(index)), "qar_kv8_append")
+    made = _serve().kv8_append(cache, starts, k_new, v_new)
+    return _done(made, "qar_kv8_append") if made is not None else _why_kv8_append(cache, starts, k_new, v_new)
+
+
+def _why_kv8_append(cache, starts, k_new, v_new):
+    _, index, batch, heads, dim, _ = cache._struct()
+    shape, dev = (batch, k_new.shape[1] if _dev(k_new, "k_new").dim() == 4 else -1, heads, dim), cache.k.device
+    _shaped(k_new, "k_new", shape, _DATA_DTYPES, dev)
+    _shaped(v_new, "v_new", shape, (k_new.dtype,), dev)
+    _shaped(starts, "starts", (batch,), _INT32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_append: the arguments do not fit")
 
 
 def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: torch.dtype = torch.bfloat16,
@@ -859,19 +881,24 @@ def qar_kv8_read(cache: KvCache, starts: torch.Tensor, tokens: int, out_dtype: t
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_read(cache, starts, tokens, out_dtype, out)
-    c, index, batch, heads, dim, _ = cache._struct()
-    shape = (batch, tokens, heads, dim)
-    if index < 0 or not _fits(starts, (batch,), torch.int32, index):
-        _shaped(starts, "starts", (batch,), _INT32, cache.k.device)
+    if out is not None:
+        out = tuple(out)
+    made = _serve().kv8_read(cache, starts, tokens, out_dtype, out)
+    return _done(made, "qar_kv8_read") if made is not None else _why_kv8_read(cache, starts, tokens, out_dtype, out)
+
+
+def _why_kv8_read(cache, starts, tokens, out_dtype, out):
+    _, index, batch, heads, dim, _ = cache._struct()
+    _whole(tokens, "tokens", 0, 1 << 32)
+    shape, dev = (batch, tokens, heads, dim), cache.k.device
+    _shaped(starts, "starts", (batch,), _INT32, dev)
     if out is None:
-        k, v = cache.k.new_empty(shape, dtype=out_dtype), cache.k.new_empty(shape, dtype=out_dtype)
+        _dtype_code(out_dtype)
     else:
-        k, v = out
-        _shaped(k, "out[0]", shape, _DATA_DTYPES, cache.k.device)
-        _shaped(v, "out[1]", shape, (k.dtype,), cache.k.device)
-    _check(lib().qar_kv8_read(c, starts.data_ptr(), tokens, k.data_ptr(), v.data_ptr(), _dtype_code(k.dtype),
-                              _current(index)), "qar_kv8_read")
-    return k, v
+        _shaped(out[0], "out[0]", shape, _DATA_DTYPES, dev)
+        _shaped(out[1], "out[1]", shape, (out[0].dtype,), dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_read: the arguments do not fit")
 
 
 def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | None = None, scale: float | None = None,
@@ -886,33 +913,30 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_attention(cache, q, q_lens, scale, weights, out, workspace)
-    c, index, batch, kv_heads, dim, width = cache._struct()
-    if q.dim() != 4:
+    made = _serve().kv8_attention(cache, q, q_lens, scale, weights, out, workspace)
+    if made is not None:
+        return _done(made, "qar_kv8_attention")
+    return _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace)
+
+
+def _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace):
+    _, index, batch, kv_heads, dim, width = cache._struct()
+    dev = cache.k.device
+    if _dev(q, "q").dim() != 4:
         raise ValueError(f"q must be [batch, queries, heads, dim], not {list(q.shape)}")
-    _, queries, heads, _ = q.shape
-    shape, dtype = (batch, queries, heads, dim), q.dtype
-    summed = (batch, kv_heads, width * QAR_KV8_PAGE)
-    if index < 0 or not (dtype in _DATA_DTYPES and _fits(q, shape, dtype, index) and
-                         (q_lens is None or _fits(q_lens, (batch,), torch.int32, index)) and
-                         (weights is None or _fits(weights, summed, torch.float32, index)) and
-                         (out is None or _fits(out, shape, dtype, index))):
-        dev = cache.k.device
-        _shaped(q, "q", shape, _DATA_DTYPES, dev)
-        if q_lens is not None:
-            _shaped(q_lens, "q_lens", (batch,), _INT32, dev)
-        if weights is not None:
-            _shaped(weights, "weights", summed, _F32, dev)
-        if out is not None:
-            _shaped(out, "out", shape, (dtype,), dev)
-    if out is None:
-        out = torch.empty_like(q)
-    L, code = lib(), _dtype_code(dtype)
-    ws, size, keep = _workspace(workspace, L.qar_kv8_attention_workspace_bytes(
-        batch, queries, heads, kv_heads, dim, width, code, weights is not None), q.device)
-    _check(L.qar_kv8_attention(c, q.data_ptr(), code, queries, heads, None if q_lens is None else q_lens.data_ptr(),
-                               dim ** -0.5 if scale is None else scale, None if weights is None else weights.data_ptr(),
-                               out.data_ptr(), ws, size, _current(index)), "qar_kv8_attention")
-    return out
+    shape = (batch, q.shape[1], q.shape[2], dim)
+    _shaped(q, "q", shape, _DATA_DTYPES, dev)
+    if q_lens is not None:
+        _shaped(q_lens, "q_lens", (batch,), _INT32, dev)
+    if scale is not None:
+        float(scale)
+    if weights is not None:
+        _shaped(weights, "weights", (batch, kv_heads, width * QAR_KV8_PAGE), _F32, dev)
+    if out is not None:
+        _shaped(out, "out", shape, (q.dtype,), dev)
+    _why_workspace(workspace, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_attention: the arguments do not fit")
 
 
 def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: int, keep: int,
@@ -923,26 +947,25 @@ def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: 
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_evict(cache, into, weights, recent, keep, kept, moved)
-    c, index, batch, heads, _, width = cache._struct()
-    d, other = into._struct("into")[:2]
-    if other != index:
+    made = _serve().kv8_evict(cache, into, weights, recent, keep, kept, moved)
+    if made is not None:
+        return _done(made, "qar_kv8_evict")
+    return _why_kv8_evict(cache, into, weights, recent, keep, kept, moved)
+
+
+def _why_kv8_evict(cache, into, weights, recent, keep, kept, moved):
+    _, index, batch, heads, _, width = cache._struct()
+    if into._struct("into")[1] != index:
         raise ValueError(f"into is on {into.k.device}, cache on {cache.k.device}")
     if not 0 <= recent < 1 << 32 or not 1 <= keep < 1 << 31:
         raise ValueError(f"recent must be at least 0 and keep at least 1, not {recent} and {keep}")
-    summed, shape = (batch, heads, width * QAR_KV8_PAGE), (batch, heads, keep)
-    if index < 0 or not (_fits(weights, summed, torch.float32, index) and
-                         (kept is None or _fits(kept, shape, torch.int32, index)) and
-                         (moved is None or _fits(moved, shape, torch.float32, index))):
-        dev = cache.k.device
-        _shaped(weights, "weights", summed, _F32, dev)
-        if kept is not None:
-            _shaped(kept, "kept", shape, _INT32, dev)
-        if moved is not None:
-            _shaped(moved, "moved", shape, _F32, dev)
-    if kept is None:
-        kept = weights.new_empty(shape, dtype=torch.int32)
-    if moved is None:
-        moved = weights.new_empty(shape)
-    _check(lib().qar_kv8_evict(c, d, weights.data_ptr(), recent, keep, kept.data_ptr(), moved.data_ptr(),
-                               _current(index)), "qar_kv8_evict")
-    return kept, moved
+    _whole(recent, "recent", 0, 1 << 32)
+    _whole(keep, "keep", 1, 1 << 31)
+    shape, dev = (batch, heads, keep), cache.k.device
+    _shaped(weights, "weights", (batch, heads, width * QAR_KV8_PAGE), _F32, dev)
+    if kept is not None:
+        _shaped(kept, "kept", shape, _INT32, dev)
+    if moved is not None:
+        _shaped(moved, "moved", shape, _F32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_evict: the arguments do not fit")
