@@ -718,13 +718,21 @@ __global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendA
 }
 
 // --- many rows: four waves of 32 rows share a page in LDS, converted to
-// binary16 once for all of them, in two buffers; the page behind it is on its
-// way to registers meanwhile.  Bound by the two products and the softmax's
-// arithmetic together (0.6 of the binary16 rate that a large matrix product
-// reaches, of it 0.5 for causal prompts).  Measured and left out: the next
-// page's scores formed beside this page's exponentials, eight waves with half
-// the keys each, raised priorities for the longest tiles: each within 4% or
-// slower.
+// binary16 once for all of them; the next page's codes are on their way to LDS
+// meanwhile, so that no registers wait for them and one more workgroup fits a
+// CU (1,000 queries x 64 heads of 64 channels 100 -> 92 us, 16 heads of 256
+// channels 126 -> 121; with 128 channels within 2% of two buffers of tiles and
+// codes in registers).
+//
+// Bound by vector and matrix instructions together: for 4 x 1,024 queries x 32
+// heads over 4,096 keys (0.8 PFLOP/s) the matrix units are busy in 39% of the
+// cycles and vector instructions issue in 60%, at 1.9 GHz, to which the chip
+// lowers its clock (2.4 GHz) for both.  Causal prompts wait for their longest
+// tiles as well.  Measured and left out, each within 4% or slower: the next
+// page's scores formed beside this page's exponentials, LDS reads 4 to 10
+// products ahead, eight waves with half the keys each, raised priorities for
+// the longest tiles, for matrix instructions or for one of the workgroups of a
+// CU; 64 rows to a wave took 1.45 times the time.
 //
 // 32x32x16 products: lane l = 32 g + r.  Row m of a tile of 32 keys is given
 // the key with bits 2 and 3 of m exchanged: lane half g then receives keys 16
@@ -745,19 +753,34 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// 16 bytes for each lane to LDS, the lanes' one behind the other from `to`,
+// which is the wave's.
+__device__ __forceinline__ void to_lds(const void* from, void* to) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 template <int DIM, int IN>
-__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void kv8_attend_many_kernel(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (IN == kInBF16 && DIM < 256))
+    void kv8_attend_many_kernel(AttendArgs a) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
     constexpr int KR = DIM / 8;                        // slots of a row of keys
     const auto k_swizzle = [](uint32_t row) { return DIM == 64 ? row / 2 % 8 : row % 16; };
-    __shared__ kv_half8 k_tile[2][kPage * KR], v_tile[2][DIM * 8];
+    __shared__ kv_half8 k_tile[kPage * KR], v_tile[DIM * 8];
+    __shared__ uint4 k_codes[U * kThreads], v_codes[U * kThreads];
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), r = lane % 32,
                    g = lane / 32;
     // the last tiles see the most keys: first
     const uint32_t split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
-    const uint32_t bh = rest % (a.c.heads * a.c.batch), tile = a.tiles - 1 - rest / (a.c.heads * a.c.batch);
-    const uint32_t h = bh % a.c.heads, b = bh / a.c.heads;
+    const uint32_t heads = a.c.heads * a.c.batch, turn = rest / heads, tile = a.tiles - 1 - turn;
+    // A CU's workgroups are 256 apart or a multiple: sequences are turned every
+    // 256, or a long one would have all of its tiles on the same CUs (two
+    // prompts of up to 2,048 tokens 105 -> 97 us; within 2% for other batches).
+    const uint32_t h = rest % a.c.heads, b = (rest % heads / a.c.heads + (uint32_t)((size_t)turn * heads / 256)) % a.c.batch;
+    const uint32_t bh = b * a.c.heads + h;
     const uint32_t first_row = tile * kTileRows + wave * 32, row = first_row + r;
 
     // Loads that depend on no other come first: a row of queries whatever the
@@ -766,7 +789,6 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
     raw.load(a.q, query_row(a, b, h, min(row, a.rows - 1)), g * 8, true);
     const int32_t* table = a.c.table + (size_t)b * a.c.width;
     const uint32_t first = split * a.pages_per_split, limit_page = min(first + a.pages_per_split, a.c.width);
-    uint4 kr[U], vr[U];
     // The pages' numbers and scales come 64 at a time, one in each lane: looked
     // up one by one, every page would wait for a scalar load, and with it for
     // the wave's LDS reads.  Asked for in ascending order; pages behind
@@ -794,37 +816,19 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
                     __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i)),
                     __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i))};
     };
-    auto load_k = [&](int32_t id) {
-        const int8_t* k = a.c.k + ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
-#pragma unroll
-        for (int u = 0; u < U; ++u) kr[u] = *reinterpret_cast<const uint4*>(k + u * kThreads * 16);
-    };
-    auto load_v = [&](int32_t id) {
-        const int8_t* v = a.c.v + ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
-#pragma unroll
-        for (int u = 0; u < U; ++u) vr[u] = *reinterpret_cast<const uint4*>(v + u * kThreads * 16);
-    };
-    auto put_k = [&](int buffer) {
+    // A page's codes go straight to LDS; each lane later reads what it asked
+    // for itself.
+    auto fetch = [&](int32_t id) {
+        const size_t at = ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t i = u * kThreads + tid;
-            const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
-            k_tile[buffer][lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
-            k_tile[buffer][lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
-        }
-    };
-    auto put_v = [&](int buffer) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t i = u * kThreads + tid, d = i / 4, e = i % 4 * 2;
-            v_tile[buffer][d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
-            v_tile[buffer][d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
+            to_lds(a.c.k + at + u * kThreads * 16, k_codes + u * kThreads + wave * 64);
+            to_lds(a.c.v + at + u * kThreads * 16, v_codes + u * kThreads + wave * 64);
         }
     };
     look_up();
     Page now = page_at(first), next = page_at(first + 1);
-    load_k(now.id);
-    load_v(now.id);
+    fetch(now.id);
 
     const Sequence seq(a, b);
     const bool there = seq.counts(row);
@@ -846,40 +850,42 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
     kv_f32x16 o[DIM / 32] = {};
     Unit unit;
     float top = -FLT_MAX, total = 0.0f;
-    auto scores = [&](int buffer, kv_f32x16 (&s)[2]) {
-        s[0] = s[1] = kv_f32x16{};
-#pragma unroll
-        for (int c = 0; c < DIM / 16; ++c)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint32_t lr = t * 32 + r;
-                const kv_half8 k = k_tile[buffer][lr * KR + ((c * 2 + g) ^ k_swizzle(lr))];
-#pragma unroll
-                for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
-            }
-    };
-
-    if (first < last) {
-        put_k(0);
-        put_v(0);
-        load_k(next.id);
-        load_v(next.id);
-    }
-    // At a page's beginning: its codes are in LDS (behind the barrier), the
-    // next page's in registers or on their way there.
+    // byte offsets of the first fragments; the others differ by an exclusive or
+    // or a constant
+    const uint32_t k_first = r * (KR * 16) + (g ^ k_swizzle(r)) * 16, v_first = r * 128 + (g ^ r / 2 % 8) * 16;
     for (uint32_t page = first; page < last; ++page) {
-        const int even = (page - first) % 2;
-        lds_barrier();
-        const Page after = page_at(page + 2);
-        if (page + 1 < last) {
-            put_k(even ^ 1);
-            put_v(even ^ 1);
-            load_k(after.id);
-            load_v(after.id);
+        loads_done();
+        uint4 kr[U], vr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) kr[u] = k_codes[u * kThreads + tid], vr[u] = v_codes[u * kThreads + tid];
+        lds_barrier();                               // all waves are done with the page before
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid;
+            const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
+            k_tile[lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
+            k_tile[lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
+            const uint32_t d = i / 4, e = i % 4 * 2;
+            v_tile[d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
+            v_tile[d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
         }
+        const Page after = page_at(page + 2);
+        if (page + 1 < last) fetch(next.id);
+        lds_barrier();
+        // kept in registers, all the fragments' addresses would take thirteen
+        uint32_t k_at = k_first, v_at = v_first;
+        asm volatile("" : "+v"(k_at), "+v"(v_at));
         if (page < my_last && now.id >= 0) {
             kv_f32x16 s[2];
-            scores(even, s);
+            s[0] = s[1] = kv_f32x16{};
+#pragma unroll
+            for (int c = 0; c < DIM / 16; ++c)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const kv_half8 k = *reinterpret_cast<const kv_half8*>((const char*)k_tile + (k_at ^ (c * 32)) + t * 32 * KR * 16);
+#pragma unroll
+                    for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
+                }
             const int32_t key0 = (int32_t)(page * kPage);
             const float shrink_all = unit.next(now.vs);
             if (shrink_all != 1.0f)
@@ -932,14 +938,14 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : DIM == 128 ? 2 : 3) void
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int d = 0; d < DIM / 32; ++d) {
-                    const uint32_t lr = d * 32 + r;
-                    const kv_half8 v = v_tile[even][lr * 8 + ((u * 2 + g) ^ lr / 2 % 8)];
+                    const kv_half8 v = *reinterpret_cast<const kv_half8*>((const char*)v_tile + (v_at ^ (u * 32)) + d * 32 * 128);
 #pragma unroll
                     for (int e = 0; e < T; ++e) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], o[d], 0, 0, 0);
                 }
         }
         now = next, next = after;
     }
+    loads_done();                                    // nothing may write to LDS that is no longer this workgroup's
 
     total = sum_over_32(total);
     if (row >= a.rows) return;
