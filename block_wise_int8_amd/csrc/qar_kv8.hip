@@ -67,6 +67,16 @@ __device__ __forceinline__ void store4(void* x, size_t e, kv_f32x4 v) {
         store_b128((float*)x + e, __builtin_bit_cast(uint4, v));
 }
 
+// The same for stores that fill a line piece by piece: these wait in the
+// cache for the rest of it.
+template <int OUT>
+__device__ __forceinline__ void merge4(void* x, size_t e, kv_f32x4 v) {
+    if constexpr (OUT == kOutBF16)
+        *reinterpret_cast<uint2*>((uint16_t*)x + e) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    else
+        *reinterpret_cast<kv_f32x4*>((float*)x + e) = v;
+}
+
 // The codes of four values, packed.
 __device__ __forceinline__ uint32_t codes4(kv_f32x4 v, float s) {
     const float f[4] = {v[0], v[1], v[2], v[3]};
@@ -962,7 +972,7 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
             if (a.splits > 1)
                 *reinterpret_cast<kv_f32x4*>(a.part + to) = y;
             else
-                store4<IN>(a.out, to, seen ? y : kv_f32x4{});
+                merge4<IN>(a.out, to, seen ? y : kv_f32x4{});
         }
     if (g) return;
     if (a.splits > 1)
