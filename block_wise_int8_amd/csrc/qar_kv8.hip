@@ -77,12 +77,25 @@ __device__ __forceinline__ void merge4(void* x, size_t e, kv_f32x4 v) {
         *reinterpret_cast<kv_f32x4*>((float*)x + e) = v;
 }
 
-// The codes of four values, packed.
-__device__ __forceinline__ uint32_t codes4(kv_f32x4 v, float s) {
-    const float f[4] = {v[0], v[1], v[2], v[3]};
-    uint32_t w[4];
-    int_code_words(f, s, 127.0f, w);
-    return pack4(w[0], w[1], w[2], w[3]);
+// Calls f with the function that gives four values' codes, packed, for a scale
+// that the workgroup shares: how a scale is divided by (exactly either way) is
+// decided once, and its reciprocal formed once, for all that f encodes.
+template <class F>
+__device__ __forceinline__ void with_codes(float s, F f) {
+    if (s >= kFastQuotientMinScale) {
+        const float r = 1.0f / s;
+        f([&](kv_f32x4 v) {
+            return pack4(code_bits_of(fast_quotient(v[0], s, r)), code_bits_of(fast_quotient(v[1], s, r)),
+                         code_bits_of(fast_quotient(v[2], s, r)), code_bits_of(fast_quotient(v[3], s, r)));
+        });
+    } else if (s != 0.0f) {
+        f([&](kv_f32x4 v) {
+            return pack4(clamped_code_bits_of(v[0] / s), clamped_code_bits_of(v[1] / s), clamped_code_bits_of(v[2] / s),
+                         clamped_code_bits_of(v[3] / s));
+        });
+    } else {
+        f([](kv_f32x4) { return 0u; });
+    }
 }
 
 __device__ __forceinline__ kv_f32x4 values4(uint32_t w, float s) {
@@ -163,25 +176,27 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
     const bool grown = scale > before;
     if (threadIdx.x == 0) *scale_at = scale;
 
-    if (which == 0) {
-        if (grown)
-            for (int i = threadIdx.x; i < old * Q; i += kThreads) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(codes) + i;
-                *w = codes4(values4(*w, before), scale);
-            }
+    with_codes(scale, [&](auto codes4) {
+        if (which == 0) {
+            if (grown)
+                for (int i = threadIdx.x; i < old * Q; i += kThreads) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(codes) + i;
+                    *w = codes4(values4(*w, before));
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = u * kThreads + threadIdx.x;
-            if (i / E < fresh)
-                reinterpret_cast<uint2*>(codes)[old * E + i] = make_uint2(codes4(v[u][0], scale), codes4(v[u][1], scale));
+            for (int u = 0; u < U; ++u) {
+                const int i = u * kThreads + threadIdx.x;
+                if (i / E < fresh)
+                    reinterpret_cast<uint2*>(codes)[old * E + i] = make_uint2(codes4(v[u][0]), codes4(v[u][1]));
+            }
+            return;
         }
-    } else {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = u * kThreads + threadIdx.x, t = i / E, e = i % E;
             if (t >= fresh) break;
-            tile[2 * e][old + t] = codes4(v[u][0], scale);
-            tile[2 * e + 1][old + t] = codes4(v[u][1], scale);
+            tile[2 * e][old + t] = codes4(v[u][0]);
+            tile[2 * e + 1][old + t] = codes4(v[u][1]);
         }
         __syncthreads();
         // four channels by four tokens at a time
@@ -198,14 +213,14 @@ __global__ __launch_bounds__(kThreads) void kv8_append_kernel(AppendArgs a) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     keep[k] = row[k * (kPage / 4)];
-                    if (grown) keep[k] = codes4(values4(keep[k], before), scale);
+                    if (grown) keep[k] = codes4(values4(keep[k], before));
                     keep[k] &= mask;
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) row[k * (kPage / 4)] = w[k] | keep[k];
         }
-    }
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -1445,14 +1460,18 @@ __global__ __launch_bounds__(kThreads) void kv8_move_kernel(EvictArgs a, uint32_
     }
     const float k_new = group_max(mk, shared[0]) / 127.0f, v_new = group_max(mv, shared[1]) / 127.0f;
     if (tid == 0) a.into.k_scales[to] = k_new, a.into.v_scales[to] = v_new;
+    with_codes(v_new, [&](auto codes4) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) tile[lane][u * (kThreads / 64) + wave] = codes4(values4(vw[u], v_scale), v_new);
+        for (int u = 0; u < U; ++u) tile[lane][u * (kThreads / 64) + wave] = codes4(values4(vw[u], v_scale));
+    });
     uint32_t* k_codes = reinterpret_cast<uint32_t*>(a.into.k + to * (kPage * DIM));
+    with_codes(k_new, [&](auto codes4) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = u * kThreads + tid;
-        k_codes[i] = codes4(values4(kw[u], source_k_scale[i / Q]), k_new);
-    }
+        for (int u = 0; u < U; ++u) {
+            const int i = u * kThreads + tid;
+            k_codes[i] = codes4(values4(kw[u], source_k_scale[i / Q]));
+        }
+    });
     __syncthreads();
     uint32_t* v_codes = reinterpret_cast<uint32_t*>(a.into.v + to * (kPage * DIM));
 #pragma unroll
