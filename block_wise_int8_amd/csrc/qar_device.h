@@ -115,7 +115,6 @@ constexpr int kDppSwapAdjacent = 0xB1;   // quad_perm [1,0,3,2]
 constexpr int kDppSwapPairs = 0x4E;      // quad_perm [2,3,0,1]
 constexpr int kDppRowHalfMirror = 0x141; // lane i <-> 7-i within each 8 lanes
 constexpr int kDppRowMirror = 0x140;     // lane i <-> 15-i within each 16 lanes
-constexpr int kDppRowRotate8 = 0x128;    // lane i <-> i ^ 8 within each 16 lanes
 
 // Max over each aligned group of L lanes (4 .. 64); every lane of a group
 // gets its group's max.  Up to 16 lanes the groups lie inside one DPP row;

@@ -15,6 +15,7 @@
 
 #include "qar_device.h"
 #include "qar_launch.h"
+#include "qar_serve.h"
 
 namespace qar {
 namespace {

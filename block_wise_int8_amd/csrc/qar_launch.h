@@ -7,27 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <tuple>
-#include <type_traits>
-#include <utility>
-
 namespace qar {
-
-// Launches k<<<blocks, threads, 0, st>>>(a...) and returns that launch's
-// own status.  hipLaunchKernel reports the launch it was asked for; reading
-// hipGetLastError() after a triple-chevron launch would instead return any
-// error an unrelated runtime call had left on the thread.
-template <typename... P, typename... A>
-hipError_t launch_threads(void (*k)(P...), uint32_t blocks, uint32_t threads, hipStream_t st, A&&... a) {
-    static_assert(sizeof...(P) == sizeof...(A), "kernel argument count");
-    std::tuple<std::decay_t<P>...> vals(static_cast<std::decay_t<P>>(std::forward<A>(a))...);
-    void* args[sizeof...(P)];
-    std::apply([&](auto&... v) {
-        size_t i = 0;
-        ((args[i++] = static_cast<void*>(&v)), ...);
-    }, vals);
-    return hipLaunchKernel(reinterpret_cast<const void*>(k), dim3(blocks), dim3(threads), args, 0, st);
-}
 
 constexpr int kMaxRanks = 32;
 
