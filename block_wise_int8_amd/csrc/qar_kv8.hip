@@ -689,28 +689,33 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_at
     }
 }
 
-// The splits' results joined.  A workgroup takes one row: DIM / 4 lanes with
-// four channels each, eight times, each time an eighth of the splits, so that
-// few rows with many splits do not wait for one load after another (one group
-// only: 16.0 us instead of the present time for 256 rows of 32 splits).
-constexpr int kJoinGroups = 8;
+// The splits' results joined: DIM / 4 lanes with four channels each take a row,
+// or GROUPS times as many, each time some of its splits.  Few rows with many
+// splits want many groups, or they wait for one load after another (one group:
+// 16.0 us, eight: 5.7 for 256 rows of 32 splits); many rows with few splits one, or
+// most groups have nothing to read (eight: 22.7 us, one: 7.5 for 23,580 rows of 3
+// splits).
+constexpr int kJoinRows = 8;                // rows times groups of a workgroup
 
-template <int DIM, int OUT>
-__global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendArgs a) {
-    constexpr int Q = DIM / 4;
-    __shared__ kv_f32x4 ys[kJoinGroups][Q];
-    __shared__ float tops[kJoinGroups], totals[kJoinGroups];
-    const uint32_t item = blockIdx.x, q = threadIdx.x % Q, group = threadIdx.x / Q;
-    const uint32_t row = item % a.rows, bh = item / a.rows, h = bh % a.c.heads, b = bh / a.c.heads;
+template <int DIM, int OUT, int GROUPS>
+__global__ __launch_bounds__(kJoinRows * DIM / 4) void kv8_join_kernel(AttendArgs a) {
+    constexpr int Q = DIM / 4, ROWS = kJoinRows / GROUPS;
+    __shared__ kv_f32x4 ys[ROWS][GROUPS][Q];
+    __shared__ float tops[ROWS][GROUPS], totals[ROWS][GROUPS];
+    const uint32_t q = threadIdx.x % Q, group = threadIdx.x / Q % GROUPS;
+    const uint32_t mine = ROWS > 1 ? threadIdx.x / Q / GROUPS : 0;
+    const uint32_t rows = a.c.batch * a.c.heads * a.rows, item = blockIdx.x * ROWS + mine;
+    const bool inside = item < rows;
+    const uint32_t row = item % a.rows, bh = min(item, rows - 1) / a.rows, h = bh % a.c.heads, b = bh / a.c.heads;
     const Sequence seq(a, b);
     // the splits that hold keys which this row may see
-    const int32_t seen_keys = seq.counts(row) ? min(seq.limit(row), seq.n) : 0;
+    const int32_t seen_keys = inside && seq.counts(row) ? min(seq.limit(row), seq.n) : 0;
     const uint32_t pages = seen_keys > 0 ? (uint32_t)(seen_keys + kPage - 1) / kPage : 0;
     const uint32_t used = (pages + a.pages_per_split - 1) / a.pages_per_split;
     float m = -FLT_MAX, l = 0.0f;
     kv_f32x4 y = {};
 #pragma unroll 4
-    for (uint32_t s = group; s < used; s += kJoinGroups) {
+    for (uint32_t s = group; s < used; s += GROUPS) {
         const size_t at = ((size_t)bh * a.splits + s) * a.rows + row;
         const float2 stat = *reinterpret_cast<const float2*>(a.stats + at * 2);
         const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + q * 4);
@@ -720,22 +725,25 @@ __global__ __launch_bounds__(kJoinGroups * DIM / 4) void kv8_join_kernel(AttendA
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], e, y[k] * f);
     }
-    ys[group][q] = y;
-    if (q == 0) tops[group] = m, totals[group] = l;
-    __syncthreads();
-    if (group) return;
-    m = tops[0];
+    if constexpr (GROUPS > 1) {
+        ys[mine][group][q] = y;
+        if (q == 0) tops[mine][group] = m, totals[mine][group] = l;
+        __syncthreads();
+        if (group) return;
+        m = tops[mine][0];
 #pragma unroll
-    for (int s = 1; s < kJoinGroups; ++s) m = fmaxf(m, tops[s]);
-    l = 0.0f;
-    y = kv_f32x4{};
+        for (int s = 1; s < GROUPS; ++s) m = fmaxf(m, tops[mine][s]);
+        l = 0.0f;
+        y = kv_f32x4{};
 #pragma unroll
-    for (int s = 0; s < kJoinGroups; ++s) {
-        const float f = __builtin_amdgcn_exp2f(tops[s] - m);
-        l = __builtin_fmaf(totals[s], f, l);
+        for (int s = 0; s < GROUPS; ++s) {
+            const float f = __builtin_amdgcn_exp2f(tops[mine][s] - m);
+            l = __builtin_fmaf(totals[mine][s], f, l);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(ys[s][q][k], f, y[k]);
+            for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(ys[mine][s][q][k], f, y[k]);
+        }
     }
+    if (!inside) return;
     const bool seen = l != 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = seen ? y[k] / l : 0.0f;
@@ -1518,7 +1526,11 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 // (2,048 workgroups against 512: 64 sequences of 8,000 tokens with weights
 // 109.6 against 104.3 us, 64 x 12 heads of 2,000 tokens 32.1 against 27.9, 4 x
 // 16 heads of 20,000 tokens 50.1 against 50.9), and at least one to a CU while
-// a wave has one page.  Many rows: cut only where the tiles leave CUs idle.
+// a wave has one page.  Many rows: cut only where the tiles leave CUs idle, to
+// about one workgroup a CU with 256 channels, of which no two fit one (two:
+// 1,000 queries x 16 heads 82 against 52 us), else two; a cut has eight pages or
+// more where half the CUs have a tile without (four: 654 queries x 32 heads x 128
+// channels 31.9 against 29.6).
 // Two tiles of 16 rows at 256 channels would not fit a wave's registers.
 constexpr uint32_t few_rows_of(int dim) { return dim == 256 ? 16 : 32; }
 
@@ -1541,7 +1553,7 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
         splits = cut(512, 16);
         if (units * splits < 256) splits = cut(256, 4);
     } else {
-        splits = units >= 256 ? 1 : cut(512, 4);
+        splits = units >= 256 ? 1 : cut(dim == 256 ? 256 : 512, units >= 128 ? 8 : 4);
     }
     if (splits < 1) splits = 1;
     p.pages_per_split = (width + splits - 1) / splits;
@@ -1648,7 +1660,10 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
             else
                 e = launch_threads(kv8_attend_few_kernel<D(), few_rows_of(D()) / 16, K(), 4>, groups, kThreads, st, a);
             if (e == hipSuccess && a.splits > 1)
-                e = launch_threads(kv8_join_kernel<D(), K()>, (uint32_t)items, kJoinGroups * D() / 4, st, a);
+                e = a.splits > 4
+                        ? launch_threads(kv8_join_kernel<D(), K(), kJoinRows>, (uint32_t)items, kJoinRows * D() / 4, st, a)
+                        : launch_threads(kv8_join_kernel<D(), K(), 1>, (uint32_t)((items + kJoinRows - 1) / kJoinRows),
+                                         kJoinRows * D() / 4, st, a);
             if (e != hipSuccess || !weights) return e;
             if (a.rows <= kOneTile) {
                 // about eight pages to a wave
