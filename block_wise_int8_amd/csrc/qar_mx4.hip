@@ -62,10 +62,16 @@ __device__ __forceinline__ Eight<IN> load8(const void* x, size_t e) {
     return v;
 }
 
-// The first `count` of eight elements, zero for the others.
+// The first `count` of eight elements, zero for the others.  Eight come in one
+// load wherever they lie: vector memory instructions take any address (element
+// by element, quantizing bf16 [3863, 2922] and back took 33.6 us instead of 14.5).
 template <int IN>
 __device__ __forceinline__ Eight<IN> load8_some(const void* x, size_t e, int count) {
     Eight<IN> v = {};
+    if (count == 8) {
+        __builtin_memcpy(v.w, (const char*)x + e * (IN == kInBF16 ? 2 : 4), sizeof v.w);
+        return v;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < count) {
@@ -304,6 +310,8 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
                                        pack_bf16x2(y[6], y[7]));
             if constexpr (FAST) {
                 store_b128((uint16_t*)out + at, q);
+            } else if (count == P) {
+                __builtin_memcpy((uint16_t*)out + at, &q, 16);
             } else {
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -314,6 +322,8 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
             if constexpr (FAST) {
                 store_b128((float*)out + at, make_uint4(__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1]),
                                                         __builtin_bit_cast(uint32_t, y[2]), __builtin_bit_cast(uint32_t, y[3])));
+            } else if (count == P) {
+                __builtin_memcpy((float*)out + at, y, 16);
             } else {
 #pragma unroll
                 for (int k = 0; k < P; ++k)
@@ -527,13 +537,13 @@ __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
 // l % 32.
 
 // N elements (16 bytes) of an output row from column `col`, as far as the row
-// goes; one store where it is aligned.
+// goes; whole ones in one store, aligned or not.
 template <int N, class T>
 __device__ __forceinline__ void store_row(T* out, size_t row_at, size_t col, size_t cols, uint4 v) {
     if (col >= cols) return;
     T* p = out + row_at + col;
-    if (cols % N == 0) {
-        *reinterpret_cast<uint4*>(p) = v;
+    if (col + N <= cols) {
+        __builtin_memcpy(p, &v, 16);
         return;
     }
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
