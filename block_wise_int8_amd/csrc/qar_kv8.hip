@@ -1211,11 +1211,17 @@ __global__ __launch_bounds__(kShareThreads) void kv8_shares_kernel(ShareArgs s) 
             const Row now = row;
             if (tile + 1 < to) load(tile + 1);
             const float factor = ks * now.factor;
-            const int32_t sees = now.limit - (int32_t)key0 - (int32_t)g * 8;
+            const auto share_of = [&](int i) {
+                return __builtin_amdgcn_exp2f(__builtin_fmaf(even[i] + odd[i], factor, -now.lse));
+            };
+            // the tile's first row sees the fewest keys; rows without a query give 0 by their sum
+            if (__builtin_amdgcn_readfirstlane(now.limit) >= (int32_t)key0 + 32) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(even[i] + odd[i], factor, -now.lse));
-                sum[i] += 16 * (i / 8) + i % 8 < sees ? x : 0.0f;
+                for (int i = 0; i < 16; ++i) sum[i] += share_of(i);
+            } else {
+                const int32_t sees = now.limit - (int32_t)key0 - (int32_t)g * 8;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) sum[i] += 16 * (i / 8) + i % 8 < sees ? share_of(i) : 0.0f;
             }
         }
         // over the 32 lanes of a half; lane r < 16 of it keeps register r's key
