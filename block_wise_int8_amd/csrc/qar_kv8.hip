@@ -1263,7 +1263,7 @@ __global__ __launch_bounds__(kShareThreads) void kv8_add_shares_kernel(ShareArgs
 // indexes in order: each thread counts what it keeps of its own tokens, and
 // then places it.  The lower index stays where weights are equal.
 
-constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64, kBins = 2048;
+constexpr int kBins = 2048;
 
 struct EvictArgs {
     Kv8 c, into;
@@ -1288,7 +1288,7 @@ __device__ __forceinline__ float weight_of(uint32_t order) {
 // A thread has `own` consecutive tokens (a multiple of four).  The order of
 // the first HELD stays in registers; tokens behind them are read again where
 // needed.  0 stands for no token: no weight's order is that low.
-template <int HELD>
+template <int THREADS, int HELD>
 struct Tokens {
     const float* w;
     uint32_t first, end;
@@ -1320,9 +1320,10 @@ struct Tokens {
     }
 };
 
-template <int HELD>
-__global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a) {
-    __shared__ uint32_t bins[kBins], wave_sum[kSelectWaves], wave_more[kSelectWaves], wave_equal[kSelectWaves];
+template <int THREADS, int HELD>
+__global__ __launch_bounds__(THREADS) void kv8_select_kernel(EvictArgs a) {
+    constexpr int WAVES = THREADS / 64, OWN = kBins / THREADS;
+    __shared__ uint32_t bins[kBins], wave_sum[WAVES], wave_more[WAVES], wave_equal[WAVES];
     __shared__ uint32_t found_bin, found_above;
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
     const uint32_t bh = blockIdx.x, h = bh % a.c.heads, b = bh / a.c.heads;
@@ -1333,15 +1334,15 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     float* moved = a.moved + (size_t)bh * a.keep;
     if (h == 0 && tid == 0) a.into.lengths[b] = (int32_t)min(n, a.keep);
     if (n <= a.keep) {
-        for (uint32_t i = tid; i < a.keep; i += kSelectThreads) {
+        for (uint32_t i = tid; i < a.keep; i += THREADS) {
             kept[i] = i < n ? (int32_t)i : -1;
             moved[i] = i < n ? w[i] : 0.0f;
         }
         return;
     }
     const uint32_t free = n - recent, need = a.keep - recent;      // `need` of the first `free` tokens stay
-    const Tokens<HELD> tokens(w, free, (free + 4 * kSelectThreads - 1) / (4 * kSelectThreads) * 4);
-    for (uint32_t i = tid; i < recent; i += kSelectThreads) {
+    const Tokens<THREADS, HELD> tokens(w, free, (free + 4 * THREADS - 1) / (4 * THREADS) * 4);
+    for (uint32_t i = tid; i < recent; i += THREADS) {
         kept[need + i] = (int32_t)(free + i);
         moved[need + i] = w[free + i];
     }
@@ -1351,30 +1352,36 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t top = pass == 2 ? 1023 : 2047;
-        for (uint32_t i = tid; i < kBins; i += kSelectThreads) bins[i] = 0;
+        for (uint32_t i = tid; i < kBins; i += THREADS) bins[i] = 0;
         __syncthreads();
         tokens.each([&](uint32_t, uint32_t o) {
             if (o != 0 && (o & mask) == prefix) atomicAdd(&bins[(o >> shift) & top], 1u);
         });
         __syncthreads();
-        // tokens in this thread's two bins and in all above them
-        const uint32_t hi = bins[2 * tid + 1], lo = bins[2 * tid];
-        uint32_t suffix = hi + lo;
+        // tokens in this thread's bins and in all above them
+        uint32_t bin[OWN], suffix = 0;
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            bin[i] = bins[OWN * tid + i];
+            suffix += bin[i];
+        }
+        uint32_t above = suffix;
         for (int d = 1; d < 64; d *= 2) {
             const uint32_t other = __shfl_down(suffix, d);
             if (lane + d < 64) suffix += other;
         }
         if (lane == 0) wave_sum[wave] = suffix;
         __syncthreads();
-        uint32_t above = suffix - hi - lo;
+        above = suffix - above;
 #pragma unroll
-        for (uint32_t v = 1; v < kSelectWaves; ++v) above += v > wave ? wave_sum[v] : 0;
-        if (above < left && above + hi >= left) {
-            found_bin = 2 * tid + 1;
-            found_above = above;
-        } else if (above + hi < left && above + hi + lo >= left) {
-            found_bin = 2 * tid;
-            found_above = above + hi;
+        for (uint32_t v = 1; v < WAVES; ++v) above += v > wave ? wave_sum[v] : 0;
+#pragma unroll
+        for (int i = OWN - 1; i >= 0; --i) {
+            if (above < left && above + bin[i] >= left) {
+                found_bin = OWN * tid + i;
+                found_above = above;
+            }
+            above += bin[i];
         }
         __syncthreads();
         prefix |= found_bin << shift;
@@ -1399,7 +1406,7 @@ __global__ __launch_bounds__(kSelectThreads) void kv8_select_kernel(EvictArgs a)
     more_before -= more;
     equal_before -= equal;
 #pragma unroll
-    for (uint32_t v = 0; v + 1 < kSelectWaves; ++v) {
+    for (uint32_t v = 0; v + 1 < WAVES; ++v) {
         more_before += v < wave ? wave_more[v] : 0;
         equal_before += v < wave ? wave_equal[v] : 0;
     }
@@ -1698,10 +1705,14 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st) {
     EvictArgs a = {c, into, weights, recent, keep, kept, moved};
-    // the table's width bounds the tokens: their order stays in registers up to 24,576
-    const hipError_t e =
-        launch_threads(c.width * kPage <= kSelectThreads * 8 ? kv8_select_kernel<8> : kv8_select_kernel<24>,
-                       c.batch * c.heads, kSelectThreads, st, a);
+    // The table's width bounds the tokens: their order stays in registers up to
+    // 24,576.  Four waves meet at a barrier sooner than sixteen: eviction of 4 x 8
+    // heads of 1,100 tokens, with the read, 20.6 against 22.9 us; at 3,900 tokens,
+    // where they would read half of the tokens again in every pass, 43.5 against 38.
+    const uint32_t tokens = c.width * kPage, groups = c.batch * c.heads;
+    const hipError_t e = tokens <= 256 * 8    ? launch_threads(kv8_select_kernel<256, 8>, groups, 256, st, a)
+                         : tokens <= 1024 * 8 ? launch_threads(kv8_select_kernel<1024, 8>, groups, 1024, st, a)
+                                              : launch_threads(kv8_select_kernel<1024, 24>, groups, 1024, st, a);
     if (e != hipSuccess) return e;
     const uint32_t out_pages = (keep + kPage - 1) / kPage;
     return with_dim(c.dim, [&](auto D) {

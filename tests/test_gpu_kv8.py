@@ -300,6 +300,21 @@ def test_evict(heads, dim, lengths, keep, recent, kind):
     _same_cache(cache, c, "evict leaves the source alone")
 
 
+@pytest.mark.parametrize("lengths,keep,recent", [([2048, 2047], 2000, 3), ([2049, 600], 1000, 100), ([8192, 8000], 100, 0),
+                                                 ([8193, 700], 4096, 1000), ([24577, 24576], 5000, 64), ([40000], 39999, 0)])
+def test_evict_long_caches(lengths, keep, recent):
+    """Lengths around what a workgroup's threads hold of a sequence."""
+    rng = np.random.default_rng(lengths[0])
+    c = ref.make_cache(rng, len(lengths), 1, 64, lengths, -(-max(lengths) // PAGE))
+    d = ref.make_cache(rng, len(lengths), 1, 64, [keep] * len(lengths), -(-keep // PAGE))
+    w = np.round(rng.standard_normal((len(lengths), 1, c["page_table"].shape[1] * PAGE)) * 300).astype(np.float32)
+    into = ref.to_cache(d)
+    kept, moved = qar.qar_kv8_evict(ref.to_cache(c), into, _dev(w), recent, keep)
+    want, wmoved = ref.evict(c, d, w, recent, keep)
+    assert np.array_equal(kept.cpu().numpy(), want) and np.array_equal(moved.cpu().numpy(), wmoved)
+    _same_cache(into, d, "into", [min(n, keep) for n in lengths])
+
+
 def test_evict_leaves_out_pages_that_are_not_there():
     rng = np.random.default_rng(20)
     c = ref.make_cache(rng, 2, 2, 64, [400, 390], 7, absent=[(0, 2), (1, 0)])
