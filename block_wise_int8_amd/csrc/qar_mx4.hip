@@ -796,6 +796,14 @@ hipError_t tiled(LinearArgs& a, hipStream_t st) {
 // 1152 x 1152 6.9 against 7.7, of 3840 x 15360 19.4 against 16.0 to 19.0.
 constexpr size_t kFewRows = 64;
 
+// Tiles of 16 rows that the few-row kernel is built for.  It reads the
+// fragments of all of them, so the workspace holds as many: what lies in those
+// without a row reaches only sums that are not stored.
+uint32_t few_tiles(size_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// Blocks of x in fragments.
+size_t few_fragments(size_t rows, uint32_t padded) { return (size_t)few_tiles(rows) * 16 * padded; }
+
 // One tile of rows of whole blocks is quantized inside the product.
 bool fused(size_t rows, size_t inner) { return rows <= 16 && inner % 32 == 0; }
 
@@ -828,7 +836,7 @@ size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols) {
     const uint32_t blocks = groups_for(inner, 32);
     if (fused(rows, inner)) return 0;
     if (rows <= kFewRows) {
-        const size_t fragments = (rows + 15) / 16 * round_up(blocks, 8) * 16;
+        const size_t fragments = few_fragments(rows, round_up(blocks, 8));
         return align256(fragments * 16) + align256(fragments);
     }
     const size_t padded = round_up(blocks, 8);
@@ -852,14 +860,13 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     a.x_codes = q.codes;
     if (rows <= kFewRows) {
         q.padded = a.padded = round_up(a.blocks, 8);
-        const size_t fragments = (rows + 15) / 16 * a.padded * 16;
-        q.scales = q.codes + align256(fragments * 16);
+        q.scales = q.codes + align256(few_fragments(rows, a.padded) * 16);
         a.x_scales = q.scales;
         const hipError_t e = quantize_call<kFragments>(q, kind, st);
         if (e != hipSuccess) return e;
-        if (rows <= 16)
+        if (few_tiles(rows) == 1)
             return kind == kInBF16 ? few_rows<kInBF16, 1, false>(a, st) : few_rows<kInF32, 1, false>(a, st);
-        if (rows <= 32)
+        if (few_tiles(rows) == 2)
             return kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
         return kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);
     }
