@@ -329,11 +329,10 @@ struct Unit {
     }
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
-    return d;
-}
+// One instruction, which the compiler forms itself: it counts the wait states
+// between a matrix instruction and a vector instruction that reads its result,
+// but not for inline assembly.
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 struct AttendArgs {
     Kv8 c;
