@@ -43,9 +43,17 @@ uint32_t u32(int64_t v) {
     return (uint32_t)v;
 }
 
+// Python's whole numbers and NumPy's.  A truth value is none (as in qar.py), and
+// a tensor would be waited for.
 int64_t whole(PyObject* o) {
-    require(PyLong_Check(o));
-    const int64_t v = PyLong_AsLongLong(o);
+    require(!PyBool_Check(o) && !THPVariable_Check(o));
+    PyObject* n = PyNumber_Index(o);
+    if (!n) {
+        PyErr_Clear();
+        throw Refused{};
+    }
+    const int64_t v = PyLong_AsLongLong(n);
+    Py_DECREF(n);
     if (v == -1 && PyErr_Occurred()) {
         PyErr_Clear();
         throw Refused{};

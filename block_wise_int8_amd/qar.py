@@ -10,6 +10,7 @@ missing library raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import re
 import struct
@@ -679,7 +680,11 @@ def _on_current(index):
 
 
 def _whole(v, what, lo, hi):
-    if isinstance(v, bool) or not isinstance(v, int) or not lo <= v < hi:
+    try:
+        n = None if isinstance(v, (bool, torch.Tensor)) else operator.index(v)
+    except TypeError:
+        n = None
+    if n is None or not lo <= n < hi:
         raise ValueError(f"{what} must be a whole number of at least {lo} and below {hi}, not {v}")
 
 
