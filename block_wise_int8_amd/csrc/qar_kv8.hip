@@ -296,10 +296,11 @@ __global__ __launch_bounds__(kThreads) void kv8_read_kernel(ReadArgs a) {
 // rounding.  A query row enters multiplied by the power of two that brings
 // its largest magnitude into [2^14, 2^15): bfloat16's 8 bits are then exact
 // for all but elements 2^29 times smaller than the row's largest; binary32
-// queries are split in two binary16 terms (22 bits, an error of 2^-23 of an
-// element).  The softmax's numerators enter the second product multiplied by
-// 2^14, in one term (an error of 2^-12 of each, for outputs that are rounded
-// to 2^-9) or, for binary32, two.  Sums, maxima and outputs are binary32.
+// queries are split in two binary16 terms (an error of 2^-23 of an element, or
+// of 2^-39 of the row's largest where that is more).  The softmax's numerators
+// enter the second product multiplied by 2^14, in one term (an error of at most
+// 2^-11 of each, for outputs that are rounded to 2^-8) or, for binary32, two.
+// Sums, maxima and outputs are binary32.
 //
 // A page's value scale enters with the numerators, as its ratio to the largest
 // scale so far (`Unit`), so that the second product adds to the outputs
