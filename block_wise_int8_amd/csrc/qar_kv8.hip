@@ -759,8 +759,8 @@ __global__ __launch_bounds__(kJoinRows * DIM / 4) void kv8_join_kernel(AttendArg
 // codes in registers).
 //
 // Bound by vector and matrix instructions together: for 4 x 1,024 queries x 32
-// heads over 4,096 keys (0.8 PFLOP/s) the matrix units are busy in 39% of the
-// cycles and vector instructions issue in 60%, at 1.9 GHz, to which the chip
+// heads over 4,096 keys (0.8 PFLOP/s) the matrix units are busy in 35% of the
+// cycles and vector instructions issue in 52%, at 2.0 GHz, to which the chip
 // lowers its clock (2.4 GHz) for both.  Causal prompts wait for their longest
 // tiles as well.  Measured and left out, each within 4% or slower: the next
 // page's scores formed beside this page's exponentials, LDS reads 4 to 10

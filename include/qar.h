@@ -433,7 +433,8 @@ qar_status qar_dequantize_int4(const uint8_t* codes, const float* scales, size_t
  *
  * Codes are uint8_t[rows][nb][16] with nb = ceil(cols / 32), the even element
  * in the low nibble; scales are uint8_t[rows][nb].  Scale bytes made elsewhere
- * may be 0 .. 254 (0 is 2^-127).
+ * may be 0 .. 254 (0 is 2^-127).  Elements must be finite, as everywhere: a NaN
+ * or an infinity has no code, and its block's result is unspecified.
  */
 #define QAR_MX4_BLOCK 32
 #define QAR_MX4_MAX_DIM ((size_t)1 << 24) /* of rows and of columns */
@@ -501,8 +502,10 @@ typedef struct qar_kv8_cache {
  * `tokens` new tokens of every sequence enter at positions starts[b] .. of
  * sequence b.  A page that they enter behind older tokens (positions below
  * starts[b]) keeps its scale unless they raise its absmax; then its older
- * values are quantized again with the new scale.  `lengths` is neither read
- * nor written.  Positions behind the table and pages that are not there are
+ * values are quantized again with the new scale.  What the pages that they
+ * enter held behind the last new token is lost: tokens are replaced from
+ * starts[b] to the end, not in the middle.  `lengths` is neither read nor
+ * written.  Positions behind the table and pages that are not there are
  * left out; a negative start leaves the sequence out.
  *   starts        [in] int32[batch].
  *   k_new, v_new  [in] [batch][tokens][kv_heads][dim] of `dtype`, 16-byte aligned.
@@ -525,9 +528,12 @@ qar_status qar_kv8_read(const qar_kv8_cache* cache, const int32_t* starts, uint3
  *   out[b][i][j] = sum over t of p_t v_t,  p = softmax(scale * q . k_t)
  * with key head j / (heads / kv_heads) for query head j.  A row that sees no
  * token gives zeros, and so do rows i >= q_lens[b].  A NaN in a query makes
- * its row NaN and no other.  Scores, maxima, sums and
- * outputs are binary32; the softmax's numerators enter the second product in
- * binary16 (bf16 queries) or as two binary16 terms (binary32 queries).
+ * its row NaN and no other (and the weights of the tokens that the row sees).
+ * Scores, maxima, sums and outputs are binary32; the softmax's numerators enter
+ * the second product in binary16 (bf16 queries: each off by at most 2^-11 of
+ * itself) or as two binary16 terms (binary32 queries: 2^-23).  Each enters times
+ * its page's value scale over the largest value scale; below 2^-28 of the row's
+ * largest numerator that product is off by up to 2^-39 of it instead.
  *   q, out     [batch][queries][heads][dim] of `dtype`, 16-byte aligned;
  *              heads % kv_heads == 0.
  *   q_lens     [in, optional] int32[batch]; NULL: `queries` for all.  Clipped
