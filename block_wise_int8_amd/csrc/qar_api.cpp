@@ -3,6 +3,7 @@
 // Nothing here allocates device memory or synchronizes.
 #include "qar.h"
 
+#include <float.h>
 #include <hip/hip_runtime_api.h>
 
 #include <stdio.h>
@@ -1105,6 +1106,172 @@ qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, 
     const hipError_t e = qar::launch_kv8_evict(kernel_cache(cache), kernel_cache(into), weights, recent, keep, kept, moved,
                                                (hipStream_t)stream);
     return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_evict");
+}
+
+// ---------------------------------------------------------------------------
+// head norms and rotary positions
+
+qar_status qar_norm_rotate(const void* qkv, qar_dtype dtype, size_t batch, size_t tokens, uint32_t heads,
+                           uint32_t kv_heads, uint32_t dim, const int32_t* positions, const float* frequencies,
+                           uint32_t pairs, const void* q_gain, const void* k_gain, float eps, uint32_t flags, void* q,
+                           void* k, void* v, void* stream) {
+    if (batch == 0 || tokens == 0) return QAR_OK;
+    if (dim != 64 && dim != 128 && dim != 256) return QAR_ERR_UNSUPPORTED;
+    if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
+    if (flags & ~(QAR_ROTATE_NORM | QAR_ROTATE_NEIGHBOURS | QAR_ROTATE_EACH_TOKEN)) return QAR_ERR_INVALID_ARG;
+    if (heads == 0 || kv_heads == 0 || heads > (1u << 20) || kv_heads > (1u << 20) || pairs > dim / 2)
+        return QAR_ERR_INVALID_ARG;
+    if (!qkv || !positions || !q || !k || !v || (pairs && !frequencies)) return QAR_ERR_INVALID_ARG;
+    const bool norm = flags & QAR_ROTATE_NORM;
+    if (norm ? !(eps >= 0.0f && eps <= FLT_MAX) : q_gain || k_gain) return QAR_ERR_INVALID_ARG;
+    if (!aligned(qkv, 16) || !aligned(positions, 4) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        (pairs && !aligned(frequencies, 4)) || (q_gain && !aligned(q_gain, 16)) || (k_gain && !aligned(k_gain, 16)))
+        return QAR_ERR_MISALIGNED;
+    const size_t row = ((size_t)heads + 2 * (size_t)kv_heads) * dim;
+    // a workgroup a token, or up to heads / 16 + 1 more where tokens are few
+    if (batch > kMaxGroups / tokens || batch * tokens > kMaxGroups / 2 || batch * tokens > QAR_MAX_ELEMENTS / row)
+        return QAR_ERR_INVALID_ARG;
+    const size_t rows = batch * tokens, size = dtype_bytes(dtype);
+    const Range out[3] = {range(q, rows * heads * dim * size), range(k, rows * kv_heads * dim * size),
+                          range(v, rows * kv_heads * dim * size)};
+    const Range in[5] = {range(qkv, rows * row * size),
+                         range(positions, (flags & QAR_ROTATE_EACH_TOKEN ? rows : batch) * 4),
+                         range(frequencies, pairs * (size_t)4), range(q_gain, q_gain ? dim * size : 0),
+                         range(k_gain, k_gain ? dim * size : 0)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range& r : in)
+            if (r.lo != r.hi && overlap(out[i], r)) return QAR_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return QAR_ERR_INVALID_ARG;
+    }
+    qar::RotateCall c = {};
+    c.x = qkv, c.positions = positions, c.frequencies = frequencies, c.q_gain = q_gain, c.k_gain = k_gain;
+    c.q = q, c.k = k, c.v = v, c.rows = rows, c.tokens = tokens;
+    c.heads = heads, c.kv_heads = kv_heads, c.pairs = pairs, c.eps = eps;
+    c.norm = norm, c.interleaved = flags & QAR_ROTATE_NEIGHBOURS, c.each_token = flags & QAR_ROTATE_EACH_TOKEN;
+    const hipError_t e = qar::launch_norm_rotate(c, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, (int)dim,
+                                                 (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_norm_rotate");
+}
+
+// ---------------------------------------------------------------------------
+// owners of the cache's pages
+
+// A cache whose refs (int32[pages]) a call changes: refs overlap nothing of it,
+// nor do table and lengths, which it may change too, overlap each other or the rest.
+static qar_status check_owned(const qar_kv8_cache* c, const int32_t* refs) {
+    const qar_status st = check_cache(c);
+    if (st != QAR_OK) return st;
+    if (!refs) return QAR_ERR_INVALID_ARG;
+    if (!aligned(refs, 4)) return QAR_ERR_MISALIGNED;
+    if ((size_t)c->batch * c->table_width > kMaxGroups) return QAR_ERR_INVALID_ARG;
+    const CacheRanges held(c);
+    if (held.touches(range(refs, (size_t)c->pages * 4))) return QAR_ERR_INVALID_ARG;
+    for (int i = 4; i < 6; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(held.r[i], held.r[j])) return QAR_ERR_INVALID_ARG;
+    return QAR_OK;
+}
+
+// Lists of int32[count] that a call reads or writes: apart from the cache, its refs and each other.
+static qar_status check_lists(const CacheRanges& held, const qar_kv8_cache* c, const int32_t* refs,
+                              const int32_t* const* lists, const size_t* counts, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!lists[i]) return QAR_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!aligned(lists[i], 4)) return QAR_ERR_MISALIGNED;
+    for (int i = 0; i < n; ++i) {
+        const Range r = range(lists[i], counts[i] * 4);
+        if (held.touches(r) || (refs && overlap(r, range(refs, (size_t)c->pages * 4)))) return QAR_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(r, range(lists[j], counts[j] * 4))) return QAR_ERR_INVALID_ARG;
+    }
+    return QAR_OK;
+}
+
+qar_status qar_kv8_fork(const qar_kv8_cache* cache, int32_t* refs, const int32_t* parents, const qar_kv8_cache* into,
+                        void* stream) {
+    if (into && into->batch == 0) return QAR_OK;
+    qar_status st = check_owned(cache, refs);
+    if (st == QAR_OK) st = check_owned(into, refs);
+    if (st != QAR_OK) return st;
+    if (into->pages != cache->pages || into->kv_heads != cache->kv_heads || into->dim != cache->dim ||
+        into->k != cache->k || into->v != cache->v || into->k_scales != cache->k_scales ||
+        into->v_scales != cache->v_scales || into->table_width < cache->table_width)
+        return QAR_ERR_INVALID_ARG;
+    const CacheRanges from(cache), to(into);
+    const size_t count = into->batch;
+    st = check_lists(to, into, refs, &parents, &count, 1);
+    if (st != QAR_OK) return st;
+    for (int i = 4; i < 6; ++i)
+        if (overlap(to.r[i], from.r[4]) || overlap(to.r[i], from.r[5])) return QAR_ERR_INVALID_ARG;
+    const hipError_t e = qar::launch_kv8_fork(kernel_cache(cache), refs, parents, kernel_cache(into), (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_fork");
+}
+
+qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t* keep, void* stream) {
+    if (cache && cache->batch == 0) return QAR_OK;
+    qar_status st = check_owned(cache, refs);
+    if (st != QAR_OK) return st;
+    const size_t count = cache->batch;
+    if (keep) st = check_lists(CacheRanges(cache), cache, refs, &keep, &count, 1);
+    if (st != QAR_OK) return st;
+    const hipError_t e = qar::launch_kv8_free(kernel_cache(cache), refs, keep, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_free");
+}
+
+qar_status qar_kv8_reserve(const qar_kv8_cache* cache, int32_t* refs, const int32_t* tokens, int32_t* room,
+                           int32_t* source, int32_t* target, void* stream) {
+    static_assert(QAR_KV8_MAX_SEQUENCES == qar::kKv8MaxSequences, "one limit");
+    if (cache && cache->batch == 0) return QAR_OK;
+    qar_status st = check_owned(cache, refs);
+    if (st != QAR_OK) return st;
+    if (cache->batch > QAR_KV8_MAX_SEQUENCES) return QAR_ERR_INVALID_ARG;
+    const int32_t* const lists[4] = {tokens, room, source, target};
+    const size_t counts[4] = {cache->batch, cache->batch, cache->batch, cache->batch};
+    st = check_lists(CacheRanges(cache), cache, refs, lists, counts, 4);
+    if (st != QAR_OK) return st;
+    const hipError_t e =
+        qar::launch_kv8_reserve(kernel_cache(cache), refs, tokens, room, source, target, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_reserve");
+}
+
+qar_status qar_kv8_compact(const qar_kv8_cache* cache, int32_t* refs, int32_t* source, int32_t* target, void* stream) {
+    if (cache && cache->batch == 0) return QAR_OK;
+    qar_status st = check_owned(cache, refs);
+    if (st != QAR_OK) return st;
+    if (cache->pages < 2) return QAR_OK;             // nothing can move
+    const int32_t* const lists[2] = {source, target};
+    const size_t counts[2] = {cache->pages / 2, cache->pages / 2};
+    st = check_lists(CacheRanges(cache), cache, refs, lists, counts, 2);
+    if (st != QAR_OK) return st;
+    const hipError_t e = qar::launch_kv8_compact(kernel_cache(cache), refs, source, target, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_compact");
+}
+
+qar_status qar_kv8_copy(const qar_kv8_cache* cache, const qar_kv8_cache* into, const int32_t* source,
+                        const int32_t* target, uint32_t count, void* stream) {
+    if (count == 0) return QAR_OK;
+    qar_status st = check_cache(cache);
+    if (st == QAR_OK) st = check_cache(into);
+    if (st != QAR_OK) return st;
+    if (cache->kv_heads != into->kv_heads || cache->dim != into->dim || count > (1u << 30) ||
+        (size_t)cache->kv_heads * cache->dim * QAR_KV8_PAGE > ((size_t)1 << 31) - 1)
+        return QAR_ERR_INVALID_ARG;
+    const CacheRanges from(cache), to(into);
+    const int32_t* const lists[2] = {source, target};
+    const size_t counts[2] = {count, count};
+    st = check_lists(to, into, nullptr, lists, counts, 2);
+    if (st != QAR_OK) return st;
+    // one pool, or two apart
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j) {
+            if (i != j && overlap(to.r[i], to.r[j])) return QAR_ERR_INVALID_ARG;
+            if (bad_overlap(to.r[i], from.r[j], i == j)) return QAR_ERR_INVALID_ARG;
+        }
+    const hipError_t e = qar::launch_kv8_copy(kernel_cache(cache), kernel_cache(into), source, target, count,
+                                              (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_copy");
 }
 
 } // extern "C"

@@ -91,6 +91,21 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
                              const uint8_t* scales, size_t cols, void* out, int out_kind, void* workspace,
                              hipStream_t st);
 
+// Head norms and rotary positions (qar_rotate.hip).
+struct RotateCall {
+    const void* x;               // [rows][heads + 2 kv_heads][dim]
+    const int32_t* positions;
+    const float* frequencies;
+    const void *q_gain, *k_gain; // may be null
+    void *q, *k, *v;
+    size_t rows, tokens;         // rows: all tokens of all sequences
+    uint32_t heads, kv_heads, pairs;
+    bool norm, interleaved, each_token;
+    float eps;
+    uint32_t parts;              // workgroups of a token: the launcher's
+};
+hipError_t launch_norm_rotate(RotateCall a, int kind, int dim, hipStream_t st);
+
 // The 8-bit paged cache (qar_kv8.hip).
 struct Kv8 {
     int8_t* k;
@@ -113,5 +128,15 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
                                 hipStream_t st);
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st);
+
+// Owners of the cache's pages (qar_kv8_pages.hip).
+constexpr uint32_t kKv8MaxSequences = 4096;
+hipError_t launch_kv8_fork(const Kv8& c, int32_t* refs, const int32_t* parents, const Kv8& into, hipStream_t st);
+hipError_t launch_kv8_free(const Kv8& c, int32_t* refs, const int32_t* keep, hipStream_t st);
+hipError_t launch_kv8_reserve(const Kv8& c, int32_t* refs, const int32_t* tokens, int32_t* room, int32_t* source,
+                              int32_t* target, hipStream_t st);
+hipError_t launch_kv8_compact(const Kv8& c, int32_t* refs, int32_t* source, int32_t* target, hipStream_t st);
+hipError_t launch_kv8_copy(const Kv8& c, const Kv8& into, const int32_t* source, const int32_t* target, uint32_t count,
+                           hipStream_t st);
 
 } // namespace qar

@@ -140,13 +140,15 @@ PyObject* status(qar_status st) { return PyLong_FromLong(st); }
 
 PyObject* result(qar_status st, const at::Tensor& t) { return st == QAR_OK ? THPVariable_Wrap(t) : status(st); }
 
-PyObject* result(qar_status st, const at::Tensor& a, const at::Tensor& b) {
+template <class... T>
+PyObject* result(qar_status st, const at::Tensor& first, const T&... others) {
     if (st != QAR_OK) return status(st);
-    PyObject* pair = PyTuple_New(2);
-    if (!pair) return nullptr;
-    PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(a));
-    PyTuple_SET_ITEM(pair, 1, THPVariable_Wrap(b));
-    return pair;
+    PyObject* all = PyTuple_New(1 + sizeof...(others));
+    if (!all) return nullptr;
+    Py_ssize_t i = 0;
+    PyTuple_SET_ITEM(all, i++, THPVariable_Wrap(first));
+    (PyTuple_SET_ITEM(all, i++, THPVariable_Wrap(others)), ...);
+    return all;
 }
 
 // ---------------------------------------------------------------------------
@@ -184,6 +186,150 @@ struct Cache {
         c.lengths = (int32_t*)gpu.filled(t[5], at::kInt, c.batch);
     }
 };
+
+// refs of the cache's pages
+int32_t* refs_of(const Gpu& gpu, const qar_kv8_cache& c, PyObject* refs) {
+    return (int32_t*)gpu.shaped(tensor(refs), at::kInt, {c.pages});
+}
+
+// a list of int32 with this many entries, None: a new one
+at::Tensor list_of(const Gpu& gpu, PyObject* given, int64_t count) {
+    if (given == Py_None) return gpu.empty({count}, at::kInt);
+    const at::Tensor& t = tensor(given);
+    gpu.shaped(t, at::kInt, {count});
+    return t;
+}
+
+int32_t* ints(const at::Tensor& t) { return (int32_t*)t.data_ptr(); }
+
+// cache, refs, parents, into
+PyObject* kv8_fork(PyObject* const* a) {
+    Cache cache(a[0]), into(a[3]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    into.fill(gpu);
+    int32_t* refs = refs_of(gpu, cache.c, a[1]);
+    const int32_t* parents = (const int32_t*)gpu.shaped(tensor(a[2]), at::kInt, {into.c.batch});
+    return status(made([&] { return qar_kv8_fork(&cache.c, refs, parents, &into.c, gpu.stream); }));
+}
+
+// cache, refs, keep (or None)
+PyObject* kv8_free(PyObject* const* a) {
+    Cache cache(a[0]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    int32_t* refs = refs_of(gpu, cache.c, a[1]);
+    const int32_t* keep = nullptr;
+    if (a[2] != Py_None) keep = (const int32_t*)gpu.shaped(tensor(a[2]), at::kInt, {cache.c.batch});
+    return status(made([&] { return qar_kv8_free(&cache.c, refs, keep, gpu.stream); }));
+}
+
+// cache, refs, tokens, room, source, target (the last three may be None)
+PyObject* kv8_reserve(PyObject* const* a) {
+    Cache cache(a[0]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    const qar_kv8_cache& c = cache.c;
+    int32_t* refs = refs_of(gpu, c, a[1]);
+    const int32_t* tokens = (const int32_t*)gpu.shaped(tensor(a[2]), at::kInt, {c.batch});
+    const at::Tensor room = list_of(gpu, a[3], c.batch), source = list_of(gpu, a[4], c.batch),
+                     target = list_of(gpu, a[5], c.batch);
+    return result(made([&] {
+                      return qar_kv8_reserve(&c, refs, tokens, ints(room), ints(source), ints(target), gpu.stream);
+                  }),
+                  room, source, target);
+}
+
+// cache, refs, source, target (the last two may be None)
+PyObject* kv8_compact(PyObject* const* a) {
+    Cache cache(a[0]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    const qar_kv8_cache& c = cache.c;
+    int32_t* refs = refs_of(gpu, c, a[1]);
+    const at::Tensor source = list_of(gpu, a[2], c.pages / 2), target = list_of(gpu, a[3], c.pages / 2);
+    return result(made([&] { return qar_kv8_compact(&c, refs, ints(source), ints(target), gpu.stream); }), source, target);
+}
+
+// cache, into, source, target
+PyObject* kv8_copy(PyObject* const* a) {
+    Cache cache(a[0]), into(a[1]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    into.fill(gpu);
+    const at::Tensor &source = tensor(a[2]), &target = tensor(a[3]);
+    require(source.dim() == 1);
+    const uint32_t count = u32(source.size(0));
+    const int32_t *sp = (const int32_t*)gpu.shaped(source, at::kInt, {count}),
+                  *tp = (const int32_t*)gpu.shaped(target, at::kInt, {count});
+    return status(made([&] { return qar_kv8_copy(&cache.c, &into.c, sp, tp, count, gpu.stream); }));
+}
+
+// ---------------------------------------------------------------------------
+// head norms and rotary positions
+
+// qkv, heads, kv_heads, positions, frequencies, q_gain, k_gain, eps, neighbours, out
+// (frequencies, the gains, eps and out, a triple, may be None)
+PyObject* norm_rotate(PyObject* const* a) {
+    const at::Tensor &x = tensor(a[0]), &positions = tensor(a[3]);
+    const Gpu gpu(x);
+    gpu.check(x);
+    require(x.dim() == 4);
+    const at::ScalarType type = x.scalar_type();
+    const qar_dtype code = data_code(type);
+    const uint32_t heads = u32(whole(a[1])), kv_heads = u32(whole(a[2])), dim = u32(x.size(3));
+    const int64_t batch = x.size(0), tokens = x.size(1);
+    require(x.size(2) == (int64_t)heads + 2 * (int64_t)kv_heads);
+    uint32_t flags = 0;
+    gpu.check(positions, at::kInt);
+    if (positions.dim() == 2) {
+        flags |= QAR_ROTATE_EACH_TOKEN;
+        require(positions.size(0) == batch && positions.size(1) == tokens);
+    } else {
+        require(positions.dim() == 1 && positions.size(0) == batch);
+    }
+    const float* frequencies = nullptr;
+    uint32_t pairs = 0;
+    if (a[4] != Py_None) {
+        const at::Tensor& f = tensor(a[4]);
+        require(f.dim() == 1);
+        pairs = u32(f.size(0));
+        frequencies = (const float*)gpu.check(f, at::kFloat).data_ptr();
+    }
+    const void* gains[2] = {nullptr, nullptr};
+    for (int i = 0; i < 2; ++i)
+        if (a[5 + i] != Py_None) gains[i] = gpu.shaped(tensor(a[5 + i]), type, {dim});
+    float eps = 0.0f;
+    if (a[7] != Py_None) {
+        const double given = PyFloat_AsDouble(a[7]);
+        if (given == -1.0 && PyErr_Occurred()) {
+            PyErr_Clear();
+            throw Refused{};
+        }
+        eps = (float)given;
+        flags |= QAR_ROTATE_NORM;
+    }
+    require(PyBool_Check(a[8]));
+    if (a[8] == Py_True) flags |= QAR_ROTATE_NEIGHBOURS;
+    at::Tensor out[3];
+    const int64_t shapes[3] = {heads, kv_heads, kv_heads};
+    require(a[9] == Py_None || (PyTuple_Check(a[9]) && PyTuple_GET_SIZE(a[9]) == 3));
+    for (int i = 0; i < 3; ++i) {
+        const int64_t shape[4] = {batch, tokens, shapes[i], dim};
+        if (a[9] == Py_None)
+            out[i] = gpu.empty(shape, type);
+        else
+            gpu.shaped(out[i] = tensor(PyTuple_GET_ITEM(a[9], i)), type, shape);
+    }
+    const void* xp = x.data_ptr();
+    const int32_t* pp = (const int32_t*)positions.data_ptr();
+    return result(made([&] {
+                      return qar_norm_rotate(xp, code, batch, tokens, heads, kv_heads, dim, pp, frequencies, pairs, gains[0],
+                                             gains[1], eps, flags, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                             gpu.stream);
+                  }),
+                  out[0], out[1], out[2]);
+}
 
 // cache, starts, k_new, v_new
 PyObject* kv8_append(PyObject* const* a) {
@@ -413,7 +559,10 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<kv8_append, 4>("kv8_append"),         method<kv8_read, 5>("kv8_read"),
                          method<kv8_attention, 7>("kv8_attention"),   method<kv8_evict, 7>("kv8_evict"),
                          method<mx4_quantize, 3>("mx4_quantize"),     method<mx4_dequantize, 5>("mx4_dequantize"),
-                         method<mx4_linear, 6>("mx4_linear"),         {nullptr, nullptr, 0, nullptr}};
+                         method<mx4_linear, 6>("mx4_linear"),         method<kv8_fork, 4>("kv8_fork"),
+                         method<kv8_free, 3>("kv8_free"),             method<kv8_reserve, 6>("kv8_reserve"),
+                         method<kv8_compact, 4>("kv8_compact"),       method<kv8_copy, 4>("kv8_copy"),
+                         method<norm_rotate, 10>("norm_rotate"),      {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qar_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -32,6 +32,8 @@ QAR_CHUNK_RUN_ELEMS = 1 << 18
 BLOCK_SIZES = (64, 128, 256)
 QAR_MX4_BLOCK = 32
 QAR_KV8_PAGE = 64
+QAR_KV8_MAX_SEQUENCES = 4096
+QAR_ROTATE_NORM, QAR_ROTATE_NEIGHBOURS, QAR_ROTATE_EACH_TOKEN = 1, 2, 4
 
 _vp, _sz, _u32, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int
 
@@ -69,6 +71,13 @@ _SIGNATURES = {
     "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int, _int],
     "qar_kv8_attention": [_vp, _vp, _int, _u32, _u32, _vp, ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
     "qar_kv8_evict": [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp],
+    "qar_norm_rotate": [_vp, _int, _sz, _sz, _u32, _u32, _u32, _vp, _vp, _u32, _vp, _vp, ctypes.c_float, _u32, _vp, _vp, _vp,
+                        _vp],
+    "qar_kv8_fork": [_vp, _vp, _vp, _vp, _vp],
+    "qar_kv8_free": [_vp, _vp, _vp, _vp],
+    "qar_kv8_reserve": [_vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "qar_kv8_compact": [_vp, _vp, _vp, _vp, _vp],
+    "qar_kv8_copy": [_vp, _vp, _vp, _vp, _u32, _vp],
     "qar_status_string": [_int],
     "qar_last_error": [],
 }
@@ -825,6 +834,13 @@ class KvCache:
                    torch.full((batch, table_width), -1, dtype=torch.int32, device=device),
                    torch.zeros(batch, dtype=torch.int32, device=device))
 
+    def forked(self, batch: int, table_width: int | None = None) -> "KvCache":
+        """The same pool with a table and lengths of its own for ``batch`` sequences (not set: what
+        qar_kv8_fork writes), as wide as this one's unless said otherwise."""
+        width = self.page_table.shape[1] if table_width is None else table_width
+        new = self.page_table.new_empty
+        return KvCache(self.k, self.k_scales, self.v, self.v_scales, new((batch, width)), new((batch,)))
+
     def _struct(self, what="cache"):
         """(the C struct as bytes, for calls of lib() itself, GPU index, batch, kv_heads, dim, table_width)"""
         k, v, ks, vs, table, lengths = self.k, self.v, self.k_scales, self.v_scales, self.page_table, self.lengths
@@ -974,3 +990,172 @@ def _why_kv8_evict(cache, into, weights, recent, keep, kept, moved):
         _shaped(moved, "moved", shape, _F32, dev)
     _on_current(index)
     raise ValueError("qar_kv8_evict: the arguments do not fit")
+
+
+# ----------------------------------------------------------------------------
+# serving: owners of the cache's pages
+
+
+def qar_kv8_fork(cache: KvCache, refs: torch.Tensor, parents: torch.Tensor, into: KvCache, stream=None) -> None:
+    """Sequence b of ``into`` (the same pool, see KvCache.forked) goes on from sequence parents[b]
+    (int32[into's batch]) of ``cache`` and shares its pages, whose owners refs (int32[pages]) counts;
+    a parent outside the batch gives an empty sequence."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_fork(cache, refs, parents, into)
+    made = _serve().kv8_fork(cache, refs, parents, into)
+    return _done(made, "qar_kv8_fork") if made is not None else _why_kv8_fork(cache, refs, parents, into)
+
+
+def _why_owned(cache, refs):
+    _, index, batch, _, _, _ = cache._struct()
+    _shaped(refs, "refs", (cache.k.shape[0],), _INT32, cache.k.device)
+    return index, batch, cache.k.device
+
+
+def _why_kv8_fork(cache, refs, parents, into):
+    index, _, dev = _why_owned(cache, refs)
+    _, other, batch, _, _, _ = into._struct("into")
+    if other != index:
+        raise ValueError(f"into is on {into.k.device}, cache on {dev}")
+    _shaped(parents, "parents", (batch,), _INT32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_fork: the arguments do not fit")
+
+
+def qar_kv8_free(cache: KvCache, refs: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> None:
+    """Every sequence is cut to its first keep[b] (int32[batch]; default: no) tokens; the pages behind them are released."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_free(cache, refs, keep)
+    made = _serve().kv8_free(cache, refs, keep)
+    return _done(made, "qar_kv8_free") if made is not None else _why_kv8_free(cache, refs, keep)
+
+
+def _why_kv8_free(cache, refs, keep):
+    index, batch, dev = _why_owned(cache, refs)
+    if keep is not None:
+        _shaped(keep, "keep", (batch,), _INT32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_free: the arguments do not fit")
+
+
+def qar_kv8_reserve(cache: KvCache, refs: torch.Tensor, tokens: torch.Tensor, room: torch.Tensor | None = None,
+                    source: torch.Tensor | None = None, target: torch.Tensor | None = None, stream=None):
+    """Pages for tokens[b] (int32[batch]) more tokens of every sequence -> (room int32[batch]: for how many
+    there is room now; source, target int32[batch]: pages that qar_kv8_copy has to copy before they are written, or -1)."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_reserve(cache, refs, tokens, room, source, target)
+    made = _serve().kv8_reserve(cache, refs, tokens, room, source, target)
+    if made is not None:
+        return _done(made, "qar_kv8_reserve")
+    return _why_kv8_reserve(cache, refs, tokens, room, source, target)
+
+
+def _why_kv8_reserve(cache, refs, tokens, room, source, target):
+    index, batch, dev = _why_owned(cache, refs)
+    _shaped(tokens, "tokens", (batch,), _INT32, dev)
+    for t, what in ((room, "room"), (source, "source"), (target, "target")):
+        if t is not None:
+            _shaped(t, what, (batch,), _INT32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_reserve: the arguments do not fit")
+
+
+def qar_kv8_compact(cache: KvCache, refs: torch.Tensor, source: torch.Tensor | None = None,
+                    target: torch.Tensor | None = None, stream=None):
+    """The pages in use get the pool's lowest numbers -> (source, target int32[pages // 2]: the moves that
+    qar_kv8_copy has to make, -1 behind them)."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_compact(cache, refs, source, target)
+    made = _serve().kv8_compact(cache, refs, source, target)
+    return _done(made, "qar_kv8_compact") if made is not None else _why_kv8_compact(cache, refs, source, target)
+
+
+def _why_kv8_compact(cache, refs, source, target):
+    index, _, dev = _why_owned(cache, refs)
+    for t, what in ((source, "source"), (target, "target")):
+        if t is not None:
+            _shaped(t, what, (cache.k.shape[0] // 2,), _INT32, dev)
+    _on_current(index)
+    raise ValueError("qar_kv8_compact: the arguments do not fit")
+
+
+def qar_kv8_copy(cache: KvCache, source: torch.Tensor, target: torch.Tensor, into: KvCache | None = None,
+                 stream=None) -> None:
+    """Page target[i] of ``into`` (default: ``cache``) becomes page source[i] of ``cache``, for every i where both
+    (int32) are pages of their pools."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_copy(cache, source, target, into)
+    if into is None:
+        into = cache
+    made = _serve().kv8_copy(cache, into, source, target)
+    return _done(made, "qar_kv8_copy") if made is not None else _why_kv8_copy(cache, into, source, target)
+
+
+def _why_kv8_copy(cache, into, source, target):
+    index = cache._struct()[1]
+    if into._struct("into")[1] != index:
+        raise ValueError(f"into is on {into.k.device}, cache on {cache.k.device}")
+    if _dev(source, "source").dim() != 1:
+        raise ValueError(f"source must have 1 dimension, not {source.dim()}")
+    _shaped(source, "source", tuple(source.shape), _INT32, cache.k.device)
+    _shaped(target, "target", tuple(source.shape), _INT32, cache.k.device)
+    _on_current(index)
+    raise ValueError("qar_kv8_copy: the arguments do not fit")
+
+
+# ----------------------------------------------------------------------------
+# serving: head norms and rotary positions
+
+
+def qar_norm_rotate(qkv: torch.Tensor, heads: int, kv_heads: int, positions: torch.Tensor,
+                    frequencies: torch.Tensor | None = None, q_gain: torch.Tensor | None = None,
+                    k_gain: torch.Tensor | None = None, eps: float | None = None, interleaved: bool = False,
+                    out: tuple | None = None, stream=None):
+    """qkv [batch, tokens, heads + 2 * kv_heads, dim] (bf16/fp32) -> (q, k, v), each [batch, tokens, its heads, dim].
+    Queries and keys are divided by the root of their mean square + ``eps`` and multiplied by their gain [dim]
+    (where ``eps`` is given), then rotated by position * frequencies (fp32[pairs]): the pairs are channels j and
+    j + pairs, or 2 j and 2 j + 1 where ``interleaved``.  ``positions`` int32[batch] are the first tokens',
+    int32[batch, tokens] every token's.  ``out`` = (q, k, v) receives them instead of new tensors."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_norm_rotate(qkv, heads, kv_heads, positions, frequencies, q_gain, k_gain, eps, interleaved, out)
+    if out is not None:
+        out = tuple(out)
+    made = _serve().norm_rotate(qkv, heads, kv_heads, positions, frequencies, q_gain, k_gain, eps, interleaved, out)
+    if made is not None:
+        return _done(made, "qar_norm_rotate")
+    return _why_norm_rotate(qkv, heads, kv_heads, positions, frequencies, q_gain, k_gain, eps, interleaved, out)
+
+
+def _why_norm_rotate(qkv, heads, kv_heads, positions, frequencies, q_gain, k_gain, eps, interleaved, out):
+    _whole(heads, "heads", 1, 1 << 32)
+    _whole(kv_heads, "kv_heads", 1, 1 << 32)
+    if _dev(qkv, "qkv").dim() != 4 or qkv.shape[2] != heads + 2 * kv_heads:
+        raise ValueError(f"qkv must be [batch, tokens, {heads + 2 * kv_heads}, dim], not {list(qkv.shape)}")
+    _dtype_code(qkv.dtype)
+    (batch, tokens, _, dim), dev = qkv.shape, qkv.device
+    each = isinstance(positions, torch.Tensor) and positions.dim() == 2
+    _shaped(positions, "positions", (batch, tokens) if each else (batch,), _INT32, dev)
+    if frequencies is not None:
+        if _dev(frequencies, "frequencies").dim() != 1:
+            raise ValueError(f"frequencies must have 1 dimension, not {frequencies.dim()}")
+        _shaped(frequencies, "frequencies", tuple(frequencies.shape), _F32, dev)
+    for t, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+        if t is not None:
+            _shaped(t, what, (dim,), (qkv.dtype,), dev)
+    if eps is not None:
+        float(eps)
+    if not isinstance(interleaved, bool):
+        raise TypeError(f"interleaved must be True or False, not {interleaved}")
+    if out is not None:
+        if len(out) != 3:
+            raise ValueError(f"out must be (q, k, v), not {len(out)} tensors")
+        for t, what, n in zip(out, ("out[0]", "out[1]", "out[2]"), (heads, kv_heads, kv_heads)):
+            _shaped(t, what, (batch, tokens, n, dim), (qkv.dtype,), dev)
+    _on_current(qkv.get_device())
+    raise ValueError("qar_norm_rotate: the arguments do not fit")

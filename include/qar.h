@@ -570,6 +570,97 @@ qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtyp
 qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, const float* weights,
                          uint32_t recent, uint32_t keep, int32_t* kept, float* moved, void* stream);
 
+/*
+ * Head norms and rotary positions ("rotate").  The joint projection of a
+ * layer's hidden states holds the queries of `heads` heads, then the keys and
+ * then the values of kv_heads heads each.  Queries and keys are normed head by
+ * head and rotated by their position, values are copied:
+ *   y = x / sqrt(mean(x^2) + eps) * gain      (QAR_ROTATE_NORM; gain where one is passed)
+ *   (y_a, y_b) -> (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position * frequencies[j]
+ * for pair j = 0 .. pairs - 1 of a head's channels: (j, j + pairs), or (2 j,
+ * 2 j + 1) with QAR_ROTATE_NEIGHBOURS; channels from 2 * pairs on are not
+ * rotated.  The angle is formed and reduced in 64 bits, the rest is binary32,
+ * each result is rounded once.  A NaN or an overflowing sum of squares in a
+ * head stays in that head.
+ *   qkv        [in]  [batch][tokens][heads + 2 kv_heads][dim] of `dtype`, 16-byte aligned.
+ *   positions  [in]  int32[batch], each sequence's first token's (the i-th has
+ *                    i more), or int32[batch][tokens] with QAR_ROTATE_EACH_TOKEN.
+ *   frequencies  [in]  float[pairs], radians a position; 0 <= pairs <= dim / 2 (NULL where 0).
+ *   q_gain, k_gain  [in, optional]  [dim] of `dtype`, 16-byte aligned; only with QAR_ROTATE_NORM.
+ *   q, k, v    [out] [batch][tokens][heads or kv_heads][dim] of `dtype`, 16-byte aligned.
+ * dim is 64, 128 or 256; eps is finite and at least 0 (a head of zeros gives
+ * zeros where it is more).
+ */
+#define QAR_ROTATE_NORM 1u
+#define QAR_ROTATE_NEIGHBOURS 2u
+#define QAR_ROTATE_EACH_TOKEN 4u
+
+qar_status qar_norm_rotate(const void* qkv, qar_dtype dtype, size_t batch, size_t tokens, uint32_t heads,
+                           uint32_t kv_heads, uint32_t dim, const int32_t* positions, const float* frequencies,
+                           uint32_t pairs, const void* q_gain, const void* k_gain, float eps, uint32_t flags, void* q,
+                           void* k, void* v, void* stream);
+
+/*
+ * Owners of the cache's pages.  refs[p] (int32[cache->pages], the caller's)
+ * counts the entries of all page tables that name page p; a page whose count is
+ * not above 0 is free.  Sequences may share the pages of tokens that they have
+ * in common; a page is written only by a sequence that owns it alone.  All is
+ * done on the device (nothing is read back, calls can be captured), and every
+ * result is that of serving the sequences in order, so equal calls give equal
+ * tables.  Entries outside the pool are pages that are not there, as everywhere.
+ * Caches of several layers whose page tables are the same take one call for the
+ * table, and one qar_kv8_copy for each layer.
+ *
+ * fork: sequence b of `into` goes on from sequence parents[b] of `cache`: its
+ * length, and the same pages up to it (their counts grow); no entries behind.
+ * A parent outside 0 .. cache->batch - 1 gives an empty sequence.  The pool is
+ * one (k, v and scales are not used); into's table and lengths are overwritten,
+ * without anything being released.
+ *   parents  [in] int32[into->batch].   into->table_width >= cache->table_width.
+ */
+qar_status qar_kv8_fork(const qar_kv8_cache* cache, int32_t* refs, const int32_t* parents, const qar_kv8_cache* into,
+                        void* stream);
+/*
+ * free: every sequence is cut to its first min(lengths[b], max(keep[b], 0))
+ * tokens (to none where keep is NULL).  Pages wholly behind them, those given
+ * ahead among them, are released and their entries become -1.
+ */
+qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t* keep, void* stream);
+/*
+ * reserve: pages for tokens[b] more tokens of every sequence.  Sequences are
+ * served in order.  One that goes on in a partly filled page with other owners
+ * gets a page in its place: source[b] and target[b] are then the two, whose
+ * content the caller copies (qar_kv8_copy) before it appends; otherwise both
+ * are -1.  Behind its last page every page up to lengths[b] + tokens[b] that is
+ * not there is given.  Pages are taken lowest free number first.  When none is
+ * left a sequence keeps what it got.  lengths are not changed.
+ *   tokens   [in]  int32[batch]; below 1 counts as none.
+ *   room     [out] int32[batch]: for how many tokens there is room now, at most
+ *                  tokens[b]; 0 for one whose shared or missing page could not be
+ *                  replaced (a partly filled page that is not there is not).
+ *   source, target  [out] int32[batch].
+ * batch <= QAR_KV8_MAX_SEQUENCES.
+ */
+#define QAR_KV8_MAX_SEQUENCES 4096
+qar_status qar_kv8_reserve(const qar_kv8_cache* cache, int32_t* refs, const int32_t* tokens, int32_t* room,
+                           int32_t* source, int32_t* target, void* stream);
+/*
+ * compact: with L pages in use, those from number L on change places with free
+ * ones below L, the lowest with the lowest.  refs and the cache's table follow;
+ * what other tables name is found in the lists.  The caller copies the pages
+ * (qar_kv8_copy), and may then give the pool from page L on to others.
+ *   source, target  [out] int32[pages / 2]: the moves, -1 behind them.
+ */
+qar_status qar_kv8_compact(const qar_kv8_cache* cache, int32_t* refs, int32_t* source, int32_t* target, void* stream);
+/*
+ * copy: page target[i] of `into` becomes page source[i] of `cache`, all heads,
+ * keys and values with their scales, for every i whose two pages are there.  The
+ * two may be one pool, or pools of equal kv_heads and dim.  A target may appear
+ * once, and not as a source.  Tables and lengths are not used.
+ */
+qar_status qar_kv8_copy(const qar_kv8_cache* cache, const qar_kv8_cache* into, const int32_t* source,
+                        const int32_t* target, uint32_t count, void* stream);
+
 /* Static text for a status code. */
 const char* qar_status_string(qar_status status);
 
