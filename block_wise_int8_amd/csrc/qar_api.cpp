@@ -899,9 +899,10 @@ size_t qar_mx4_linear_workspace_bytes(size_t rows, size_t inner, size_t cols) {
     return qar::mx4_linear_workspace(rows, inner, cols);
 }
 
-qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
-                          const uint8_t* scales, size_t cols, void* out, qar_dtype out_dtype, void* workspace,
-                          size_t workspace_bytes, void* stream) {
+static qar_status mx4_linear_call(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                                  const uint8_t* scales, size_t cols, const qar::Epilogue& epilogue, void* out,
+                                  qar_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream,
+                                  const char* where) {
     if (rows == 0 || cols == 0) return QAR_OK;
     if (inner == 0) return QAR_ERR_INVALID_ARG;
     if (mx4_sizes(rows, inner) != QAR_OK || mx4_sizes(cols, inner) != QAR_OK || mx4_sizes(rows, cols) != QAR_OK)
@@ -909,19 +910,46 @@ qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t in
     if (!x || !codes || !scales || !out) return QAR_ERR_INVALID_ARG;
     if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return QAR_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(out, 16)) return QAR_ERR_MISALIGNED;
+    if ((epilogue.bias && !aligned(epilogue.bias, 16)) || (epilogue.residual && !aligned(epilogue.residual, 16)))
+        return QAR_ERR_MISALIGNED;
     const size_t need = qar::mx4_linear_workspace(rows, inner, cols);
     if (need && (!workspace || workspace_bytes < need)) return QAR_ERR_INVALID_ARG;
     if (need && !aligned(workspace, 256)) return QAR_ERR_MISALIGNED;
-    const size_t nb = cols * mx4_blocks(inner);
-    const Range in[3] = {range(x, rows * inner * dtype_bytes(dtype)), range(codes, nb * 16), range(scales, nb)};
-    const Range oo = range(out, rows * cols * dtype_bytes(out_dtype)), wo = range(workspace, need);
-    for (const Range& r : in)
-        if (overlap(oo, r) || (need && overlap(wo, r))) return QAR_ERR_INVALID_ARG;
+    const size_t nb = cols * mx4_blocks(inner), out_size = dtype_bytes(out_dtype);
+    const Range oo = range(out, rows * cols * out_size), wo = range(workspace, need);
+    const Range in[5] = {range(x, rows * inner * dtype_bytes(dtype)), range(codes, nb * 16), range(scales, nb),
+                         range(epilogue.bias, epilogue.bias ? cols * out_size : 0),
+                         range(epilogue.residual, epilogue.residual ? rows * cols * out_size : 0)};
+    for (int i = 0; i < 5; ++i) {
+        if (in[i].lo == in[i].hi) continue;
+        // the residual may be replaced by the result
+        if (bad_overlap(oo, in[i], i == 4) || (need && overlap(wo, in[i]))) return QAR_ERR_INVALID_ARG;
+    }
     if (need && overlap(wo, oo)) return QAR_ERR_INVALID_ARG;
     const hipError_t e = qar::launch_mx4_linear(
-        x, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, rows, inner, codes, scales, cols, out,
+        x, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, rows, inner, codes, scales, cols, epilogue, out,
         out_dtype == QAR_BF16 ? qar::kOutBF16 : qar::kOutF32, workspace, (hipStream_t)stream);
-    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_mx4_linear");
+    return e == hipSuccess ? QAR_OK : hip_fail(e, where);
+}
+
+qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                          const uint8_t* scales, size_t cols, void* out, qar_dtype out_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    return mx4_linear_call(x, dtype, rows, inner, codes, scales, cols, qar::Epilogue{}, out, out_dtype, workspace,
+                           workspace_bytes, stream, "qar_mx4_linear");
+}
+
+qar_status qar_mx4_linear_fused(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                                const uint8_t* scales, size_t cols, const void* bias, qar_activation activation,
+                                const void* residual, void* out, qar_dtype out_dtype, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    static_assert((int)QAR_ACT_RELU == (int)qar::kActRelu && (int)QAR_ACT_SILU == (int)qar::kActSilu &&
+                      (int)QAR_ACT_GELU == (int)qar::kActGelu && (int)QAR_ACT_GELU_TANH == (int)qar::kActGeluTanh,
+                  "one numbering");
+    if (rows && cols && (activation < QAR_ACT_NONE || activation > QAR_ACT_GELU_TANH)) return QAR_ERR_UNSUPPORTED;
+    const qar::Epilogue epilogue = {bias, activation, residual};
+    return mx4_linear_call(x, dtype, rows, inner, codes, scales, cols, epilogue, out, out_dtype, workspace,
+                           workspace_bytes, stream, "qar_mx4_linear_fused");
 }
 
 // ---------------------------------------------------------------------------

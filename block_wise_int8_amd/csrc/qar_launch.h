@@ -87,9 +87,15 @@ hipError_t launch_mx4_quantize(const void* x, int kind, size_t rows, size_t cols
 hipError_t launch_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, size_t rows, size_t cols, void* out,
                                  int kind, hipStream_t st);
 size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols);
+enum : int { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct Epilogue {
+    const void* bias = nullptr;      // [cols] of out's type
+    int activation = kActNone;
+    const void* residual = nullptr;  // like out
+};
 hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner, const uint8_t* codes,
-                             const uint8_t* scales, size_t cols, void* out, int out_kind, void* workspace,
-                             hipStream_t st);
+                             const uint8_t* scales, size_t cols, const Epilogue& epilogue, void* out, int out_kind,
+                             void* workspace, hipStream_t st);
 
 // Head norms and rotary positions (qar_rotate.hip).
 struct RotateCall {

@@ -334,6 +334,114 @@ __global__ __launch_bounds__(kThreads) void mx4_dequantize_kernel(const uint8_t*
 }
 
 // ---------------------------------------------------------------------------
+// activations.  EXACT: for binary32 results, to a few units of 2^-24; otherwise
+// for results that are rounded to bf16's 2^-9, to 2^-16.
+
+// e^(x + low), low far below x (to 2^-22, or 2^-16 for |x| < 90)
+template <bool EXACT>
+__device__ __forceinline__ float exp_of(float x, float low = 0.0f) {
+    constexpr float kLog2E = 1.44269504088896340736f;
+    const float t = x * kLog2E, e = __builtin_amdgcn_exp2f(t);
+    if constexpr (!EXACT) return e;
+    // the product's rounding, and what log2 e is more than its binary32 value
+    const float rest = __builtin_fmaf(x, 1.92596299112661746887e-8f, __builtin_fmaf(x, kLog2E, -t));
+    return e > 0.0f && e < INFINITY ? __builtin_fmaf(e, __builtin_fmaf(rest, 0.693147180559945309f, low), e) : e;
+}
+
+// -2 sqrt(2 / pi) (v + 0.044715 v^3).  An exponent of 80 has to be known to 2^-28
+// of itself: with EXACT every rounding and the constants' own go into `low`.
+template <bool EXACT>
+__device__ __forceinline__ float tanh_exponent(float v, float& low) {
+    constexpr double k1 = -1.59576912160573071176, k3 = k1 * 0.044715;
+    constexpr float c1 = (float)k1, c3 = (float)k3;
+    const float square = v * v;
+    if constexpr (!EXACT) return v * __builtin_fmaf(c3, square, c1);
+    const float cube = c3 * square, p = cube + c1, back = p - c1;
+    const float lost = __builtin_fmaf(c3, square, -cube) + c3 * __builtin_fmaf(v, v, -square) + (float)(k3 - c3) * square +
+                       (float)(k1 - c1) + ((cube - back) + (c1 - (p - back)));
+    const float u = v * p;
+    low = __builtin_fmaf(v, lost, __builtin_fmaf(v, p, -u));
+    return u;
+}
+
+// Half the complementary error function of a / sqrt 2, a >= 0: e^(-a^2 / 2)
+// times t Q(t), t = 1 / (1 + k a).  Q was fitted to the scaled function for the
+// smallest relative error over 0 .. 14 (2^-24.9, or 2^-16.9); behind that the
+// exponential leaves nothing.
+template <bool EXACT>
+__device__ __forceinline__ float half_erfc(float a) {
+    const float square = a * a;
+    float t, q, e;
+    if constexpr (EXACT) {
+        constexpr float c[9] = {0.139621407f, 0.139861897f, 0.119832717f, 0.105508596f, -0.0231112316f,
+                                0.159176186f, -0.255716026f, 0.143972546f, -0.0291461032f};
+        t = 1.0f / __builtin_fmaf(0.35f, a, 1.0f);
+        q = c[8];
+#pragma unroll
+        for (int i = 7; i >= 0; --i) q = __builtin_fmaf(q, t, c[i]);
+        e = exp_of<true>(-0.5f * square, -0.5f * __builtin_fmaf(a, a, -square));
+    } else {
+        constexpr float c[6] = {0.120074235f, 0.11374189f, 0.14419657f, -0.0169485137f, 0.216037527f,
+                                -0.0770976022f};
+        t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
+        q = c[5];
+#pragma unroll
+        for (int i = 4; i >= 0; --i) q = __builtin_fmaf(q, t, c[i]);
+        e = exp_of<false>(-0.5f * square);
+    }
+    return e * (t * q);
+}
+
+// N elements of a row from column `col` as binary32, zeros behind its end.
+template <int N, class T>
+__device__ __forceinline__ void row_values(const T* x, size_t row_at, size_t col, size_t cols, float (&y)[N]) {
+    const T* p = x + row_at + col;
+    T w[N] = {};
+    if (col + N <= cols)
+        __builtin_memcpy(w, p, sizeof w);
+    else
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (col + k < cols) w[k] = p[k];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        if constexpr (sizeof(T) == 2)
+            y[k] = bf16_lo(w[k]);
+        else
+            y[k] = w[k];
+    }
+}
+
+// The activation of N values: which one is decided once for all.
+template <bool EXACT, int N>
+__device__ __forceinline__ void activate(float (&y)[N], int activation) {
+    const auto over = [](float n, float d) { return EXACT ? n / d : n * __builtin_amdgcn_rcpf(d); };
+    const auto all = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = f(y[i]);
+    };
+    switch (activation) {
+    case kActRelu: all([](float v) { return v < 0.0f ? 0.0f : v; }); break;
+    case kActSilu: all([&](float v) { return over(v, 1.0f + exp_of<EXACT>(-v)); }); break;
+    case kActGelu:
+        all([](float v) {
+            const float h = half_erfc<EXACT>(fabsf(v));
+            return v < 0.0f ? v * h : __builtin_fmaf(v, -h, v);
+        });
+        break;
+    case kActGeluTanh:
+        // (1 + tanh u) / 2 = 1 / (1 + e^(-2 u))
+        all([&](float v) {
+            float low = 0.0f;
+            const float u = tanh_exponent<EXACT>(v, low);
+            return over(v, 1.0f + exp_of<EXACT>(u, low));
+        });
+        break;
+    default: break;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the product, few rows of x: out[r][c] = sum over k of x[r][k] w[c][k].
 //
 // Bound by reading the weights, so these go from memory to registers once and
@@ -356,6 +464,8 @@ struct LinearArgs {
     uint32_t padded;
     uint32_t row_tiles, col_tiles;     // of the tiled product
     int out_kind;
+    const void *bias, *residual;       // of out's type, may be null
+    int activation;
 };
 
 __device__ __forceinline__ mx_i32x8 operand(uint4 q) {
@@ -411,7 +521,7 @@ struct RowsOfX {
     }
 };
 
-template <int IN, int MT, int CT, int NW, bool FUSED>
+template <int IN, int MT, int CT, int NW, bool FUSED, bool EPILOGUE>
 __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
     static_assert(!FUSED || MT == 1, "rows of one tile");
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
@@ -514,6 +624,24 @@ __global__ __launch_bounds__(NW * 64) void mx4_few_rows_kernel(LinearArgs a) {
         const size_t row = m * 16 + row16, col = c0 + quad * 4;
         if (row >= a.rows) continue;
         const size_t at = row * a.cols + col;
+        if constexpr (EPILOGUE) {
+            float v[4] = {y[0], y[1], y[2], y[3]}, bias[4] = {}, add[4] = {};
+            if (a.out_kind == kOutBF16) {
+                if (a.bias) row_values<4>((const uint16_t*)a.bias, 0, col, a.cols, bias);
+                if (a.residual) row_values<4>((const uint16_t*)a.residual, row * a.cols, col, a.cols, add);
+            } else {
+                if (a.bias) row_values<4>((const float*)a.bias, 0, col, a.cols, bias);
+                if (a.residual) row_values<4>((const float*)a.residual, row * a.cols, col, a.cols, add);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] += bias[k];
+            if (a.out_kind == kOutBF16)
+                activate<false>(v, a.activation);
+            else
+                activate<true>(v, a.activation);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = v[k] + add[k];
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (col + k >= a.cols) break;
@@ -568,7 +696,7 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
-template <int OUT, int BM, int BN, int WM, int WN>
+template <int OUT, int BM, int BN, int WM, int WN, bool EPILOGUE>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(LinearArgs a) {
     static_assert(BM == BN, "one size of buffer");
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
@@ -712,13 +840,22 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     // time, so that a store writes whole lines: eight lanes a row of 128 bytes
     // (straight from the registers a store touches 32 rows with 32 bytes each).
     // 16-byte slot c of row r lies at c ^ (r % 8) of its group of eight.
+    // With an epilogue they pass as binary32: bias, activation and residual come
+    // on the way out, where a lane's columns are the same for all of its rows and
+    // the residual is read in whole lines, and the result is rounded once.
     using T = std::conditional_t<OUT == kOutBF16, uint16_t, float>;
+    using S = std::conditional_t<EPILOGUE, float, T>;
     // A buffer to a wave, or half of one: all are read out, and none is being written.
-    constexpr int ROW = WN * sizeof(T), SHARE = NT / 64 > 4 ? 2 : 1, STRIP = BM * 128 / SHARE;
+    constexpr int ROW = WN * sizeof(S), SHARE = NT / 64 > 4 ? 2 : 1, STRIP = BM * 128 / SHARE;
     constexpr int NOW = std::min(STRIP / (32 * ROW), TM);
     static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
+    constexpr int N = 16 / sizeof(T), PER = WN / N;  // columns of a lane, lanes to a row
     const uint32_t home = wave / SHARE;
     char* strip = reinterpret_cast<char*>(home == 0 ? s0 : home == 1 ? s1 : home == 2 ? s2 : s3) + wave % SHARE * STRIP;
+    const size_t col = n0 + wn * WN + lane % PER * N;
+    [[maybe_unused]] float bias[N] = {};
+    if constexpr (EPILOGUE)
+        if (a.bias) row_values<N>((const T*)a.bias, 0, col, a.cols, bias);
 #pragma unroll
     for (int i0 = 0; i0 < TM; i0 += NOW) {
 #pragma unroll
@@ -727,23 +864,58 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t row = i * 32 + fr, at = (j * 32 + 8 * q + 4 * half) * sizeof(T);
+                    const uint32_t row = i * 32 + fr, at = (j * 32 + 8 * q + 4 * half) * sizeof(S);
                     char* to = strip + row * ROW + (at & ~127u) + ((at / 16 % 8 ^ row % 8) * 16) + at % 16;
                     const float y0 = acc[i0 + i][j][4 * q], y1 = acc[i0 + i][j][4 * q + 1], y2 = acc[i0 + i][j][4 * q + 2],
                                 y3 = acc[i0 + i][j][4 * q + 3];
-                    if constexpr (OUT == kOutBF16)
+                    if constexpr (sizeof(S) == 2)
                         *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(y0, y1), pack_bf16x2(y2, y3));
                     else
                         *reinterpret_cast<mx_f32x4*>(to) = mx_f32x4{y0, y1, y2, y3};
                 }
         __builtin_amdgcn_wave_barrier();
-        constexpr int PER = ROW / 16;               // lanes to a row
+        constexpr int STORES = NOW * 32 * PER / 64, AT_ONCE = EPILOGUE ? 4 : STORES;
+#pragma unroll 1
+        for (int k0 = 0; k0 < STORES; k0 += AT_ONCE) {
+            // an epilogue's reads of the residual are under way together
+            [[maybe_unused]] float add[EPILOGUE ? AT_ONCE : 1][N] = {};
+            if constexpr (EPILOGUE)
+                if (a.residual)
 #pragma unroll
-        for (int k = 0; k < NOW * 32 * PER / 64; ++k) {
-            const uint32_t row = k * (64 / PER) + lane / PER, c = lane % PER;
-            const uint4 v = *reinterpret_cast<const uint4*>(strip + row * ROW + (c & ~7u) * 16 + ((c % 8 ^ row % 8) * 16));
-            const size_t r = m0 + wm * WM + i0 * 32 + row;
-            if (r < a.rows) store_row<16 / sizeof(T)>((T*)a.out, r * a.cols, n0 + wn * WN + c * (16 / sizeof(T)), a.cols, v);
+                    for (int k = 0; k < AT_ONCE; ++k) {
+                        const size_t r = m0 + wm * WM + i0 * 32 + (k0 + k) * (64 / PER) + lane / PER;
+                        if (r < a.rows) row_values<N>((const T*)a.residual, r * a.cols, col, a.cols, add[k]);
+                    }
+#pragma unroll
+            for (int k = 0; k < AT_ONCE; ++k) {
+                const uint32_t row = (k0 + k) * (64 / PER) + lane / PER;
+                const size_t r = m0 + wm * WM + i0 * 32 + row;
+                const auto slot = [&](uint32_t c) {
+                    return *reinterpret_cast<const uint4*>(strip + row * ROW + (c & ~7u) * 16 + ((c % 8 ^ row % 8) * 16));
+                };
+                uint4 v;
+                if constexpr (!EPILOGUE) {
+                    v = slot(lane % PER);
+                } else {
+                    float y[N];
+#pragma unroll
+                    for (int e = 0; e < N; e += 4) {
+                        const uint4 w = slot((lane % PER * N + e) / 4);
+                        y[e] = __builtin_bit_cast(float, w.x) + bias[e], y[e + 1] = __builtin_bit_cast(float, w.y) + bias[e + 1];
+                        y[e + 2] = __builtin_bit_cast(float, w.z) + bias[e + 2], y[e + 3] = __builtin_bit_cast(float, w.w) + bias[e + 3];
+                    }
+                    activate<sizeof(T) == 4>(y, a.activation);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) y[e] += add[k][e];
+                    if constexpr (sizeof(T) == 2)
+                        v = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                       pack_bf16x2(y[6], y[7]));
+                    else
+                        v = make_uint4(__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1]),
+                                       __builtin_bit_cast(uint32_t, y[2]), __builtin_bit_cast(uint32_t, y[3]));
+                }
+                if (r < a.rows) store_row<N>((T*)a.out, r * a.cols, col, a.cols, v);
+            }
         }
         __builtin_amdgcn_wave_barrier();
     }
@@ -776,19 +948,20 @@ hipError_t quantize_call(QuantizeArgs a, int kind, hipStream_t st) {
 // [32, 5376] x [5376, 5376] 12.5 against 14.2, [50, 8000] x [8000, 2880] 17.6
 // against 13.7.  Four tiles and four or sixteen waves were slower than the
 // better of these everywhere but once (2%).
-template <int IN, int MT, bool FUSED>
+template <int IN, int MT, bool FUSED, bool EPILOGUE>
 hipError_t few_rows(const LinearArgs& a, hipStream_t st) {
     constexpr int NW = 8;
     if (groups_for(a.cols, 32) >= (MT == 1 ? 256u : 160u))
-        return launch_threads(mx4_few_rows_kernel<IN, MT, 2, NW, FUSED>, groups_for(a.cols, 32), NW * 64, st, a);
-    return launch_threads(mx4_few_rows_kernel<IN, MT, 1, NW, FUSED>, groups_for(a.cols, 16), NW * 64, st, a);
+        return launch_threads(mx4_few_rows_kernel<IN, MT, 2, NW, FUSED, EPILOGUE>, groups_for(a.cols, 32), NW * 64, st, a);
+    return launch_threads(mx4_few_rows_kernel<IN, MT, 1, NW, FUSED, EPILOGUE>, groups_for(a.cols, 16), NW * 64, st, a);
 }
 
-template <int IN, int BM, int BN, int WM, int WN>
+template <int IN, int BM, int BN, int WM, int WN, bool EPILOGUE>
 hipError_t tiled(LinearArgs& a, hipStream_t st) {
     a.row_tiles = groups_for(a.rows, BM);
     a.col_tiles = groups_for(a.cols, BN);
-    return launch_threads(mx4_tiled_kernel<IN, BM, BN, WM, WN>, a.row_tiles * a.col_tiles, (BM / WM) * (BN / WN) * 64, st, a);
+    return launch_threads(mx4_tiled_kernel<IN, BM, BN, WM, WN, EPILOGUE>, a.row_tiles * a.col_tiles,
+                          (BM / WM) * (BN / WN) * 64, st, a);
 }
 
 // The few-row kernel, which reads x again for every 16 or 32 columns, against
@@ -844,18 +1017,17 @@ size_t mx4_linear_workspace(size_t rows, size_t inner, size_t cols) {
            align256((cols + 255) / 256 * 256 * padded);
 }
 
-hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner, const uint8_t* codes, const uint8_t* scales,
-                             size_t cols, void* out, int out_kind, void* workspace, hipStream_t st) {
-    LinearArgs a = {};
-    a.x = x, a.codes = codes, a.scales = scales, a.out = out, a.out_kind = out_kind;
-    a.rows = rows, a.inner = inner, a.cols = cols;
-    a.blocks = groups_for(inner, 32);
+namespace {
+
+template <bool EPILOGUE>
+hipError_t linear(LinearArgs a, int kind, const uint8_t* w_scales, void* workspace, hipStream_t st) {
+    const size_t rows = a.rows, inner = a.inner, cols = a.cols;
     if (fused(rows, inner)) {
         a.padded = round_up(a.blocks, 8);
-        return kind == kInBF16 ? few_rows<kInBF16, 1, true>(a, st) : few_rows<kInF32, 1, true>(a, st);
+        return kind == kInBF16 ? few_rows<kInBF16, 1, true, EPILOGUE>(a, st) : few_rows<kInF32, 1, true, EPILOGUE>(a, st);
     }
     QuantizeArgs q = {};
-    q.x = x, q.rows = rows, q.cols = inner, q.blocks = a.blocks;
+    q.x = a.x, q.rows = rows, q.cols = inner, q.blocks = a.blocks;
     q.codes = (uint8_t*)workspace;
     a.x_codes = q.codes;
     if (rows <= kFewRows) {
@@ -864,16 +1036,15 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
         a.x_scales = q.scales;
         const hipError_t e = quantize_call<kFragments>(q, kind, st);
         if (e != hipSuccess) return e;
-        if (few_tiles(rows) == 1)
-            return kind == kInBF16 ? few_rows<kInBF16, 1, false>(a, st) : few_rows<kInF32, 1, false>(a, st);
-        if (few_tiles(rows) == 2)
-            return kind == kInBF16 ? few_rows<kInBF16, 2, false>(a, st) : few_rows<kInF32, 2, false>(a, st);
-        return kind == kInBF16 ? few_rows<kInBF16, 4, false>(a, st) : few_rows<kInF32, 4, false>(a, st);
+        // fragments are the same for both types of x: one kernel serves them
+        if (few_tiles(rows) == 1) return few_rows<kInBF16, 1, false, EPILOGUE>(a, st);
+        if (few_tiles(rows) == 2) return few_rows<kInBF16, 2, false, EPILOGUE>(a, st);
+        return few_rows<kInBF16, 4, false, EPILOGUE>(a, st);
     }
     q.padded = a.padded = round_up(a.blocks, 8);
     q.scales = q.codes + align256(rows * q.padded * 16);
     q.w_tiles = q.scales + align256((rows + 255) / 256 * 256 * (size_t)q.padded);
-    q.w_scales = scales;
+    q.w_scales = w_scales;
     q.w_rows = cols;
     a.x_scales = q.scales;
     a.w_tiles = q.w_tiles;
@@ -886,11 +1057,24 @@ hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner,
     const auto tiles = [&](size_t size) { return (size_t)groups_for(rows, size) * groups_for(cols, size); };
     const auto go = [&](auto OUT) {
         constexpr int out = decltype(OUT)::value;
-        if (tiles(256) >= 256) return tiled<out, 256, 256, 128, 64>(a, st);
-        if (tiles(128) >= 256) return tiled<out, 128, 128, 64, 64>(a, st);
-        return tiled<out, 64, 64, 32, 64>(a, st);
+        if (tiles(256) >= 256) return tiled<out, 256, 256, 128, 64, EPILOGUE>(a, st);
+        if (tiles(128) >= 256) return tiled<out, 128, 128, 64, 64, EPILOGUE>(a, st);
+        return tiled<out, 64, 64, 32, 64, EPILOGUE>(a, st);
     };
-    return out_kind == kOutBF16 ? go(std::integral_constant<int, kOutBF16>{}) : go(std::integral_constant<int, kOutF32>{});
+    return a.out_kind == kOutBF16 ? go(std::integral_constant<int, kOutBF16>{}) : go(std::integral_constant<int, kOutF32>{});
+}
+
+} // namespace
+
+hipError_t launch_mx4_linear(const void* x, int kind, size_t rows, size_t inner, const uint8_t* codes, const uint8_t* scales,
+                             size_t cols, const Epilogue& epilogue, void* out, int out_kind, void* workspace, hipStream_t st) {
+    LinearArgs a = {};
+    a.x = x, a.codes = codes, a.scales = scales, a.out = out, a.out_kind = out_kind;
+    a.rows = rows, a.inner = inner, a.cols = cols;
+    a.blocks = groups_for(inner, 32);
+    a.bias = epilogue.bias, a.residual = epilogue.residual, a.activation = epilogue.activation;
+    return a.bias || a.residual || a.activation != kActNone ? linear<true>(a, kind, scales, workspace, st)
+                                                            : linear<false>(a, kind, scales, workspace, st);
 }
 
 } // namespace qar

@@ -502,33 +502,63 @@ PyObject* mx4_dequantize(PyObject* const* a) {
     return result(made([&] { return qar_mx4_dequantize(m.codes, m.scales, rows, cols, op, code, gpu.stream); }), out);
 }
 
+// A product's tensors; the call is made by the two functions below.
+struct Linear {
+    const at::Tensor &x, &c;
+    const Gpu gpu;
+    int64_t rows, inner, cols;
+    qar_dtype code, out_code;
+    at::Tensor out;
+    Linear(PyObject* x_, PyObject* c_, PyObject* out_, PyObject* out_dtype) : x(tensor(x_)), c(tensor(c_)), gpu(x) {
+        gpu.check(x);
+        require(x.dim() == 2 && c.dim() == 2);
+        rows = x.size(0), inner = x.size(1), cols = c.size(0);
+        code = data_code(x.scalar_type());
+        if (out_ == Py_None) {
+            const at::ScalarType type = out_dtype == Py_None ? x.scalar_type() : dtype_of(out_dtype);
+            data_code(type);
+            out = gpu.empty({rows, cols}, type);
+        } else {
+            out = tensor(out_);
+            gpu.filled(out, out.scalar_type(), rows * cols);
+        }
+        out_code = data_code(out.scalar_type());
+    }
+};
+
 // x, codes, scales, out, out_dtype, workspace (the last three may be None)
 PyObject* mx4_linear(PyObject* const* a) {
-    const at::Tensor &x = tensor(a[0]), &c = tensor(a[1]);
-    const Gpu gpu(x);
-    gpu.check(x);
-    require(x.dim() == 2 && c.dim() == 2);
-    const int64_t rows = x.size(0), inner = x.size(1), cols = c.size(0);
-    const qar_dtype code = data_code(x.scalar_type());
-    const Mx4 m(gpu, c, a[2], mx4_blocks(inner));
-    at::Tensor out;
-    if (a[3] == Py_None) {
-        const at::ScalarType type = a[4] == Py_None ? x.scalar_type() : dtype_of(a[4]);
-        data_code(type);
-        out = gpu.empty({rows, cols}, type);
-    } else {
-        out = tensor(a[3]);
-        gpu.filled(out, out.scalar_type(), rows * cols);
-    }
-    const qar_dtype out_code = data_code(out.scalar_type());
-    const Workspace ws(gpu, a[5], qar_mx4_linear_workspace_bytes(rows, inner, cols));
-    const void* xp = x.data_ptr();
-    void* op = out.data_ptr();
+    const Linear l(a[0], a[1], a[3], a[4]);
+    const Mx4 m(l.gpu, l.c, a[2], mx4_blocks(l.inner));
+    const Workspace ws(l.gpu, a[5], qar_mx4_linear_workspace_bytes(l.rows, l.inner, l.cols));
+    const void* xp = l.x.data_ptr();
+    void* op = l.out.data_ptr();
     return result(made([&] {
-                      return qar_mx4_linear(xp, code, rows, inner, m.codes, m.scales, cols, op, out_code, ws.data, ws.bytes,
-                                            gpu.stream);
+                      return qar_mx4_linear(xp, l.code, l.rows, l.inner, m.codes, m.scales, l.cols, op, l.out_code, ws.data,
+                                            ws.bytes, l.gpu.stream);
                   }),
-                  out);
+                  l.out);
+}
+
+// x, codes, scales, bias, activation, residual, out, out_dtype, workspace (bias, residual and the last three may be None)
+PyObject* mx4_linear_fused(PyObject* const* a) {
+    const Linear l(a[0], a[1], a[6], a[7]);
+    const Mx4 m(l.gpu, l.c, a[2], mx4_blocks(l.inner));
+    const at::ScalarType type = l.out.scalar_type();
+    const void *bias = nullptr, *residual = nullptr;
+    if (a[3] != Py_None) bias = l.gpu.shaped(tensor(a[3]), type, {l.cols});
+    if (a[5] != Py_None) residual = l.gpu.filled(tensor(a[5]), type, l.rows * l.cols);
+    const int64_t activation = whole(a[4]);
+    require(activation >= 0 && activation <= INT32_MAX);
+    const Workspace ws(l.gpu, a[8], qar_mx4_linear_workspace_bytes(l.rows, l.inner, l.cols));
+    const void* xp = l.x.data_ptr();
+    void* op = l.out.data_ptr();
+    return result(made([&] {
+                      return qar_mx4_linear_fused(xp, l.code, l.rows, l.inner, m.codes, m.scales, l.cols, bias,
+                                                  (qar_activation)activation, residual, op, l.out_code, ws.data, ws.bytes,
+                                                  l.gpu.stream);
+                  }),
+                  l.out);
 }
 
 // ---------------------------------------------------------------------------
@@ -562,7 +592,8 @@ PyMethodDef methods[] = {method<kv8_append, 4>("kv8_append"),         method<kv8
                          method<mx4_linear, 6>("mx4_linear"),         method<kv8_fork, 4>("kv8_fork"),
                          method<kv8_free, 3>("kv8_free"),             method<kv8_reserve, 6>("kv8_reserve"),
                          method<kv8_compact, 4>("kv8_compact"),       method<kv8_copy, 4>("kv8_copy"),
-                         method<norm_rotate, 10>("norm_rotate"),      {nullptr, nullptr, 0, nullptr}};
+                         method<norm_rotate, 10>("norm_rotate"),      method<mx4_linear_fused, 9>("mx4_linear_fused"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qar_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

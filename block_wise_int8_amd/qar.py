@@ -33,6 +33,7 @@ BLOCK_SIZES = (64, 128, 256)
 QAR_MX4_BLOCK = 32
 QAR_KV8_PAGE = 64
 QAR_KV8_MAX_SEQUENCES = 4096
+QAR_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 QAR_ROTATE_NORM, QAR_ROTATE_NEIGHBOURS, QAR_ROTATE_EACH_TOKEN = 1, 2, 4
 
 _vp, _sz, _u32, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_uint32, ctypes.c_int
@@ -66,6 +67,7 @@ _SIGNATURES = {
     "qar_mx4_dequantize": [_vp, _vp, _sz, _sz, _vp, _int, _vp],
     "qar_mx4_linear_workspace_bytes": [_sz, _sz, _sz],
     "qar_mx4_linear": [_vp, _int, _sz, _sz, _vp, _vp, _sz, _vp, _int, _vp, _sz, _vp],
+    "qar_mx4_linear_fused": [_vp, _int, _sz, _sz, _vp, _vp, _sz, _vp, _int, _vp, _vp, _int, _vp, _sz, _vp],
     "qar_kv8_append": [_vp, _vp, _vp, _vp, _int, _u32, _vp],
     "qar_kv8_read": [_vp, _vp, _u32, _vp, _vp, _int, _vp],
     "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int, _int],
@@ -787,7 +789,7 @@ def qar_mx4_linear(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, o
     return _why_mx4_linear(x, codes, scales, out, out_dtype, workspace)
 
 
-def _why_mx4_linear(x, codes, scales, out, out_dtype, workspace):
+def _why_mx4_linear(x, codes, scales, out, out_dtype, workspace, where="qar_mx4_linear"):
     rows, inner = _matrix(x, "x").shape
     cols = _matrix(codes, "codes").shape[0]
     _dev(scales, "scales")
@@ -796,7 +798,37 @@ def _why_mx4_linear(x, codes, scales, out, out_dtype, workspace):
     _why_out(out, out_dtype, rows * cols, x.device)
     _why_workspace(workspace, x.device)
     _on_current(x.get_device())
-    raise ValueError("qar_mx4_linear: the arguments do not fit")
+    raise ValueError(f"{where}: the arguments do not fit")
+
+
+def qar_mx4_linear_fused(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, bias: torch.Tensor | None = None,
+                         activation: str | None = None, residual: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """residual + activation(the product of qar_mx4_linear + bias) -> out [rows, cols], rounded once.  ``bias`` [cols]
+    and ``residual`` [rows, cols] are of out's type; ``activation`` is None, "relu", "silu", "gelu" or "gelu_tanh";
+    ``out`` may be the residual itself."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_mx4_linear_fused(x, codes, scales, bias, activation, residual, out, out_dtype, workspace)
+    number = QAR_ACTIVATIONS.get(activation) if activation is None or isinstance(activation, str) else None
+    made = _serve().mx4_linear_fused(x, codes, scales, bias, number, residual, out, out_dtype, workspace)
+    if made is not None:
+        return _done(made, "qar_mx4_linear_fused")
+    return _why_mx4_linear_fused(x, codes, scales, bias, activation, residual, out, out_dtype, workspace)
+
+
+def _why_mx4_linear_fused(x, codes, scales, bias, activation, residual, out, out_dtype, workspace):
+    if activation is not None and not (isinstance(activation, str) and activation in QAR_ACTIVATIONS):
+        raise ValueError(f"activation must be one of {', '.join(map(str, QAR_ACTIVATIONS))}, not {activation}")
+    if isinstance(x, torch.Tensor) and isinstance(codes, torch.Tensor) and x.dim() == codes.dim() == 2:
+        numel = x.shape[0] * codes.shape[0]
+        dtype = out.dtype if isinstance(out, torch.Tensor) else x.dtype if out_dtype is None else out_dtype
+        if bias is not None:
+            _shaped(bias, "bias", (codes.shape[0],), (dtype,), x.device)
+        if residual is not None:
+            _expect(residual, "residual", numel, (dtype,), x.device)
+    _why_mx4_linear(x, codes, scales, out, out_dtype, workspace, "qar_mx4_linear_fused")
 
 
 def _why_workspace(workspace, device):

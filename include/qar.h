@@ -471,6 +471,32 @@ qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t in
                           size_t workspace_bytes, void* stream);
 
 /*
+ * The same product with an epilogue:
+ *   out[r][c] = residual[r][c] + activation(sum + bias[c])
+ * where sum is the one above, all in binary32, the result rounded once.
+ *   bias       [in, optional] cols elements of out_dtype, 16-byte aligned.
+ *   activation  y -> y, max(y, 0), y / (1 + e^-y), y (1 + erf(y / sqrt 2)) / 2, or
+ *              y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2; each to 2^-16
+ *              of itself where the result is bf16, else to 2^-21 (below 2^-119
+ *              it may be 0).
+ *   residual   [in, optional] rows * cols elements of out_dtype, 16-byte
+ *              aligned; may be `out` itself.
+ *   workspace  that of qar_mx4_linear.
+ */
+typedef enum qar_activation QAR_ENUM_BASE {
+    QAR_ACT_NONE = 0,
+    QAR_ACT_RELU = 1,
+    QAR_ACT_SILU = 2,
+    QAR_ACT_GELU = 3,
+    QAR_ACT_GELU_TANH = 4
+} qar_activation;
+
+qar_status qar_mx4_linear_fused(const void* x, qar_dtype dtype, size_t rows, size_t inner, const uint8_t* codes,
+                                const uint8_t* scales, size_t cols, const void* bias, qar_activation activation,
+                                const void* residual, void* out, qar_dtype out_dtype, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/*
  * The paged cache of keys and values held in 8 bits ("kv8").  A pool of
  * `pages` pages of QAR_KV8_PAGE tokens; page p holds, for each of kv_heads
  * heads, the keys' int8 codes [token][dim], the values' [dim][token], and a

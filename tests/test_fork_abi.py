@@ -196,3 +196,48 @@ def test_forked_tables():
     f = c.forked(5)
     assert f.k is c.k and f.v_scales is c.v_scales and f.page_table.shape == (5, 3) and f.lengths.shape == (5,)
     assert c.forked(1, 9).page_table.shape == (1, 9) and f.page_table.dtype == I32
+
+
+# ---------------------------------------------------------------------------
+# the product with an epilogue
+
+
+def test_mx4_linear_fused_refusals(L):
+    good = dict(x=M, dtype=0, rows=4, inner=96, codes=2 * M, scales=3 * M, cols=50, bias=5 * M, activation=1, residual=6 * M,
+                out=4 * M, out_dtype=0, ws=None, size=0)
+
+    def call(**kw):
+        return L.qar_mx4_linear_fused(*{**good, **kw}.values(), None)
+    assert call(rows=0) == OK and call(cols=0) == OK and call(inner=0) == INV
+    for name in ("x", "codes", "scales", "out"):
+        assert call(**{name: None}) == INV, name
+    assert call(dtype=2) == UNS and call(out_dtype=7) == UNS and call(activation=5) == UNS and call(activation=-1) == UNS
+    for name in ("x", "codes", "bias", "residual", "out"):
+        assert call(**{name: 7 * M + 8}) == MIS, name
+    assert call(out=2 * M) == INV and call(out=5 * M + 80) == INV and call(bias=4 * M + 384) == INV
+    assert call(residual=4 * M + 16) == INV and call(residual=4 * M - 16) == INV         # the output only as a whole
+    need = L.qar_mx4_linear_workspace_bytes(40, 96, 50)
+    assert call(rows=40) == INV and call(rows=40, ws=8 * M, size=need - 1) == INV
+    for at in (4 * M, 5 * M, 6 * M, M):
+        assert call(rows=40, ws=at, size=need) == INV
+    assert call(rows=1 << 21, inner=1 << 20) == INV
+
+
+def test_mx4_linear_fused_arguments():
+    u8 = torch.uint8
+    x, codes, scales = _t(2, 32), _t(5, 16, dtype=u8), _t(5, 1, dtype=u8)
+    cases = [
+        (dict(bias=_t(4)), ValueError, "bias must be"), (dict(bias=_t(5, dtype=BF)), TypeError, "bias must be torch.float32"),
+        (dict(bias=_t(5), out_dtype=BF), TypeError, "bias must be torch.bfloat16"),
+        (dict(residual=_t(2, 4)), ValueError, "residual must hold 10"),
+        (dict(residual=_t(2, 5), out=_t(2, 5, dtype=BF)), TypeError, "residual must be torch.bfloat16"),
+        (dict(activation="tanh"), ValueError, "activation must be"), (dict(activation=1), ValueError, "activation must be"),
+        (dict(out=_t(2, 4)), ValueError, "out must hold 10"), (dict(out_dtype=torch.float16), TypeError, "bfloat16 and float32")]
+    for i, (kw, error, text) in enumerate(cases):
+        with pytest.raises(error, match=text):
+            qar.qar_mx4_linear_fused(x, codes, scales, **kw)
+            pytest.fail(f"case {i} was not refused")
+    ext = qar._serve()
+    assert ext.mx4_linear_fused(*[None] * 9) is None
+    with pytest.raises(TypeError, match="9 arguments"):
+        ext.mx4_linear_fused(None)
