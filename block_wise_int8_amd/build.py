@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libqar.so")
 EXTENSION = os.path.join(HERE, "_qar_torch.so")
-SOURCES = [os.path.join(CSRC, name) for name in ("qar_kernels.hip", "qar_kv8.hip", "qar_kv8_pages.hip", "qar_mx4.hip",
-                                               "qar_rotate.hip", "qar_api.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in ("qar_kernels.hip", "qar_kv8.hip", "qar_kv8_pages.hip", "qar_kv8_shared.hip",
+                                               "qar_mx4.hip", "qar_rotate.hip", "qar_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -1137,6 +1137,51 @@ qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, 
 }
 
 // ---------------------------------------------------------------------------
+// attention behind prefixes that sequences share
+
+size_t qar_kv8_attention_shared_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
+                                                uint32_t dim, uint32_t table_width, uint32_t groups) {
+    if (batch == 0 || queries == 0 || table_width == 0 || groups == 0 || groups > batch ||
+        (dim != 64 && dim != 128 && dim != 256) || !kv8_rows_ok(batch, queries, heads, kv_heads, table_width))
+        return 0;
+    return qar::kv8_shared_workspace(batch, kv_heads, queries * (heads / kv_heads), (int)dim, table_width, groups);
+}
+
+qar_status qar_kv8_attention_shared(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
+                                    uint32_t heads, const int32_t* starts, const int32_t* prefix, uint32_t groups,
+                                    const int32_t* q_lens, float scale, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+    if (cache && (cache->batch == 0 || queries == 0)) return QAR_OK;
+    const qar_status st = check_cache(cache);
+    if (st != QAR_OK) return st;
+    if (!q || !out || !starts || !prefix || groups == 0 || groups > cache->batch ||
+        !kv8_rows_ok(cache->batch, queries, heads, cache->kv_heads, cache->table_width))
+        return QAR_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(starts, 4) || !aligned(prefix, 4) || (q_lens && !aligned(q_lens, 4)))
+        return QAR_ERR_MISALIGNED;
+    const size_t need = qar::kv8_shared_workspace(cache->batch, cache->kv_heads, queries * (heads / cache->kv_heads),
+                                                  (int)cache->dim, cache->table_width, groups);
+    if (!workspace || workspace_bytes < need) return QAR_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return QAR_ERR_MISALIGNED;
+    const size_t bytes = (size_t)cache->batch * queries * heads * cache->dim * dtype_bytes(dtype);
+    const CacheRanges held(cache);
+    const Range w[2] = {range(out, bytes), range(workspace, need)};
+    const Range in[4] = {range(q, bytes), range(starts, (size_t)(groups + 1) * 4), range(prefix, (size_t)groups * 4),
+                         range(q_lens, q_lens ? (size_t)cache->batch * 4 : 0)};
+    if (overlap(w[0], w[1])) return QAR_ERR_INVALID_ARG;
+    for (const Range& x : w) {
+        if (held.touches(x)) return QAR_ERR_INVALID_ARG;
+        for (const Range& r : in)
+            if (r.lo != r.hi && overlap(x, r)) return QAR_ERR_INVALID_ARG;
+    }
+    const hipError_t e =
+        qar::launch_kv8_shared(kernel_cache(cache), q, dtype == QAR_BF16 ? qar::kInBF16 : qar::kInF32, queries, heads, starts,
+                               prefix, groups, q_lens, scale, out, workspace, (hipStream_t)stream);
+    return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_attention_shared");
+}
+
+// ---------------------------------------------------------------------------
 // head norms and rotary positions
 
 qar_status qar_norm_rotate(const void* qkv, qar_dtype dtype, size_t batch, size_t tokens, uint32_t heads,

@@ -1,0 +1,678 @@
+// qar_kv8_shared.hip -- attention over the 8-bit cache for sequences whose
+// first tokens are the same pages, on gfx950.
+//
+// A softmax over a prefix and over a sequence's own tokens is joined from the
+// two parts' maxima, sums and outputs.  So the prefix is attended to once for
+// all: the queries of a group's sequences (with the heads that share a key
+// head) are the rows of one product, and a page of the prefix is read, and its
+// codes converted, once for all rows of a tile instead of once for each
+// sequence.  The own tokens are attended to sequence by sequence.  Either is
+// cut into slots of pages, whose lengths are found on the device from the
+// prefix and the sequence's length, and the slots of a row are joined last.
+#include <float.h>
+#include <hip/hip_runtime.h>
+
+#include "qar_kv8_device.h"
+
+namespace qar {
+namespace {
+
+struct SharedArgs {
+    Kv8 c;
+    const void* q;
+    const int32_t *starts, *prefix;     // [groups + 1], [groups]
+    const int32_t* q_lens;              // may be null: every sequence has `queries`
+    void* out;
+    float *part, *stats;                // [row][slot][dim], [row][slot]: maximum and sum
+    uint32_t queries, heads, group, rows, groups;
+    uint32_t prefix_tiles, own_tiles;   // of rows: of all groups, of a sequence
+    uint32_t prefix_slots, own_slots;
+    float scale;                        // of the scores, times log2(e), without its sign
+    bool negative;                      // its sign, which the queries take
+};
+
+// ---------------------------------------------------------------------------
+// which rows and pages
+
+__device__ __forceinline__ uint32_t start_of(const SharedArgs& a, uint32_t g) {
+    return (uint32_t)clamp_length(a.starts[g], a.c.batch);
+}
+
+// How many of `count` ascending things f(i) are at most `top`; a wave looks at
+// 64 at once.
+template <class F>
+__device__ __forceinline__ uint32_t count_up_to(uint32_t count, uint32_t top, F f) {
+    const uint32_t lane = threadIdx.x % 64;
+    uint32_t n = 0;
+    for (uint32_t base = 0; base < count; base += 64) {
+        const uint64_t mask = __ballot(base + lane < count && f(min(base + lane, count - 1)) <= top);
+        n += (uint32_t)__builtin_popcountll(mask);
+        if (~mask) break;
+    }
+    return n;
+}
+
+// Pages that group g's sequences have in common.
+__device__ __forceinline__ uint32_t prefix_pages(const SharedArgs& a, uint32_t g) {
+    return (uint32_t)clamp_length(a.prefix[g], a.c.width * kPage) / kPage;
+}
+
+// Pages before sequence b's own.
+__device__ __forceinline__ uint32_t pages_before(const SharedArgs& a, uint32_t b) {
+    const uint32_t n = count_up_to(a.groups, b, [&](uint32_t g) { return start_of(a, g); });
+    if (n == 0) return 0;
+    const uint32_t end = start_of(a, n), pages = prefix_pages(a, n - 1);
+    return b < end ? pages : 0;
+}
+
+// `pages` cut into at most `slots` slots.
+struct Cut {
+    uint32_t per, used;
+    __device__ __forceinline__ Cut(uint32_t pages, uint32_t slots) {
+        per = max((pages + slots - 1) / slots, 4u);          // a page for each of a workgroup's waves
+        used = (pages + per - 1) / per;
+    }
+};
+
+// A sequence's numbers.
+struct Seq {
+    int32_t n, m;
+    __device__ __forceinline__ Seq(const SharedArgs& a, uint32_t b)
+        : n(clamp_length(a.c.lengths[b], a.c.width * kPage)),
+          m(a.q_lens ? clamp_length(a.q_lens[b], a.queries) : (int32_t)a.queries) {}
+};
+
+// What a workgroup does: a tile of rows of one key head, a slot of pages.  Row
+// r is row r % a.rows of sequence first_seq + r / a.rows; that is its query
+// r / a.group with head r % a.group of the key head's group.
+struct Work {
+    uint32_t head, slot, first_seq, first_row, row_count;
+    uint32_t first, last;                // pages
+    bool any;
+    __device__ __forceinline__ Work(const SharedArgs& a, uint32_t unit, uint32_t tile_rows) {
+        const uint32_t prefix_units = a.prefix_tiles * a.c.heads * a.prefix_slots;
+        any = false;
+        if (unit < prefix_units) {
+            slot = unit % a.prefix_slots;
+            head = unit / a.prefix_slots % a.c.heads;
+            // group g's tiles begin at g plus the whole tiles of all rows before it: room for a last, partial tile of each
+            const uint32_t tile = unit / a.prefix_slots / a.c.heads;
+            const auto first_tile = [&](uint32_t g) { return (uint32_t)((uint64_t)start_of(a, g) * a.rows / tile_rows) + g; };
+            const uint32_t g = count_up_to(a.groups, tile, first_tile) - 1;   // the first group's begin at or before tile 0 ...
+            if (g >= a.groups) return;                                        // ... if no sequences are before it
+            first_seq = start_of(a, g);
+            const uint32_t end = start_of(a, g + 1), pages = prefix_pages(a, g);
+            row_count = end > first_seq ? (end - first_seq) * a.rows : 0;
+            first_row = (tile - first_tile(g)) * tile_rows;
+            const Cut cut(pages, a.prefix_slots);
+            first = slot * cut.per;
+            last = min(first + cut.per, pages);
+            any = first_row < row_count && first < last;
+        } else {
+            unit -= prefix_units;
+            const uint32_t of_slot = unit % a.own_slots, rest = unit / a.own_slots;
+            slot = a.prefix_slots + of_slot;
+            head = rest % a.c.heads;
+            first_seq = rest / a.c.heads % a.c.batch;
+            first_row = (a.own_tiles - 1 - rest / a.c.heads / a.c.batch) * tile_rows;   // the longest first
+            row_count = a.rows;
+            const uint32_t before = pages_before(a, first_seq);
+            const uint32_t pages = (uint32_t)(clamp_length(a.c.lengths[first_seq], a.c.width * kPage) + kPage - 1) / kPage;
+            const Cut cut(pages > before ? pages - before : 0, a.own_slots);
+            first = before + of_slot * cut.per;
+            last = min(first + cut.per, pages);
+            any = first < last;
+        }
+    }
+};
+
+// A row of the queries, and of the parts.
+struct Row {
+    bool there;
+    int32_t limit;                       // it sees the keys below
+    size_t query, item;
+    __device__ __forceinline__ Row(const SharedArgs& a, const Work& w, uint32_t r) {
+        there = r < w.row_count;
+        const uint32_t safe = there ? r : 0, b = w.first_seq + safe / a.rows, mine = safe % a.rows;
+        const Seq seq(a, b);
+        const int32_t i = (int32_t)(mine / a.group);
+        there = there && i < seq.m;
+        limit = seq.n - seq.m + i + 1;
+        query = ((size_t)b * a.queries + i) * a.heads + w.head * a.group + mine % a.group;
+        item = ((size_t)b * a.c.heads + w.head) * a.rows + mine;
+    }
+};
+
+// The smallest and the largest over each 16 lanes.
+__device__ __forceinline__ int32_t lanes16_min(int32_t v) {
+#pragma unroll
+    for (int d = 8; d; d /= 2) v = min(v, __shfl_xor(v, d));
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// few rows: a wave takes a page at a time, from memory to registers (the
+// layout of kv8_attend_few_kernel, qar_kv8.hip).
+
+template <int DIM, int MT, int IN, int NW>
+__global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_shared_few_kernel(SharedArgs a, uint32_t first_unit) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    constexpr int KC = DIM / 64, VC = DIM / 16;
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
+    const Work work(a, first_unit + blockIdx.x, 16 * MT);
+    if (!work.any) return;
+    const uint32_t h = work.head, first = work.first, last = work.last;
+    int32_t my_id;
+    float my_ks, my_vs;
+    auto look_up = [&](uint32_t page) {
+        my_id = -1, my_ks = my_vs = 0.0f;
+        if (page < last) {
+            my_id = valid_page(a.c.table[(size_t)work.first_seq * a.c.width + page], a.c.pages);
+            if (my_id >= 0) {
+                my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
+                my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
+            }
+        }
+    };
+    look_up(first + wave + lane * NW);
+
+    Query<IN, DIM, 16, 64> raw[MT];
+    int32_t limit[MT], all_see = INT32_MAX;                  // every row sees the keys below
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const Row row(a, work, work.first_row + i * 16 + r);
+        raw[i].load(a.q, row.there ? row.query : 0, g * 16, row.there);
+        limit[i] = row.there ? row.limit : INT32_MAX;        // rows that are not there are not stored
+        all_see = min(all_see, lanes16_min(limit[i]));
+    }
+    all_see = __builtin_amdgcn_readfirstlane(all_see);
+    kv_half8 q[MT][DIM / 32][T];
+    float undo[MT];
+
+    kv_f32x4 o[MT][VC] = {};
+    Unit unit;
+    float top[MT], total[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) top[i] = -FLT_MAX, total[i] = 0.0f;
+
+    const size_t head_bytes = (size_t)kPage * DIM;
+    const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16, v_at = r * kPage + g * 16;
+    uint4 kr[4][KC], vr[VC];
+    auto load_k = [&](int32_t id) {
+        const int8_t* p = a.c.k + ((size_t)max(id, 0) * a.c.heads + h) * head_bytes + k_at;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int c = 0; c < KC; ++c) kr[t][c] = *reinterpret_cast<const uint4*>(p + t * 4 * DIM + c * 64);
+    };
+    auto load_v = [&](int32_t id) {
+        const int8_t* p = a.c.v + ((size_t)max(id, 0) * a.c.heads + h) * head_bytes + v_at;
+#pragma unroll
+        for (int c = 0; c < VC; ++c) vr[c] = *reinterpret_cast<const uint4*>(p + c * 16 * kPage);
+    };
+
+    for (uint32_t base = first + wave; base < last; base += 64 * NW) {
+        if (base != first + wave) look_up(base + lane * NW);
+        const uint32_t count = min(64u, (last - base + NW - 1) / NW);
+        int32_t id = __builtin_amdgcn_readlane(my_id, 0);
+        load_k(id);
+        load_v(id);
+        if (base == first + wave) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i) undo[i] = raw[i].template convert<16, T>(a.negative, q[i]) * a.scale;
+        }
+        for (uint32_t i = 0; i < count; ++i) {
+            const int32_t next = __builtin_amdgcn_readlane(my_id, min(i + 1, count - 1));
+            const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i));
+            const float vs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i));
+            const int32_t key0 = (int32_t)((base + i * NW) * kPage);
+
+            kv_f32x4 s[MT][4] = {};
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    kv_half8 k[4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        k[t] = u ? half_codes(kr[t][c].z, kr[t][c].w) : half_codes(kr[t][c].x, kr[t][c].y);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+#pragma unroll
+                        for (int e = 0; e < T; ++e)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t)
+                                s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[t], q[j][2 * c + u][e], s[j][t], 0, 0, 0);
+                }
+            if (i + 1 < count) load_k(next);
+
+            const float shrink_all = unit.next(vs);
+            if (shrink_all != 1.0f)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink_all;
+            kv_half8 p[MT][2][T];
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                float factor = ks * undo[j];
+                if (key0 + kPage > all_see || id < 0) {
+                    const int32_t sees = (id < 0 ? 0 : limit[j]) - key0 - (int32_t)g * 16;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s[j][t][k] = 4 * t + k < sees ? s[j][t][k] * factor : -INFINITY;
+                    factor = 1.0f;
+                }
+                float m = max3(s[j][0][0], s[j][0][1], s[j][0][2]);
+#pragma unroll
+                for (int k = 3; k < 15; k += 2) m = max3(m, s[j][k / 4][k % 4], s[j][(k + 1) / 4][(k + 1) % 4]);
+                m = fmaxf(max_over_16(fmaxf(m, s[j][3][3])) * factor, top[j]);
+                if (__any(m > top[j])) {
+                    const float shrink = __builtin_amdgcn_exp2f(top[j] - m);
+                    total[j] *= shrink;
+#pragma unroll
+                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink;
+                    top[j] = m;
+                }
+                const float off = unit.lift - m;
+                float sum = 0.0f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float x[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][2 * u + k / 4][k % 4], factor, off));
+                    sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                    half_terms<T>(x, p[j][u]);
+                }
+                total[j] = __builtin_fmaf(sum, unit.drop, total[j]);
+            }
+#pragma unroll
+            for (int c = 0; c < VC; c += 2) {
+                const kv_half8 v[2][2] = {{half_codes(vr[c].x, vr[c].y), half_codes(vr[c + 1].x, vr[c + 1].y)},
+                                          {half_codes(vr[c].z, vr[c].w), half_codes(vr[c + 1].z, vr[c + 1].w)}};
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < T; ++e)
+#pragma unroll
+                        for (int j = 0; j < MT; ++j)
+#pragma unroll
+                            for (int d = 0; d < 2; ++d)
+                                o[j][c + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u][d], p[j][u][e], o[j][c + d], 0, 0, 0);
+            }
+            if (i + 1 < count) load_v(next);
+            id = next;
+        }
+    }
+
+    // the waves' results meet in LDS, 16 rows at a time
+    __shared__ float os[NW][16][DIM + 4];
+    __shared__ float tops[NW][16], totals[NW][16];
+    __shared__ size_t items[16];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const uint32_t row0 = work.first_row + j * 16;
+        if (j) __syncthreads();
+        if (row0 < work.row_count) {
+            total[j] = sum_over_16(total[j]);
+            if (g == 0) tops[wave][r] = top[j], totals[wave][r] = total[j];
+            if (threadIdx.x < 16) items[r] = Row(a, work, row0 + r).item;
+#pragma unroll
+            for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[j][c] * unit.unit;
+        }
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 16 * DIM; i += NW * 64) {
+            const uint32_t row16 = i / DIM, d = i % DIM;
+            if (row0 + row16 >= work.row_count) break;
+            float m = tops[0][row16], l = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 1; w < NW; ++w) m = fmaxf(m, tops[w][row16]);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = __builtin_amdgcn_exp2f(tops[w][row16] - m);
+                l = __builtin_fmaf(totals[w][row16], f, l);
+                y = __builtin_fmaf(os[w][row16][d], f, y);
+            }
+            const size_t at = items[row16] * (a.prefix_slots + a.own_slots) + work.slot;
+            a.part[at * DIM + d] = y;
+            if (d == 0) a.stats[at * 2] = m, a.stats[at * 2 + 1] = l;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// many rows: four waves of 32 rows share a page in LDS (the layout of
+// kv8_attend_many_kernel, qar_kv8.hip).
+
+constexpr int kTileRows = 128;
+
+template <int DIM, int IN>
+__global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (IN == kInBF16 && DIM < 256))
+    void kv8_shared_many_kernel(SharedArgs a, uint32_t first_unit) {
+    constexpr int T = IN == kInBF16 ? 1 : 2;
+    constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
+    constexpr int KR = DIM / 8;                        // slots of a row of keys
+    const auto k_swizzle = [](uint32_t row) { return DIM == 64 ? row / 2 % 8 : row % 16; };
+    __shared__ kv_half8 k_tile[kPage * KR], v_tile[DIM * 8];
+    __shared__ uint4 k_codes[U * kThreads], v_codes[U * kThreads];
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), r = lane % 32,
+                   g = lane / 32;
+    const Work work(a, first_unit + blockIdx.x, kTileRows);
+    if (!work.any) return;
+    const uint32_t h = work.head, first = work.first;
+    const uint32_t first_row = work.first_row + wave * 32;
+    const Row row(a, work, first_row + r);
+    Query<IN, DIM, 8, 16> raw;
+    raw.load(a.q, row.there ? row.query : 0, g * 8, row.there);
+
+    // Own pages: only as far as the tile's last row sees.
+    uint32_t last = work.last;
+    if (work.slot >= a.prefix_slots) {
+        const Seq seq(a, work.first_seq);
+        const int32_t i = min((int32_t)(min(work.first_row + kTileRows, a.rows) - 1) / (int32_t)a.group, seq.m - 1);
+        const int32_t keys = seq.n - seq.m + i + 1;
+        last = min(last, seq.m > 0 && keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u);
+    }
+    // what the wave's rows see: all of them the keys below all_see, none a page from my_last on
+    int32_t all_see = row.there ? row.limit : INT32_MAX, most = row.there ? row.limit : 0;
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        all_see = min(all_see, __shfl_xor(all_see, d));
+        most = max(most, __shfl_xor(most, d));
+    }
+    all_see = __builtin_amdgcn_readfirstlane(all_see);
+    most = __builtin_amdgcn_readfirstlane(most);
+    const uint32_t my_last = min(last, most > 0 ? (uint32_t)(most + kPage - 1) / kPage : 0u);
+    const int32_t limit = row.there ? row.limit : INT32_MAX;
+
+    const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
+    struct Page {
+        int32_t id;
+        float ks, vs;          // 0 for a page that is not there: what page 0 holds must not matter
+    };
+    uint32_t base = first;
+    int32_t my_id;
+    float my_ks, my_vs;
+    auto look_up = [&] {
+        my_id = valid_page(table[min(base + lane, work.last - 1)], a.c.pages);
+        const size_t at = (size_t)max(my_id, 0) * a.c.heads + h;
+        my_ks = my_id < 0 ? 0.0f : a.c.k_scales[at];
+        my_vs = my_id < 0 ? 0.0f : a.c.v_scales[at];
+    };
+    auto page_at = [&](uint32_t page) {
+        if (page - base >= 64) {
+            base = page;
+            look_up();
+        }
+        const uint32_t i = page - base;
+        return Page{__builtin_amdgcn_readlane(my_id, i),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i)),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i))};
+    };
+    auto fetch = [&](int32_t id) {
+        const size_t at = ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            to_lds(a.c.k + at + u * kThreads * 16, k_codes + u * kThreads + wave * 64);
+            to_lds(a.c.v + at + u * kThreads * 16, v_codes + u * kThreads + wave * 64);
+        }
+    };
+    look_up();
+    Page now = page_at(first), next = page_at(first + 1);
+    fetch(now.id);
+
+    kv_half8 q[DIM / 16][T];
+    const float undo = raw.template convert<32, T>(a.negative, q) * a.scale;
+
+    kv_f32x16 o[DIM / 32] = {};
+    Unit unit;
+    float top = -FLT_MAX, total = 0.0f;
+    const uint32_t k_first = r * (KR * 16) + (g ^ k_swizzle(r)) * 16, v_first = r * 128 + (g ^ r / 2 % 8) * 16;
+    for (uint32_t page = first; page < last; ++page) {
+        loads_done();
+        uint4 kr[U], vr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) kr[u] = k_codes[u * kThreads + tid], vr[u] = v_codes[u * kThreads + tid];
+        lds_barrier();                               // all waves are done with the page before
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid;
+            const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
+            k_tile[lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
+            k_tile[lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
+            const uint32_t d = i / 4, e = i % 4 * 2;
+            v_tile[d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
+            v_tile[d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
+        }
+        const Page after = page_at(page + 2);
+        if (page + 1 < last) fetch(next.id);
+        lds_barrier();
+        // kept in registers, all the fragments' addresses would take thirteen
+        uint32_t k_at = k_first, v_at = v_first;
+        asm volatile("" : "+v"(k_at), "+v"(v_at));
+        if (page < my_last && now.id >= 0) {
+            kv_f32x16 s[2];
+            s[0] = s[1] = kv_f32x16{};
+#pragma unroll
+            for (int c = 0; c < DIM / 16; ++c)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const kv_half8 k = *reinterpret_cast<const kv_half8*>((const char*)k_tile + (k_at ^ (c * 32)) + t * 32 * KR * 16);
+#pragma unroll
+                    for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
+                }
+            const int32_t key0 = (int32_t)(page * kPage);
+            const float shrink_all = unit.next(now.vs);
+            if (shrink_all != 1.0f)
+#pragma unroll
+                for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink_all;
+            float factor = now.ks * undo;
+            if (key0 + kPage > all_see) {
+                // register k of tile t is key 32 t + 16 (k / 8) + 8 g + k % 8
+                const int32_t sees = limit - key0 - (int32_t)g * 8;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        s[t][k] = 32 * t + 16 * (k / 8) + k % 8 < sees ? s[t][k] * factor : -INFINITY;
+                factor = 1.0f;
+            }
+            float m = max3(s[0][15], s[1][15], s[0][14]);
+            float m1 = max3(s[1][14], s[0][13], s[1][13]);
+#pragma unroll
+            for (int k = 0; k < 12; k += 2) {
+                m = max3(m, s[0][k], s[0][k + 1]);
+                m1 = max3(m1, s[1][k], s[1][k + 1]);
+            }
+            m = max3(m, s[0][12], s[1][12]);
+            m = fmaxf(max_over_32(fmaxf(m, m1)) * factor, top);
+            // outputs and sums are taken to the new maximum when it has grown by
+            // 2^1.5, which the numerators' type has room for
+            if (__any(m > top + 1.5f)) {
+                const float shrink = __builtin_amdgcn_exp2f(top - m);
+                total *= shrink;
+#pragma unroll
+                for (int d = 0; d < DIM / 32; ++d) o[d] *= shrink;
+                top = m;
+            }
+            const float off = unit.lift - top;
+            kv_half8 p[4][T];
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][u % 2 * 8 + k], factor, off));
+                sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                half_terms<T>(x, p[u]);
+            }
+            total = __builtin_fmaf(sum, unit.drop, total);
+            // neighbouring products add to different tiles: none waits for the one before it
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int d = 0; d < DIM / 32; ++d) {
+                    const kv_half8 v = *reinterpret_cast<const kv_half8*>((const char*)v_tile + (v_at ^ (u * 32)) + d * 32 * 128);
+#pragma unroll
+                    for (int e = 0; e < T; ++e) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], o[d], 0, 0, 0);
+                }
+        }
+        now = next, next = after;
+    }
+    loads_done();                                    // nothing may write to LDS that is no longer this workgroup's
+
+    total = sum_over_32(total);
+    if (first_row + r >= work.row_count) return;
+    const size_t at = row.item * (a.prefix_slots + a.own_slots) + work.slot;
+    // register k of tile d is channel 32 d + 8 (k / 4) + 4 g + k % 4
+#pragma unroll
+    for (int d = 0; d < DIM / 32; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<kv_f32x4*>(a.part + at * DIM + d * 32 + k * 2 + g * 4) =
+                kv_f32x4{o[d][k], o[d][k + 1], o[d][k + 2], o[d][k + 3]} * unit.unit;
+    if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
+}
+
+// ---------------------------------------------------------------------------
+// a row's slots joined: DIM / 4 lanes with four channels each take a row.
+
+template <int DIM, int OUT>
+__global__ __launch_bounds__(kThreads) void kv8_shared_join_kernel(SharedArgs a) {
+    constexpr int Q = DIM / 4, ROWS = kThreads / Q;
+    const uint32_t q = threadIdx.x % Q;
+    const size_t item = (size_t)blockIdx.x * ROWS + threadIdx.x / Q, all = (size_t)a.c.batch * a.c.heads * a.rows;
+    // a wave's rows may be of several sequences: each looks up its own
+    const size_t safe = min(item, all - 1);
+    const uint32_t mine = safe % a.rows, bh = safe / a.rows, h = bh % a.c.heads, b = bh / a.c.heads;
+    uint32_t before = 0;
+    for (uint32_t lane = 0; lane < 64; lane += Q < 64 ? Q : 64) {
+        const uint32_t other = pages_before(a, __builtin_amdgcn_readlane(b, lane));
+        if (threadIdx.x % 64 / Q == lane / Q || Q >= 64) before = other;
+    }
+    const Seq seq(a, b);
+    const int32_t i = (int32_t)(mine / a.group);
+    const uint32_t pages = (uint32_t)(seq.n + kPage - 1) / kPage;
+    const Cut prefix(before, a.prefix_slots), own(pages > before ? pages - before : 0, a.own_slots);
+    float m = -FLT_MAX, l = 0.0f;
+    kv_f32x4 y = {};
+    if (i < seq.m) {
+        const uint32_t slots = a.prefix_slots + a.own_slots, count = prefix.used + own.used;
+#pragma unroll 4
+        for (uint32_t s = 0; s < count; ++s) {
+            const size_t at = safe * slots + (s < prefix.used ? s : a.prefix_slots + s - prefix.used);
+            const float2 stat = *reinterpret_cast<const float2*>(a.stats + at * 2);
+            const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + q * 4);
+            const float top = fmaxf(m, stat.x), f = __builtin_amdgcn_exp2f(m - top), e = __builtin_amdgcn_exp2f(stat.x - top);
+            m = top;
+            l = __builtin_fmaf(stat.y, e, l * f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], e, y[k] * f);
+        }
+    }
+    if (item >= all) return;
+    const bool seen = l != 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = seen ? y[k] / l : 0.0f;
+    store4<OUT>(a.out, (((size_t)b * a.queries + i) * a.heads + h * a.group + mine % a.group) * DIM + q * 4, y);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+
+template <int D>
+using Dim = std::integral_constant<int, D>;
+
+template <class F>
+hipError_t with_dim(int dim, F f) {
+    return dim == 64 ? f(Dim<64>{}) : dim == 128 ? f(Dim<128>{}) : f(Dim<256>{});
+}
+
+template <class F>
+hipError_t with_kind(int kind, F f) {
+    return kind == kInBF16 ? f(std::integral_constant<int, kInBF16>{}) : f(std::integral_constant<int, kInF32>{});
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Rows of the few-row kernel's tile.  Two tiles of 16 rows at 256 channels
+// would not fit a wave's registers.
+uint32_t few_rows(int dim, uint32_t rows) { return dim == 256 || rows <= 16 ? 16 : 32; }
+bool is_few(int dim, size_t rows) { return rows <= (dim == 256 ? 16 : 32); }
+
+// How a call is cut.  Group sizes, prefixes and lengths are on the device; the
+// host goes by their averages and bounds.
+struct Plan {
+    bool prefix_few, own_few;
+    uint32_t prefix_rows, own_rows;      // of a tile
+    uint32_t prefix_tiles, own_tiles, prefix_slots, own_slots;
+};
+
+uint32_t slots_for(size_t units, uint32_t width) {
+    const size_t want = (512 + units - 1) / units, most = (width + 3) / 4;
+    return (uint32_t)(want < most ? want : most);
+}
+
+Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups) {
+    Plan p = {};
+    const size_t all = (size_t)batch * rows, mean = (all + groups - 1) / groups;
+    p.prefix_few = is_few(dim, mean);
+    p.prefix_rows = p.prefix_few ? few_rows(dim, (uint32_t)mean) : kTileRows;
+    p.prefix_tiles = (uint32_t)(all / p.prefix_rows) + groups;
+    const size_t likely = groups == 1 ? (all + p.prefix_rows - 1) / p.prefix_rows : (all / p.prefix_rows + (groups + 1) / 2);
+    p.prefix_slots = slots_for(likely * kv_heads, width);
+    p.own_few = is_few(dim, rows);
+    p.own_rows = p.own_few ? few_rows(dim, rows) : kTileRows;
+    p.own_tiles = (rows + p.own_rows - 1) / p.own_rows;
+    p.own_slots = slots_for((size_t)batch * kv_heads * p.own_tiles, width);
+    return p;
+}
+
+} // namespace
+
+size_t kv8_shared_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups) {
+    const Plan p = plan_for(batch, kv_heads, rows, dim, width, groups);
+    const size_t parts = (size_t)batch * kv_heads * rows * (p.prefix_slots + p.own_slots);
+    return align256(parts * 8) + align256(parts * dim * 4);
+}
+
+hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads, const int32_t* starts,
+                             const int32_t* prefix, uint32_t groups, const int32_t* q_lens, float scale, void* out,
+                             void* workspace, hipStream_t st) {
+    SharedArgs a = {};
+    a.c = c, a.q = q, a.starts = starts, a.prefix = prefix, a.groups = groups, a.q_lens = q_lens, a.out = out;
+    a.queries = queries, a.heads = heads, a.group = heads / c.heads, a.rows = queries * a.group;
+    a.scale = (scale < 0 ? -scale : scale) * 1.44269504088896340736f;
+    a.negative = scale < 0;
+    const Plan p = plan_for(c.batch, c.heads, a.rows, c.dim, c.width, groups);
+    a.prefix_tiles = p.prefix_tiles, a.own_tiles = p.own_tiles, a.prefix_slots = p.prefix_slots, a.own_slots = p.own_slots;
+    const size_t items = (size_t)c.batch * c.heads * a.rows, parts = items * (p.prefix_slots + p.own_slots);
+    a.stats = (float*)workspace;
+    a.part = (float*)((uint8_t*)workspace + align256(parts * 8));
+    return with_dim(c.dim, [&](auto D) {
+        return with_kind(kind, [&](auto K) {
+            const uint32_t prefix_units = p.prefix_tiles * c.heads * p.prefix_slots;
+            const uint32_t own_units = c.batch * c.heads * p.own_tiles * p.own_slots;
+            const auto attend = [&](bool few, uint32_t tile, uint32_t first, uint32_t count) {
+                if (!few) return launch_threads(kv8_shared_many_kernel<D(), K()>, count, kThreads, st, a, first);
+                if (tile == 16) return launch_threads(kv8_shared_few_kernel<D(), 1, K(), 4>, count, kThreads, st, a, first);
+                return launch_threads(kv8_shared_few_kernel<D(), D() == 256 ? 1 : 2, K(), 4>, count, kThreads, st, a, first);
+            };
+            hipError_t e;
+            if (p.prefix_few == p.own_few && p.prefix_rows == p.own_rows) {
+                e = attend(p.own_few, p.own_rows, 0, prefix_units + own_units);
+            } else {
+                e = attend(p.prefix_few, p.prefix_rows, 0, prefix_units);
+                if (e == hipSuccess) e = attend(p.own_few, p.own_rows, prefix_units, own_units);
+            }
+            if (e != hipSuccess) return e;
+            constexpr size_t rows = kThreads / (D() / 4);
+            return launch_threads(kv8_shared_join_kernel<D(), K()>, (uint32_t)((items + rows - 1) / rows), kThreads, st, a);
+        });
+    });
+}
+
+} // namespace qar

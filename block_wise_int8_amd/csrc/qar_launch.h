@@ -135,6 +135,12 @@ hipError_t launch_kv8_attention(const Kv8& c, const void* q, int kind, uint32_t 
 hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights, uint32_t recent, uint32_t keep,
                             int32_t* kept, float* moved, hipStream_t st);
 
+// Attention behind prefixes that sequences share (qar_kv8_shared.hip).
+size_t kv8_shared_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups);
+hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads, const int32_t* starts,
+                             const int32_t* prefix, uint32_t groups, const int32_t* q_lens, float scale, void* out,
+                             void* workspace, hipStream_t st);
+
 // Owners of the cache's pages (qar_kv8_pages.hip).
 constexpr uint32_t kKv8MaxSequences = 4096;
 hipError_t launch_kv8_fork(const Kv8& c, int32_t* refs, const int32_t* parents, const Kv8& into, hipStream_t st);

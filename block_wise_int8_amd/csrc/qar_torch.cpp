@@ -61,6 +61,19 @@ int64_t whole(PyObject* o) {
     return v;
 }
 
+double number(PyObject* o) {
+    const double given = PyFloat_AsDouble(o);
+    if (given == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw Refused{};
+    }
+    return given;
+}
+
+float scale_of(PyObject* given, uint32_t dim) {
+    return (float)(given == Py_None ? 1.0 / std::sqrt((double)dim) : number(given));
+}
+
 at::ScalarType dtype_of(PyObject* o) {
     require(THPDtype_Check(o));
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
@@ -301,12 +314,7 @@ PyObject* norm_rotate(PyObject* const* a) {
         if (a[5 + i] != Py_None) gains[i] = gpu.shaped(tensor(a[5 + i]), type, {dim});
     float eps = 0.0f;
     if (a[7] != Py_None) {
-        const double given = PyFloat_AsDouble(a[7]);
-        if (given == -1.0 && PyErr_Occurred()) {
-            PyErr_Clear();
-            throw Refused{};
-        }
-        eps = (float)given;
+        eps = (float)number(a[7]);
         flags |= QAR_ROTATE_NORM;
     }
     require(PyBool_Check(a[8]));
@@ -391,15 +399,7 @@ PyObject* kv8_attention(PyObject* const* a) {
     const void* qp = gpu.shaped(q, type, shape);
     const int32_t* lens = nullptr;
     if (a[2] != Py_None) lens = (const int32_t*)gpu.shaped(tensor(a[2]), at::kInt, {c.batch});
-    float scale = (float)(1.0 / std::sqrt((double)c.dim));
-    if (a[3] != Py_None) {
-        const double given = PyFloat_AsDouble(a[3]);
-        if (given == -1.0 && PyErr_Occurred()) {
-            PyErr_Clear();
-            throw Refused{};
-        }
-        scale = (float)given;
-    }
+    const float scale = scale_of(a[3], c.dim);
     float* weights = nullptr;
     if (a[4] != Py_None)
         weights = (float*)gpu.shaped(tensor(a[4]), at::kFloat, {c.batch, c.kv_heads, (int64_t)c.table_width * QAR_KV8_PAGE});
@@ -414,6 +414,39 @@ PyObject* kv8_attention(PyObject* const* a) {
     return result(made([&] {
                       return qar_kv8_attention(&c, qp, code, queries, heads, lens, scale, weights, op, ws.data, ws.bytes,
                                                gpu.stream);
+                  }),
+                  out);
+}
+
+// cache, q, starts, prefix, q_lens, scale, out, workspace (the last four may be None)
+PyObject* kv8_attention_shared(PyObject* const* a) {
+    Cache cache(a[0]);
+    const Gpu gpu(cache.t[0]);
+    cache.fill(gpu);
+    const qar_kv8_cache& c = cache.c;
+    const at::Tensor &q = tensor(a[1]), &starts = tensor(a[2]);
+    require(q.dim() == 4 && starts.dim() == 1 && starts.size(0) >= 2);
+    const uint32_t queries = u32(q.size(1)), heads = u32(q.size(2)), groups = u32(starts.size(0) - 1);
+    const int64_t shape[4] = {c.batch, queries, heads, c.dim};
+    const at::ScalarType type = q.scalar_type();
+    const qar_dtype code = data_code(type);
+    const void* qp = gpu.shaped(q, type, shape);
+    const int32_t* sp = (const int32_t*)gpu.check(starts, at::kInt).data_ptr();
+    const int32_t* pp = (const int32_t*)gpu.shaped(tensor(a[3]), at::kInt, {groups});
+    const int32_t* lens = nullptr;
+    if (a[4] != Py_None) lens = (const int32_t*)gpu.shaped(tensor(a[4]), at::kInt, {c.batch});
+    const float scale = scale_of(a[5], c.dim);
+    at::Tensor out;
+    if (a[6] == Py_None)
+        out = gpu.empty(shape, type);
+    else
+        gpu.shaped(out = tensor(a[6]), type, shape);
+    const Workspace ws(gpu, a[7], qar_kv8_attention_shared_workspace_bytes(c.batch, queries, heads, c.kv_heads, c.dim,
+                                                                           c.table_width, groups));
+    void* op = out.data_ptr();
+    return result(made([&] {
+                      return qar_kv8_attention_shared(&c, qp, code, queries, heads, sp, pp, groups, lens, scale, op, ws.data,
+                                                      ws.bytes, gpu.stream);
                   }),
                   out);
 }
@@ -593,6 +626,7 @@ PyMethodDef methods[] = {method<kv8_append, 4>("kv8_append"),         method<kv8
                          method<kv8_free, 3>("kv8_free"),             method<kv8_reserve, 6>("kv8_reserve"),
                          method<kv8_compact, 4>("kv8_compact"),       method<kv8_copy, 4>("kv8_copy"),
                          method<norm_rotate, 10>("norm_rotate"),      method<mx4_linear_fused, 9>("mx4_linear_fused"),
+                         method<kv8_attention_shared, 8>("kv8_attention_shared"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qar_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

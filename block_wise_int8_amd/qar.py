@@ -72,6 +72,8 @@ _SIGNATURES = {
     "qar_kv8_read": [_vp, _vp, _u32, _vp, _vp, _int, _vp],
     "qar_kv8_attention_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _int, _int],
     "qar_kv8_attention": [_vp, _vp, _int, _u32, _u32, _vp, ctypes.c_float, _vp, _vp, _vp, _sz, _vp],
+    "qar_kv8_attention_shared_workspace_bytes": [_u32, _u32, _u32, _u32, _u32, _u32, _u32],
+    "qar_kv8_attention_shared": [_vp, _vp, _int, _u32, _u32, _vp, _vp, _u32, _vp, ctypes.c_float, _vp, _vp, _sz, _vp],
     "qar_kv8_evict": [_vp, _vp, _vp, _u32, _u32, _vp, _vp, _vp],
     "qar_norm_rotate": [_vp, _int, _sz, _sz, _u32, _u32, _u32, _vp, _vp, _u32, _vp, _vp, ctypes.c_float, _u32, _vp, _vp, _vp,
                         _vp],
@@ -972,7 +974,7 @@ def qar_kv8_attention(cache: KvCache, q: torch.Tensor, q_lens: torch.Tensor | No
     return _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace)
 
 
-def _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace):
+def _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace, where="qar_kv8_attention"):
     _, index, batch, kv_heads, dim, width = cache._struct()
     dev = cache.k.device
     if _dev(q, "q").dim() != 4:
@@ -989,7 +991,34 @@ def _why_kv8_attention(cache, q, q_lens, scale, weights, out, workspace):
         _shaped(out, "out", shape, (q.dtype,), dev)
     _why_workspace(workspace, dev)
     _on_current(index)
-    raise ValueError("qar_kv8_attention: the arguments do not fit")
+    raise ValueError(f"{where}: the arguments do not fit")
+
+
+def qar_kv8_attention_shared(cache: KvCache, q: torch.Tensor, starts: torch.Tensor, prefix: torch.Tensor,
+                             q_lens: torch.Tensor | None = None, scale: float | None = None,
+                             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """qar_kv8_attention for sequences that share their first tokens' pages, which are read once for each group:
+    sequences starts[g] .. starts[g + 1] - 1 (int32[groups + 1]) have their first prefix[g] (int32[groups]) tokens in
+    common.  ``workspace`` (at least lib().qar_kv8_attention_shared_workspace_bytes(...) bytes) is allocated with torch
+    when not given."""
+    if stream is not None:
+        with _as_current(stream):
+            return qar_kv8_attention_shared(cache, q, starts, prefix, q_lens, scale, out, workspace)
+    made = _serve().kv8_attention_shared(cache, q, starts, prefix, q_lens, scale, out, workspace)
+    if made is not None:
+        return _done(made, "qar_kv8_attention_shared")
+    return _why_kv8_attention_shared(cache, q, starts, prefix, q_lens, scale, out, workspace)
+
+
+def _why_kv8_attention_shared(cache, q, starts, prefix, q_lens, scale, out, workspace):
+    cache._struct()
+    dev = cache.k.device
+    if _dev(starts, "starts").dim() != 1 or starts.shape[0] < 2:
+        raise ValueError(f"starts must be [groups + 1], not {list(starts.shape)}")
+    _shaped(starts, "starts", tuple(starts.shape), _INT32, dev)
+    _shaped(prefix, "prefix", (starts.shape[0] - 1,), _INT32, dev)
+    _why_kv8_attention(cache, q, q_lens, scale, None, out, workspace, "qar_kv8_attention_shared")
 
 
 def qar_kv8_evict(cache: KvCache, into: KvCache, weights: torch.Tensor, recent: int, keep: int,

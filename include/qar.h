@@ -579,6 +579,26 @@ qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtyp
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The same attention for a batch whose sequences share their first tokens:
+ * group g is sequences starts[g] .. starts[g + 1] - 1, and its sequences' tables
+ * name the same pages for their first prefix[g] tokens.  The pages wholly among
+ * these are read once for all of the group's queries (through the table of its
+ * first sequence), the others sequence by sequence; the result is that of
+ * qar_kv8_attention up to the order of the sums, whatever the lengths.
+ * Sequences outside all groups share nothing.
+ *   starts     [in] int32[groups + 1], ascending, 0 .. batch; 1 <= groups <= batch.
+ *   prefix     [in] int32[groups]; below 0 counts as 0.
+ *   workspace  [scratch] qar_kv8_attention_shared_workspace_bytes(...) bytes, as
+ *              for qar_kv8_attention (never NULL).
+ */
+size_t qar_kv8_attention_shared_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
+                                                uint32_t dim, uint32_t table_width, uint32_t groups);
+qar_status qar_kv8_attention_shared(const qar_kv8_cache* cache, const void* q, qar_dtype dtype, uint32_t queries,
+                                    uint32_t heads, const int32_t* starts, const int32_t* prefix, uint32_t groups,
+                                    const int32_t* q_lens, float scale, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
  * Every sequence and head keeps `keep` tokens: its last min(recent, keep) and,
  * of the others, those with the largest weights, the lower position where
  * weights are equal (NaN counts as the largest).  A sequence of at most `keep`

@@ -241,3 +241,69 @@ def test_mx4_linear_fused_arguments():
     assert ext.mx4_linear_fused(*[None] * 9) is None
     with pytest.raises(TypeError, match="9 arguments"):
         ext.mx4_linear_fused(None)
+
+
+# ---------------------------------------------------------------------------
+# attention behind shared prefixes
+
+
+def test_attention_shared_refusals(L):
+    size = L.qar_kv8_attention_shared_workspace_bytes
+    need = size(3, 1, 4, 2, 64, 4, 2)
+    assert need > 0 and need % 256 == 0
+    good = dict(q=600 * M, dtype=0, queries=1, heads=4, starts=610 * M, prefix=620 * M, groups=2, q_lens=None, scale=1.0,
+                out=700 * M, ws=800 * M, size=need)
+
+    def call(c=None, **kw):
+        return L.qar_kv8_attention_shared(c or ctypes.byref(_struct()), *{**good, **kw}.values(), None)
+    assert call(queries=0) == OK and call(ctypes.byref(_struct(batch=0))) == OK
+    for kw, status in BAD_CACHES:
+        assert call(ctypes.byref(_struct(**kw))) == status, kw
+    for name in ("q", "out", "starts", "prefix", "ws"):
+        assert call(**{name: None}) == INV, name
+    assert call(groups=0) == INV and call(groups=4) == INV and call(heads=3) == INV and call(heads=0) == INV
+    assert call(queries=(1 << 30) + 1) == INV and call(dtype=2) == UNS
+    assert call(q=600 * M + 8) == MIS and call(out=700 * M + 8) == MIS and call(q_lens=900 * M + 2) == MIS
+    assert call(starts=610 * M + 2) == MIS and call(prefix=620 * M + 1) == MIS and call(ws=800 * M + 128) == MIS
+    assert call(size=need - 1) == INV
+    for at in (600 * M, 610 * M, 620 * M, 200 * M, 500 * M, 800 * M):
+        assert call(out=at) == INV, at
+    for at in (600 * M, 610 * M, 620 * M, M, 700 * M):
+        assert call(ws=at) == INV, at
+    assert call(q_lens=700 * M) == INV and call(out=610 * M - 16) == INV
+    assert size(0, 1, 4, 2, 64, 4, 1) == size(3, 0, 4, 2, 64, 4, 1) == size(3, 1, 3, 2, 64, 4, 1) == size(3, 1, 4, 2, 80, 4, 1) == 0
+    assert size(3, 1, 4, 2, 64, 0, 1) == size(3, 1, 4, 2, 64, 4, 0) == size(3, 1, 4, 2, 64, 4, 4) == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_shared_workspace(L, dim):
+    """A slot of the prefix and one of the own pages at least: a maximum, a sum and a row of outputs for each row."""
+    for batch, queries, heads, kv_heads, width, groups in [(1, 1, 1, 1, 1, 1), (64, 1, 32, 8, 600, 1), (64, 1, 32, 8, 600, 64),
+                                                           (3, 500, 12, 12, 40, 2), (1000, 1, 8, 1, 9, 7)]:
+        assert L.qar_kv8_attention_shared_workspace_bytes(batch, queries, heads, kv_heads, dim, width, groups) >= \
+            batch * queries * heads * 2 * (dim * 4 + 8)
+
+
+def test_attention_shared_arguments():
+    c, q, three, one = _cache(), _t(3, 1, 4, 64), _t(3, dtype=I32), _t(1, dtype=I32)
+    two = _t(2, dtype=I32)
+    cases = [(dict(starts=one, prefix=one), ValueError, "starts must be"), (dict(starts=three, prefix=three), ValueError, "prefix must be"),
+             (dict(starts=_t(2), prefix=one), TypeError, "starts must be torch.int32"), (dict(starts=two, prefix=_t(1)), TypeError, "prefix"),
+             (dict(q=_t(3, 4, 64)), ValueError, "q must be"), (dict(q_lens=two), ValueError, "q_lens must be"),
+             (dict(out=_t(3, 1, 4, 32)), ValueError, "out must be"), (dict(workspace=torch.zeros(3)), TypeError, "workspace must be")]
+    for i, (kw, error, text) in enumerate(cases):
+        with pytest.raises(error, match=text):
+            qar.qar_kv8_attention_shared(c, **{**dict(q=q, starts=two, prefix=one), **kw})
+            pytest.fail(f"case {i} was not refused")
+    assert qar._serve().kv8_attention_shared(*[None] * 8) is None
+
+
+def test_the_header_beside_the_kernels_holds_no_vector_assembly():
+    """What tests/test_serve_sources.py asks of the kernels' sources, of the header that they share."""
+    import os
+    import re
+
+    from block_wise_int8_amd import build
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(build.CSRC, "qar_kv8_device.h")).read())
+    for s in re.findall(r"\basm\b[^;]*;", text):
+        assert not re.search(r'"[^"]*\bv_\w+', s), s
