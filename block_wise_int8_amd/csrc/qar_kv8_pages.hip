@@ -124,7 +124,7 @@ constexpr int kSequences = 4096;         // what the arrays below hold
 constexpr uint32_t kHasAll = ~0u, kLastOwner = ~1u;
 
 __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
-    __shared__ int32_t shared_page[kSequences];   // the page that a sequence goes on in, -1: at a page's start; -2: nowhere
+    __shared__ alignas(16) int32_t shared_page[kSequences];   // the page that a sequence goes on in, -1: at a page's start; -2: nowhere
     __shared__ uint32_t begin[kSequences + 1];    // of the sequence's looked-at entries, among all sequences'
     __shared__ uint32_t short_of[kSequences];     // the first page that it did not get, or one of the two above
     __shared__ int32_t found[4 * kScan];          // free pages that nobody has taken yet
@@ -162,8 +162,14 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
             if (id >= 0) {
                 const int32_t owners = a.refs[id];
                 if (owners > 1) {
+                    // sixteen at a time: one by one, each would wait for LDS
                     uint32_t rank = 0;
-                    for (uint32_t j = 0; j < b; ++j) rank += shared_page[j] == id;
+#pragma unroll 4
+                    for (uint32_t j = 0; j < b; j += 4) {
+                        const int4 four = *reinterpret_cast<const int4*>(shared_page + j);
+                        rank += (four.x == id) + (four.y == id && j + 1 < b) + (four.z == id && j + 2 < b) +
+                                (four.w == id && j + 3 < b);
+                    }
                     count += owners - (int32_t)rank > 1;
                     // the last owner keeps the page, if those before it got theirs
                     if (owners - (int32_t)rank <= 1) short_of[b] = kLastOwner;
@@ -180,6 +186,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
 
     // the entries in order, a thread each; free pages are looked for from the
     // front as far as they are needed
+    bool ran_out = false;
     uint32_t next_page = 0, have = 0, taken = 0;  // pages looked at; found and not taken: found[taken .. taken + have)
     for (uint32_t base = 0; base < entries; base += kScan) {
         const uint32_t e = base + tid;
@@ -238,6 +245,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
         }
         // the pool is empty
         if (wants && number >= served) atomicMin(&short_of[b], w);
+        ran_out |= served < total;
         __syncthreads();
     }
 
@@ -245,7 +253,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
         const uint32_t n = length_of(b), end = end_of(b, n);
         const uint32_t lacks = short_of[b];
         uint32_t room = shared_page[b] == -2 ? 0 : end - n;
-        if (lacks != kHasAll) {
+        if (ran_out && lacks != kHasAll) {
             bool fails = n % kPage && lacks == n / kPage;
             // the last owner of a page: one of those before it may have stayed without a copy
             if (shared_page[b] >= 0)

@@ -9,13 +9,13 @@
 // for every pair (a, b) of the rotated channels.  Bound by memory: each
 // element is read once and written once, and the arithmetic between, some
 // twenty instructions for a pair, fits under that.  What is not obvious is
-// where the pairs lie.  A lane owns two runs of eight channels (16 bytes of
-// bf16) of a head, chosen so that a pair is never split between lanes: with
-// pairs that lie half the rotated channels apart, run l and the run of its
-// partners; with neighbouring pairs, runs 2 l and 2 l + 1.  A head is then 4, 8
-// or 16 lanes, whose sum of squares is a few DPP moves, and a lane's sines and
-// cosines are the same for every head of a token: a workgroup computes a
-// token's once, and its lanes keep theirs in registers over the heads.
+// where the pairs lie.  A lane owns pieces of 16 bytes of a head, two or (for
+// binary32) four, chosen so that a pair is never split between lanes and that
+// neighbouring lanes read neighbouring pieces: with pairs that lie half the
+// rotated channels apart, pieces and the pieces of their partners.  A head is
+// then 4, 8 or 16 lanes, whose sum of squares is a few DPP moves, and a lane's
+// sines and cosines are the same for every head of a token: a workgroup
+// computes a token's once, and its lanes keep theirs in registers over the heads.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -29,34 +29,34 @@ namespace {
 
 enum : int { kHalves = 0, kNeighbours = 1, kSplitHalves = 2 };
 
-// Eight elements as binary32.
+// The elements of 16 bytes.
 template <int IN>
-__device__ __forceinline__ void load_run(const void* x, size_t e, float (&y)[8]) {
-    if constexpr (IN == kInBF16) {
-        const uint4 q = load_b128((const uint16_t*)x + e);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+constexpr int kPiece = IN == kInBF16 ? 8 : 4;
+
+template <int IN>
+__device__ __forceinline__ void load_piece(const void* x, size_t e, float (&y)[kPiece<IN>]) {
+    const uint4 q = load_b128((const char*)x + e * (16 / kPiece<IN>));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(w[i]), y[2 * i + 1] = bf16_hi(w[i]);
-    } else {
-        const uint4 a = load_b128((const float*)x + e), b = load_b128((const float*)x + e + 4);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __builtin_bit_cast(float, w[i]);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (IN == kInBF16)
+            y[2 * i] = bf16_lo(w[i]), y[2 * i + 1] = bf16_hi(w[i]);
+        else
+            y[i] = __builtin_bit_cast(float, w[i]);
     }
 }
 
 template <int OUT>
-__device__ __forceinline__ void store_run(void* x, size_t e, const float (&y)[8]) {
-    if constexpr (OUT == kInBF16) {
-        store_b128((uint16_t*)x + e, make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                                                pack_bf16x2(y[6], y[7])));
-    } else {
+__device__ __forceinline__ void store_piece(void* x, size_t e, const float (&y)[kPiece<OUT>]) {
+    uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4)
-            store_b128((float*)x + e + i,
-                       make_uint4(__builtin_bit_cast(uint32_t, y[i]), __builtin_bit_cast(uint32_t, y[i + 1]),
-                                  __builtin_bit_cast(uint32_t, y[i + 2]), __builtin_bit_cast(uint32_t, y[i + 3])));
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (OUT == kInBF16)
+            w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+        else
+            w[i] = __builtin_bit_cast(uint32_t, y[i]);
     }
+    store_b128((char*)x + e * (16 / kPiece<OUT>), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // The sum over a head's lanes.
@@ -84,11 +84,12 @@ __device__ __forceinline__ float2 cos_sin(int32_t position, float frequency) {
     return make_float2(k == 1 || k == 2 ? -a : a, k >= 2 ? -b : b);
 }
 
-// PAIRS: kSplitHalves is kHalves where the pairs are no multiple of eight and
+// PAIRS: kSplitHalves is kHalves where the pairs are no multiple of a piece, and
 // partners meet in LDS.
 template <int DIM, int IN, int PAIRS>
 __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
     constexpr int L = DIM / 16, H = kThreads / L;                   // lanes of a head, heads at a time
+    constexpr int E = kPiece<IN>, U = 8 / E, HALF = DIM / 2 / E;    // a lane's units of two pieces; half a head's pieces
     __shared__ float2 table[DIM / 2];
     __shared__ float rows[PAIRS == kSplitHalves ? H : 1][PAIRS == kSplitHalves ? DIM + 4 : 1];
     const uint32_t tid = threadIdx.x, l = tid % L, mine = tid / L;
@@ -96,20 +97,26 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
     const uint32_t part = blockIdx.x % a.parts, all = a.heads + 2 * a.kv_heads, rotated = a.heads + a.kv_heads;
     const uint32_t per = (all + a.parts - 1) / a.parts, first = part * per, last = min(first + per, all);
 
-    // the lane's runs of eight channels
-    uint32_t run[2];
-    if (PAIRS == kHalves && l < a.pairs / 8)
-        run[0] = l, run[1] = l + a.pairs / 8;
-    else
-        run[0] = 2 * l, run[1] = 2 * l + 1;
+    // Unit u of a head is a piece of first partners and that of their second
+    // ones, u and u + pairs / E; behind these, two pieces that are not rotated
+    // (with neighbours all units are of that kind, and turn within themselves).
+    const uint32_t paired = PAIRS == kHalves ? a.pairs / E : 0;
+    uint32_t unit[U], at[U][2];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        unit[i] = i * L + l;
+        at[i][0] = (unit[i] < paired ? unit[i] : unit[i] + paired) * E;
+        at[i][1] = (unit[i] < paired ? unit[i] + paired : unit[i] + HALF) * E;
+    }
 
-    float x[2][8] = {};
-    uint32_t h = first + mine;
+    float x[U][2][E] = {};
     auto load = [&](uint32_t head) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) load_run<IN>(a.x, (token * all + head) * DIM + run[i] * 8, x[i]);
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) load_piece<IN>(a.x, (token * all + head) * DIM + at[i][j], x[i][j]);
     };
-    if (h < last) load(h);
+    if (first + mine < last) load(first + mine);
 
     if (first < rotated && tid < a.pairs) {
         const size_t b = token / a.tokens;
@@ -117,98 +124,115 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
         table[tid] = cos_sin(position, a.frequencies[tid]);
     }
     __syncthreads();
-    // of the lane's pairs: eight with halves, four of each run with neighbours
-    float2 turn[8];
+    // the lane's pairs: E of a unit with halves, E / 2 of each piece with neighbours
+    float2 turn[U][E];
     if constexpr (PAIRS != kSplitHalves) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t pair = l * 8 + i;
-            turn[i] = pair < a.pairs ? table[pair] : make_float2(1.0f, 0.0f);
-        }
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const uint32_t pair = PAIRS == kHalves ? unit[i] * E + k : (at[i][k / (E / 2)] + k % (E / 2) * 2) / 2;
+                turn[i][k] = pair < a.pairs ? table[pair] : make_float2(1.0f, 0.0f);
+            }
     }
 
     for (uint32_t base = first; base < last; base += H) {
-        float y[2][8];
+        float y[U][2][E];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[i][k] = x[i][k];
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < E; ++k) y[i][j][k] = x[i][j][k];
         const uint32_t head = base + mine;
         if (head + H < last) load(head + H);
         const bool turned = head < rotated, there = head < last;
         if (a.norm) {
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < U; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) sum = __builtin_fmaf(y[i][k], y[i][k], sum);
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) sum = __builtin_fmaf(y[i][j][k], y[i][j][k], sum);
             sum = lanes_sum<L>(sum);
             if (turned) {
                 const float r = 1.0f / sqrtf(sum * (1.0f / DIM) + a.eps);
                 const void* gain = head < a.heads ? a.q_gain : a.k_gain;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float g[8];
-                    if (gain) load_run<IN>(gain, run[i] * 8, g);
+                for (int i = 0; i < U; ++i)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[i][k] = gain ? y[i][k] * r * g[k] : y[i][k] * r;
-                }
+                    for (int j = 0; j < 2; ++j) {
+                        float g[E];
+                        if (gain) load_piece<IN>(gain, at[i][j], g);
+#pragma unroll
+                        for (int k = 0; k < E; ++k) y[i][j][k] = gain ? y[i][j][k] * r * g[k] : y[i][j][k] * r;
+                    }
             }
         }
         if constexpr (PAIRS == kHalves) {
-            if (turned && l < a.pairs / 8) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float u = y[0][k], v = y[1][k];
-                    y[0][k] = u * turn[k].x - v * turn[k].y;
-                    y[1][k] = v * turn[k].x + u * turn[k].y;
+            for (int i = 0; i < U; ++i)
+                if (turned && unit[i] < paired) {
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const float u = y[i][0][k], v = y[i][1][k];
+                        y[i][0][k] = u * turn[i][k].x - v * turn[i][k].y;
+                        y[i][1][k] = v * turn[i][k].x + u * turn[i][k].y;
+                    }
                 }
-            }
         } else if constexpr (PAIRS == kNeighbours) {
             if (turned) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < U; ++i)
 #pragma unroll
-                    for (int k = 0; k < 8; k += 2) {
-                        const float2 t = turn[i * 4 + k / 2];
-                        const float u = y[i][k], v = y[i][k + 1];
-                        y[i][k] = u * t.x - v * t.y;
-                        y[i][k + 1] = v * t.x + u * t.y;
+                    for (int k = 0; k < E; ++k) {
+                        const float2 t = turn[i][k];
+                        float* z = y[i][k / (E / 2)] + k % (E / 2) * 2;
+                        const float u = z[0], v = z[1];
+                        z[0] = u * t.x - v * t.y;
+                        z[1] = v * t.x + u * t.y;
                     }
             }
         } else {
             // a head's lanes are of one wave, which writes and reads in order
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < U; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) rows[mine][run[i] * 8 + k] = y[i][k];
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) rows[mine][at[i][j] + k] = y[i][j][k];
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < U; ++i)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t c = run[i] * 8 + k;
-                    if (turned && c < 2 * a.pairs) {
-                        const bool upper = c >= a.pairs;
-                        const float2 t = table[upper ? c - a.pairs : c];
-                        const float partner = rows[mine][upper ? c - a.pairs : c + a.pairs];
-                        y[i][k] = y[i][k] * t.x + (upper ? partner : -partner) * t.y;
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const uint32_t c = at[i][j] + k;
+                        if (turned && c < 2 * a.pairs) {
+                            const bool upper = c >= a.pairs;
+                            const float2 t = table[upper ? c - a.pairs : c];
+                            const float partner = rows[mine][upper ? c - a.pairs : c + a.pairs];
+                            y[i][j][k] = y[i][j][k] * t.x + (upper ? partner : -partner) * t.y;
+                        }
                     }
-                }
             __builtin_amdgcn_wave_barrier();
         }
         if (!there) continue;
         void* out = head < a.heads ? a.q : turned ? a.k : a.v;
         const uint32_t of = head < a.heads ? a.heads : a.kv_heads, index = head < a.heads ? head : (head - a.heads) % a.kv_heads;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) store_run<IN>(out, (token * of + index) * DIM + run[i] * 8, y[i]);
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) store_piece<IN>(out, (token * of + index) * DIM + at[i][j], y[i][j]);
     }
 }
 
 template <int DIM, int IN>
 hipError_t launch(const RotateCall& a, uint32_t groups, hipStream_t st) {
     if (a.interleaved) return launch_threads(norm_rotate_kernel<DIM, IN, kNeighbours>, groups, kThreads, st, a);
-    if (a.pairs % 8 == 0) return launch_threads(norm_rotate_kernel<DIM, IN, kHalves>, groups, kThreads, st, a);
+    if (a.pairs % kPiece<IN> == 0) return launch_threads(norm_rotate_kernel<DIM, IN, kHalves>, groups, kThreads, st, a);
     return launch_threads(norm_rotate_kernel<DIM, IN, kSplitHalves>, groups, kThreads, st, a);
 }
 
