@@ -12,6 +12,8 @@
 #include <float.h>
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "qar_kv8_device.h"
 
 namespace qar {
@@ -34,35 +36,38 @@ struct SharedArgs {
 // ---------------------------------------------------------------------------
 // which rows and pages
 
-__device__ __forceinline__ uint32_t start_of(const SharedArgs& a, uint32_t g) {
-    return (uint32_t)clamp_length(a.starts[g], a.c.batch);
-}
+// A group's sequences, and the pages that they have in common.
+struct Group {
+    uint32_t start, end, pages;
+};
 
-// How many of `count` ascending things f(i) are at most `top`; a wave looks at
-// 64 at once.
+// The last group with first(start, g) <= top, where first ascends; {0, 0, 0}
+// if there is none.  A wave looks at 64 groups at once, and at all that it
+// may want of them, so that one load follows no other.
 template <class F>
-__device__ __forceinline__ uint32_t count_up_to(uint32_t count, uint32_t top, F f) {
+__device__ __forceinline__ Group last_group(const SharedArgs& a, uint32_t top, uint32_t& index, F first) {
     const uint32_t lane = threadIdx.x % 64;
-    uint32_t n = 0;
-    for (uint32_t base = 0; base < count; base += 64) {
-        const uint64_t mask = __ballot(base + lane < count && f(min(base + lane, count - 1)) <= top);
-        n += (uint32_t)__builtin_popcountll(mask);
+    Group found = {0, 0, 0};
+    for (uint32_t base = 0; base < a.groups; base += 64) {
+        const uint32_t g = min(base + lane, a.groups - 1);
+        const uint32_t start = (uint32_t)clamp_length(a.starts[g], a.c.batch), end = (uint32_t)clamp_length(a.starts[g + 1], a.c.batch);
+        const uint32_t pages = (uint32_t)clamp_length(a.prefix[g], a.c.width * kPage) / kPage;
+        const uint64_t mask = __ballot(base + lane < a.groups && first(start, g) <= top);
+        if (!mask) break;
+        const int i = 63 - __builtin_clzll(mask);
+        found = Group{(uint32_t)__builtin_amdgcn_readlane((int)start, i), (uint32_t)__builtin_amdgcn_readlane((int)end, i),
+                      (uint32_t)__builtin_amdgcn_readlane((int)pages, i)};
+        index = base + i;
         if (~mask) break;
     }
-    return n;
-}
-
-// Pages that group g's sequences have in common.
-__device__ __forceinline__ uint32_t prefix_pages(const SharedArgs& a, uint32_t g) {
-    return (uint32_t)clamp_length(a.prefix[g], a.c.width * kPage) / kPage;
+    return found;
 }
 
 // Pages before sequence b's own.
 __device__ __forceinline__ uint32_t pages_before(const SharedArgs& a, uint32_t b) {
-    const uint32_t n = count_up_to(a.groups, b, [&](uint32_t g) { return start_of(a, g); });
-    if (n == 0) return 0;
-    const uint32_t end = start_of(a, n), pages = prefix_pages(a, n - 1);
-    return b < end ? pages : 0;
+    uint32_t index;
+    const Group g = last_group(a, b, index, [](uint32_t start, uint32_t) { return start; });
+    return b < g.end ? g.pages : 0;
 }
 
 // `pages` cut into at most `slots` slots.
@@ -89,40 +94,35 @@ struct Work {
     uint32_t head, slot, first_seq, first_row, row_count;
     uint32_t first, last;                // pages
     bool any;
-    __device__ __forceinline__ Work(const SharedArgs& a, uint32_t unit, uint32_t tile_rows) {
-        const uint32_t prefix_units = a.prefix_tiles * a.c.heads * a.prefix_slots;
-        any = false;
-        if (unit < prefix_units) {
-            slot = unit % a.prefix_slots;
-            head = unit / a.prefix_slots % a.c.heads;
-            // group g's tiles begin at g plus the whole tiles of all rows before it: room for a last, partial tile of each
-            const uint32_t tile = unit / a.prefix_slots / a.c.heads;
-            const auto first_tile = [&](uint32_t g) { return (uint32_t)((uint64_t)start_of(a, g) * a.rows / tile_rows) + g; };
-            const uint32_t g = count_up_to(a.groups, tile, first_tile) - 1;   // the first group's begin at or before tile 0 ...
-            if (g >= a.groups) return;                                        // ... if no sequences are before it
-            first_seq = start_of(a, g);
-            const uint32_t end = start_of(a, g + 1), pages = prefix_pages(a, g);
-            row_count = end > first_seq ? (end - first_seq) * a.rows : 0;
-            first_row = (tile - first_tile(g)) * tile_rows;
-            const Cut cut(pages, a.prefix_slots);
-            first = slot * cut.per;
-            last = min(first + cut.per, pages);
-            any = first_row < row_count && first < last;
-        } else {
-            unit -= prefix_units;
-            const uint32_t of_slot = unit % a.own_slots, rest = unit / a.own_slots;
-            slot = a.prefix_slots + of_slot;
-            head = rest % a.c.heads;
-            first_seq = rest / a.c.heads % a.c.batch;
-            first_row = (a.own_tiles - 1 - rest / a.c.heads / a.c.batch) * tile_rows;   // the longest first
-            row_count = a.rows;
-            const uint32_t before = pages_before(a, first_seq);
-            const uint32_t pages = (uint32_t)(clamp_length(a.c.lengths[first_seq], a.c.width * kPage) + kPage - 1) / kPage;
-            const Cut cut(pages > before ? pages - before : 0, a.own_slots);
-            first = before + of_slot * cut.per;
-            last = min(first + cut.per, pages);
-            any = first < last;
-        }
+    __device__ __forceinline__ void of_prefix(const SharedArgs& a, uint32_t unit, uint32_t tile_rows) {
+        slot = unit % a.prefix_slots;
+        head = unit / a.prefix_slots % a.c.heads;
+        // group g's tiles begin at g plus the whole tiles of all rows before it: room for a last, partial tile of each
+        const uint32_t tile = unit / a.prefix_slots / a.c.heads;
+        const auto first_tile = [&](uint32_t start, uint32_t g) { return (uint32_t)((uint64_t)start * a.rows / tile_rows) + g; };
+        uint32_t index = 0;
+        const Group g = last_group(a, tile, index, first_tile);
+        first_seq = g.start;
+        row_count = g.end > g.start ? (g.end - g.start) * a.rows : 0;
+        first_row = (tile - first_tile(g.start, index)) * tile_rows;
+        const Cut cut(g.pages, a.prefix_slots);
+        first = slot * cut.per;
+        last = min(first + cut.per, g.pages);
+        any = first_row < row_count && first < last;
+    }
+    __device__ __forceinline__ void of_own(const SharedArgs& a, uint32_t unit, uint32_t tile_rows) {
+        const uint32_t of_slot = unit % a.own_slots, rest = unit / a.own_slots;
+        slot = a.prefix_slots + of_slot;
+        head = rest % a.c.heads;
+        first_seq = rest / a.c.heads % a.c.batch;
+        first_row = (a.own_tiles - 1 - rest / a.c.heads / a.c.batch) * tile_rows;   // the longest first
+        row_count = a.rows;
+        const int32_t n = clamp_length(a.c.lengths[first_seq], a.c.width * kPage);
+        const uint32_t before = pages_before(a, first_seq), pages = (uint32_t)(n + kPage - 1) / kPage;
+        const Cut cut(pages > before ? pages - before : 0, a.own_slots);
+        first = before + of_slot * cut.per;
+        last = min(first + cut.per, pages);
+        any = first < last;
     }
 };
 
@@ -154,13 +154,17 @@ __device__ __forceinline__ int32_t lanes16_min(int32_t v) {
 // few rows: a wave takes a page at a time, from memory to registers (the
 // layout of kv8_attend_few_kernel, qar_kv8.hip).
 
-template <int DIM, int MT, int IN, int NW>
-__global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_shared_few_kernel(SharedArgs a, uint32_t first_unit) {
+constexpr int kFewWaves = 4;
+
+template <int DIM>
+constexpr int kFewLds = kFewWaves * 16 * (DIM + 4) * 4 + 2 * kFewWaves * 16 * 4 + 16 * 8;
+
+template <int DIM, int MT, int IN>
+__device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work, char* lds) {
+    constexpr int NW = kFewWaves;
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int KC = DIM / 64, VC = DIM / 16;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
-    const Work work(a, first_unit + blockIdx.x, 16 * MT);
-    if (!work.any) return;
     const uint32_t h = work.head, first = work.first, last = work.last;
     int32_t my_id;
     float my_ks, my_vs;
@@ -308,9 +312,9 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_sh
     }
 
     // the waves' results meet in LDS, 16 rows at a time
-    __shared__ float os[NW][16][DIM + 4];
-    __shared__ float tops[NW][16], totals[NW][16];
-    __shared__ size_t items[16];
+    size_t* items = reinterpret_cast<size_t*>(lds);
+    auto tops = reinterpret_cast<float (*)[16]>(lds + 16 * 8), totals = tops + NW;
+    auto os = reinterpret_cast<float (*)[16][DIM + 4]>(totals + NW);
 #pragma unroll
     for (int j = 0; j < MT; ++j) {
         const uint32_t row0 = work.first_row + j * 16;
@@ -347,46 +351,46 @@ __global__ __launch_bounds__(NW * 64, DIM == 256 || MT == 2 ? 1 : 2) void kv8_sh
 // kv8_attend_many_kernel, qar_kv8.hip).
 
 constexpr int kTileRows = 128;
+constexpr int kAhead = 6;
+
+// The order of a chain of N products of T terms and the LDS reads before them,
+// which the compiler would otherwise put right before their use.
+template <int N, int T>
+__device__ __forceinline__ void lay_out_products() {
+    constexpr int kMatrix = 0x8, kLdsRead = 0x100;
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, kAhead, 0);
+#pragma unroll
+    for (int f = 0; f < N; ++f) {
+        __builtin_amdgcn_sched_group_barrier(kMatrix, T, 0);
+        if (f + kAhead < N) __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <int DIM>
+constexpr int kManyLds = kPage * DIM * 2 * 2 + kPage * DIM * 2;     // a page in binary16, and the next one's codes
 
 template <int DIM, int IN>
-__global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (IN == kInBF16 && DIM < 256))
-    void kv8_shared_many_kernel(SharedArgs a, uint32_t first_unit) {
+__device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& work, bool own, char* lds) {
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
     constexpr int KR = DIM / 8;                        // slots of a row of keys
     const auto k_swizzle = [](uint32_t row) { return DIM == 64 ? row / 2 % 8 : row % 16; };
-    __shared__ kv_half8 k_tile[kPage * KR], v_tile[DIM * 8];
-    __shared__ uint4 k_codes[U * kThreads], v_codes[U * kThreads];
+    auto k_tile = reinterpret_cast<kv_half8*>(lds), v_tile = k_tile + kPage * KR;
+    auto k_codes = reinterpret_cast<uint4*>(v_tile + DIM * 8), v_codes = k_codes + U * kThreads;
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), r = lane % 32,
                    g = lane / 32;
-    const Work work(a, first_unit + blockIdx.x, kTileRows);
-    if (!work.any) return;
     const uint32_t h = work.head, first = work.first;
     const uint32_t first_row = work.first_row + wave * 32;
-    const Row row(a, work, first_row + r);
-    Query<IN, DIM, 8, 16> raw;
-    raw.load(a.q, row.there ? row.query : 0, g * 8, row.there);
 
     // Own pages: only as far as the tile's last row sees.
     uint32_t last = work.last;
-    if (work.slot >= a.prefix_slots) {
+    if (own) {
         const Seq seq(a, work.first_seq);
         const int32_t i = min((int32_t)(min(work.first_row + kTileRows, a.rows) - 1) / (int32_t)a.group, seq.m - 1);
         const int32_t keys = seq.n - seq.m + i + 1;
         last = min(last, seq.m > 0 && keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u);
     }
-    // what the wave's rows see: all of them the keys below all_see, none a page from my_last on
-    int32_t all_see = row.there ? row.limit : INT32_MAX, most = row.there ? row.limit : 0;
-#pragma unroll
-    for (int d = 16; d; d /= 2) {
-        all_see = min(all_see, __shfl_xor(all_see, d));
-        most = max(most, __shfl_xor(most, d));
-    }
-    all_see = __builtin_amdgcn_readfirstlane(all_see);
-    most = __builtin_amdgcn_readfirstlane(most);
-    const uint32_t my_last = min(last, most > 0 ? (uint32_t)(most + kPage - 1) / kPage : 0u);
-    const int32_t limit = row.there ? row.limit : INT32_MAX;
-
     const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
     struct Page {
         int32_t id;
@@ -423,6 +427,21 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
     Page now = page_at(first), next = page_at(first + 1);
     fetch(now.id);
 
+    const Row row(a, work, first_row + r);
+    Query<IN, DIM, 8, 16> raw;
+    raw.load(a.q, row.there ? row.query : 0, g * 8, row.there);
+    // what the wave's rows see: all of them the keys below all_see, none a page from my_last on
+    int32_t all_see = row.there ? row.limit : INT32_MAX, most = row.there ? row.limit : 0;
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        all_see = min(all_see, __shfl_xor(all_see, d));
+        most = max(most, __shfl_xor(most, d));
+    }
+    all_see = __builtin_amdgcn_readfirstlane(all_see);
+    most = __builtin_amdgcn_readfirstlane(most);
+    const uint32_t my_last = min(last, most > 0 ? (uint32_t)(most + kPage - 1) / kPage : 0u);
+    const int32_t limit = row.there ? row.limit : INT32_MAX;
+
     kv_half8 q[DIM / 16][T];
     const float undo = raw.template convert<32, T>(a.negative, q) * a.scale;
 
@@ -455,14 +474,22 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
         if (page < my_last && now.id >= 0) {
             kv_f32x16 s[2];
             s[0] = s[1] = kv_f32x16{};
+            // fragments of both products are read kAhead products before they are used
+            constexpr int FK = DIM / 8;
+            kv_half8 kf[FK];
+            const auto read_k = [&](int f) {
+                kf[f] = *reinterpret_cast<const kv_half8*>((const char*)k_tile + (k_at ^ (f / 2 * 32)) + f % 2 * 32 * KR * 16);
+            };
 #pragma unroll
-            for (int c = 0; c < DIM / 16; ++c)
+            for (int f = 0; f < kAhead; ++f) read_k(f);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const kv_half8 k = *reinterpret_cast<const kv_half8*>((const char*)k_tile + (k_at ^ (c * 32)) + t * 32 * KR * 16);
+            for (int f = 0; f < FK; ++f) {
+                if (f + kAhead < FK) read_k(f + kAhead);
 #pragma unroll
-                    for (int e = 0; e < T; ++e) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[c][e], s[t], 0, 0, 0);
-                }
+                for (int e = 0; e < T; ++e)
+                    s[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[f], q[f / 2][e], s[f % 2], 0, 0, 0);
+            }
+            lay_out_products<FK, T>();
             const int32_t key0 = (int32_t)(page * kPage);
             const float shrink_all = unit.next(now.vs);
             if (shrink_all != 1.0f)
@@ -511,14 +538,22 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
             }
             total = __builtin_fmaf(sum, unit.drop, total);
             // neighbouring products add to different tiles: none waits for the one before it
+            constexpr int D = DIM / 32, FV = 4 * D;
+            kv_half8 vf[FV];
+            const auto read_v = [&](int f) {
+                vf[f] = *reinterpret_cast<const kv_half8*>((const char*)v_tile + (v_at ^ (f / D * 32)) + f % D * 32 * 128);
+            };
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int f = 0; f < kAhead; ++f) read_v(f);
 #pragma unroll
-                for (int d = 0; d < DIM / 32; ++d) {
-                    const kv_half8 v = *reinterpret_cast<const kv_half8*>((const char*)v_tile + (v_at ^ (u * 32)) + d * 32 * 128);
+            for (int f = 0; f < FV; ++f) {
+                if (f + kAhead < FV) read_v(f + kAhead);
 #pragma unroll
-                    for (int e = 0; e < T; ++e) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, p[u][e], o[d], 0, 0, 0);
-                }
+                for (int e = 0; e < T; ++e)
+                    o[f % D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[f], p[f / D][e], o[f % D], 0, 0, 0);
+            }
+            lay_out_products<FV, T>();
         }
         now = next, next = after;
     }
@@ -526,7 +561,7 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
 
     total = sum_over_32(total);
     if (first_row + r >= work.row_count) return;
-    const size_t at = row.item * (a.prefix_slots + a.own_slots) + work.slot;
+    const size_t at = Row(a, work, first_row + r).item * (a.prefix_slots + a.own_slots) + work.slot;
     // register k of tile d is channel 32 d + 8 (k / 4) + 4 g + k % 4
 #pragma unroll
     for (int d = 0; d < DIM / 32; ++d)
@@ -538,20 +573,63 @@ __global__ __launch_bounds__(kThreads, (DIM == 256 ? 1 : DIM == 128 ? 2 : 3) + (
 }
 
 // ---------------------------------------------------------------------------
-// a row's slots joined: DIM / 4 lanes with four channels each take a row.
+// the kernels: one form for both kinds of tiles, or many rows for the prefix
+// and few for the own pages.  The prefix comes first and leaves a CU half empty
+// (see `plan_for`); there the own pages, which wait for memory, run beside it:
+// 64 sequences of 32 heads x 128 behind 32,768 tokens 70 us, in two launches
+// 87, in turn eight by eight 93.
 
-template <int DIM, int OUT>
-__global__ __launch_bounds__(kThreads) void kv8_shared_join_kernel(SharedArgs a) {
-    constexpr int Q = DIM / 4, ROWS = kThreads / Q;
-    const uint32_t q = threadIdx.x % Q;
-    const size_t item = (size_t)blockIdx.x * ROWS + threadIdx.x / Q, all = (size_t)a.c.batch * a.c.heads * a.rows;
-    // a wave's rows may be of several sequences: each looks up its own
+enum : int { kFew = 0, kMany = 1, kManyFew = 2 };
+
+template <int DIM, int MT, int IN, int FORM>
+__global__ __launch_bounds__(kThreads, DIM == 256 || (FORM == kFew && MT == 2) ? 1 : 2)
+    void kv8_shared_kernel(SharedArgs a, uint32_t prefix_units) {
+    constexpr int BYTES = FORM == kFew ? kFewLds<DIM> : FORM == kMany ? kManyLds<DIM> : std::max(kFewLds<DIM>, kManyLds<DIM>);
+    __shared__ alignas(16) char lds[BYTES];
+    const bool own = blockIdx.x >= prefix_units;
+    const uint32_t unit = own ? blockIdx.x - prefix_units : blockIdx.x;
+    Work work;
+    if (own)
+        work.of_own(a, unit, FORM == kMany ? kTileRows : 16 * MT);
+    else
+        work.of_prefix(a, unit, FORM == kFew ? 16 * MT : kTileRows);
+    if (!work.any) return;
+    if constexpr (FORM == kFew) {
+        attend_few<DIM, MT, IN>(a, work, lds);
+    } else if constexpr (FORM == kMany) {
+        attend_many<DIM, IN>(a, work, own, lds);
+    } else {
+        if (own)
+            attend_few<DIM, MT, IN>(a, work, lds);
+        else
+            attend_many<DIM, IN>(a, work, false, lds);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// a row's slots joined: DIM / 4 lanes with four channels each take a row, or
+// GROUPS times as many, each time some of its slots.
+
+constexpr int kJoinRows = 8;                // rows times groups of a workgroup
+
+template <int DIM, int OUT, int GROUPS>
+__global__ __launch_bounds__(kJoinRows * DIM / 4) void kv8_shared_join_kernel(SharedArgs a) {
+    constexpr int Q = DIM / 4, ROWS = kJoinRows / GROUPS;
+    __shared__ kv_f32x4 ys[ROWS][GROUPS][Q];
+    __shared__ float tops[ROWS][GROUPS], totals[ROWS][GROUPS];
+    const uint32_t q = threadIdx.x % Q, group = threadIdx.x / Q % GROUPS, of_group = threadIdx.x / Q / GROUPS;
+    const size_t item = (size_t)blockIdx.x * ROWS + of_group, all = (size_t)a.c.batch * a.c.heads * a.rows;
     const size_t safe = min(item, all - 1);
     const uint32_t mine = safe % a.rows, bh = safe / a.rows, h = bh % a.c.heads, b = bh / a.c.heads;
+    // a wave's rows may be of several sequences: each is looked up by all of the wave
     uint32_t before = 0;
-    for (uint32_t lane = 0; lane < 64; lane += Q < 64 ? Q : 64) {
-        const uint32_t other = pages_before(a, __builtin_amdgcn_readlane(b, lane));
-        if (threadIdx.x % 64 / Q == lane / Q || Q >= 64) before = other;
+    if constexpr (GROUPS * Q >= 64) {
+        before = pages_before(a, __builtin_amdgcn_readfirstlane(b));
+    } else {
+        for (uint32_t lane = 0; lane < 64; lane += Q) {
+            const uint32_t other = pages_before(a, __builtin_amdgcn_readlane(b, lane));
+            if (threadIdx.x % 64 / Q == lane / Q) before = other;
+        }
     }
     const Seq seq(a, b);
     const int32_t i = (int32_t)(mine / a.group);
@@ -562,7 +640,7 @@ __global__ __launch_bounds__(kThreads) void kv8_shared_join_kernel(SharedArgs a)
     if (i < seq.m) {
         const uint32_t slots = a.prefix_slots + a.own_slots, count = prefix.used + own.used;
 #pragma unroll 4
-        for (uint32_t s = 0; s < count; ++s) {
+        for (uint32_t s = group; s < count; s += GROUPS) {
             const size_t at = safe * slots + (s < prefix.used ? s : a.prefix_slots + s - prefix.used);
             const float2 stat = *reinterpret_cast<const float2*>(a.stats + at * 2);
             const kv_f32x4 x = *reinterpret_cast<const kv_f32x4*>(a.part + at * DIM + q * 4);
@@ -571,6 +649,24 @@ __global__ __launch_bounds__(kThreads) void kv8_shared_join_kernel(SharedArgs a)
             l = __builtin_fmaf(stat.y, e, l * f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(x[k], e, y[k] * f);
+        }
+    }
+    if constexpr (GROUPS > 1) {
+        ys[of_group][group][q] = y;
+        if (q == 0) tops[of_group][group] = m, totals[of_group][group] = l;
+        __syncthreads();
+        if (group) return;
+        m = tops[of_group][0];
+#pragma unroll
+        for (int s = 1; s < GROUPS; ++s) m = fmaxf(m, tops[of_group][s]);
+        l = 0.0f;
+        y = kv_f32x4{};
+#pragma unroll
+        for (int s = 0; s < GROUPS; ++s) {
+            const float f = __builtin_amdgcn_exp2f(tops[of_group][s] - m);
+            l = __builtin_fmaf(totals[of_group][s], f, l);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __builtin_fmaf(ys[of_group][s][q][k], f, y[k]);
         }
     }
     if (item >= all) return;
@@ -604,15 +700,24 @@ uint32_t few_rows(int dim, uint32_t rows) { return dim == 256 || rows <= 16 ? 16
 bool is_few(int dim, size_t rows) { return rows <= (dim == 256 ? 16 : 32); }
 
 // How a call is cut.  Group sizes, prefixes and lengths are on the device; the
-// host goes by their averages and bounds.
+// host goes by their averages and bounds.  A slot more for a row is a row of
+// outputs more to write and to read again, so there are no more than fill the
+// CUs: of many rows one workgroup a CU with 128 or 256 channels (64 sequences
+// behind 32,768 tokens, 32 heads x 128: one 70 us, two 82, three 81; 16 heads x
+// 256, 32 sequences: 89, 99, 118), three with 64, whose pages are shorter (64
+// heads: 89, 76, 70); of few rows and of own pages one (eight sequences behind
+// 32,768 tokens 34 us, with two 45; 800 rows of four sequences each behind 8,000
+// tokens 135 and 160).  Where a slot would be more than 64 pages long, two
+// workgroups share a CU's units better than one uses them (64 sequences behind
+// 131,072 tokens 234 against 275 us).
 struct Plan {
     bool prefix_few, own_few;
     uint32_t prefix_rows, own_rows;      // of a tile
     uint32_t prefix_tiles, own_tiles, prefix_slots, own_slots;
 };
 
-uint32_t slots_for(size_t units, uint32_t width) {
-    const size_t want = (512 + units - 1) / units, most = (width + 3) / 4;
+uint32_t slots_for(size_t units, uint32_t width, size_t target) {
+    const size_t want = (target + units - 1) / units, most = (width + 3) / 4;
     return (uint32_t)(want < most ? want : most);
 }
 
@@ -623,11 +728,12 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
     p.prefix_rows = p.prefix_few ? few_rows(dim, (uint32_t)mean) : kTileRows;
     p.prefix_tiles = (uint32_t)(all / p.prefix_rows) + groups;
     const size_t likely = groups == 1 ? (all + p.prefix_rows - 1) / p.prefix_rows : (all / p.prefix_rows + (groups + 1) / 2);
-    p.prefix_slots = slots_for(likely * kv_heads, width);
+    p.prefix_slots = slots_for(likely * kv_heads, width, !p.prefix_few && dim == 64 ? 768 : 256);
+    if (!p.prefix_few && dim == 128 && width / p.prefix_slots > 64) p.prefix_slots *= 2;
     p.own_few = is_few(dim, rows);
     p.own_rows = p.own_few ? few_rows(dim, rows) : kTileRows;
     p.own_tiles = (rows + p.own_rows - 1) / p.own_rows;
-    p.own_slots = slots_for((size_t)batch * kv_heads * p.own_tiles, width);
+    p.own_slots = slots_for((size_t)batch * kv_heads * p.own_tiles, width, 256);
     return p;
 }
 
@@ -656,21 +762,27 @@ hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t que
         return with_kind(kind, [&](auto K) {
             const uint32_t prefix_units = p.prefix_tiles * c.heads * p.prefix_slots;
             const uint32_t own_units = c.batch * c.heads * p.own_tiles * p.own_slots;
-            const auto attend = [&](bool few, uint32_t tile, uint32_t first, uint32_t count) {
-                if (!few) return launch_threads(kv8_shared_many_kernel<D(), K()>, count, kThreads, st, a, first);
-                if (tile == 16) return launch_threads(kv8_shared_few_kernel<D(), 1, K(), 4>, count, kThreads, st, a, first);
-                return launch_threads(kv8_shared_few_kernel<D(), D() == 256 ? 1 : 2, K(), 4>, count, kThreads, st, a, first);
+            constexpr int two = D() == 256 ? 1 : 2;                      // tiles of 16 rows
+            const auto attend = [&](bool few, uint32_t rows, uint32_t prefix, uint32_t own) {
+                const auto go = [&](auto kernel) { return launch_threads(kernel, prefix + own, kThreads, st, a, prefix); };
+                if (!few) return go(kv8_shared_kernel<D(), 1, K(), kMany>);
+                return rows == 16 ? go(kv8_shared_kernel<D(), 1, K(), kFew>) : go(kv8_shared_kernel<D(), two, K(), kFew>);
             };
             hipError_t e;
             if (p.prefix_few == p.own_few && p.prefix_rows == p.own_rows) {
-                e = attend(p.own_few, p.own_rows, 0, prefix_units + own_units);
+                e = attend(p.own_few, p.own_rows, prefix_units, own_units);
+            } else if (!p.prefix_few && p.own_rows == 16) {
+                e = launch_threads(kv8_shared_kernel<D(), 1, K(), kManyFew>, prefix_units + own_units, kThreads, st, a,
+                                   prefix_units);
             } else {
-                e = attend(p.prefix_few, p.prefix_rows, 0, prefix_units);
-                if (e == hipSuccess) e = attend(p.own_few, p.own_rows, prefix_units, own_units);
+                e = attend(p.prefix_few, p.prefix_rows, prefix_units, 0);
+                if (e == hipSuccess) e = attend(p.own_few, p.own_rows, 0, own_units);
             }
             if (e != hipSuccess) return e;
-            constexpr size_t rows = kThreads / (D() / 4);
-            return launch_threads(kv8_shared_join_kernel<D(), K()>, (uint32_t)((items + rows - 1) / rows), kThreads, st, a);
+            return p.prefix_slots + p.own_slots > 4
+                       ? launch_threads(kv8_shared_join_kernel<D(), K(), kJoinRows>, (uint32_t)items, kJoinRows * D() / 4, st, a)
+                       : launch_threads(kv8_shared_join_kernel<D(), K(), 1>, (uint32_t)((items + kJoinRows - 1) / kJoinRows),
+                                        kJoinRows * D() / 4, st, a);
         });
     });
 }
