@@ -412,6 +412,19 @@ __device__ __forceinline__ void row_values(const T* x, size_t row_at, size_t col
     }
 }
 
+// The elements of 16 bytes.
+template <class T>
+__device__ __forceinline__ void values_of_16(uint4 q, float (&y)[16 / sizeof(T)]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 2)
+            y[2 * i] = bf16_lo(w[i]), y[2 * i + 1] = bf16_hi(w[i]);
+        else
+            y[i] = __builtin_bit_cast(float, w[i]);
+    }
+}
+
 // The activation of N values: which one is decided once for all.
 template <bool EXACT, int N>
 __device__ __forceinline__ void activate(float (&y)[N], int activation) {
@@ -424,9 +437,10 @@ __device__ __forceinline__ void activate(float (&y)[N], int activation) {
     case kActRelu: all([](float v) { return v < 0.0f ? 0.0f : v; }); break;
     case kActSilu: all([&](float v) { return over(v, 1.0f + exp_of<EXACT>(-v)); }); break;
     case kActGelu:
+        // v (1 - h) above 0, v h below
         all([](float v) {
             const float h = half_erfc<EXACT>(fabsf(v));
-            return v < 0.0f ? v * h : __builtin_fmaf(v, -h, v);
+            return __builtin_fmaf(-fabsf(v), h, v < 0.0f ? 0.0f : v);
         });
         break;
     case kActGeluTanh:
@@ -832,8 +846,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
             }
         }
     }
-    arrive<0>();                                    // nothing may write to LDS that is no longer this workgroup's
-
     // The weights are the first operand, so lane l = 32 h + r holds row r of a
     // subtile and its columns 8 q + 4 h .. + 3 in registers 4 q .. + 3.  They
     // pass through the wave's own stretch of LDS, a few subtiles of rows at a
@@ -850,9 +862,28 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     constexpr int NOW = std::min(STRIP / (32 * ROW), TM);
     static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
     constexpr int N = 16 / sizeof(T), PER = WN / N;  // columns of a lane, lanes to a row
+    constexpr int STORES = NOW * 32 * PER / 64, ALL = STORES * (TM / NOW);
+    const size_t col = n0 + wn * WN + lane % PER * N;
+    // A tile inside a bf16 output asks for all of its residual before it waits
+    // for the last loads to LDS (8192 x 5376 x 21504: 693 -> 625 us with GELU);
+    // binary32, twice the registers, four stores' worth at a time.
+    constexpr bool EARLY = EPILOGUE && sizeof(T) == 2;
+    constexpr int AT_ONCE = EPILOGUE && !EARLY ? 4 : STORES;
+    [[maybe_unused]] uint4 residual[EARLY ? ALL : 1];
+    const bool early = EARLY && a.residual && m0 + BM <= a.rows && n0 + BN <= a.cols;
+    const auto row_of = [&](int k) {                // of store k
+        return m0 + wm * WM + k / STORES * (NOW * 32) + k % STORES * (64 / PER) + lane / PER;
+    };
+    if (early) {
+#pragma unroll
+        for (int k = 0; k < ALL; ++k)
+            if constexpr (EARLY) __builtin_memcpy(&residual[k], (const T*)a.residual + row_of(k) * a.cols + col, 16);
+        arrive<ALL>();
+    } else {
+        arrive<0>();                                // nothing may write to LDS that is no longer this workgroup's
+    }
     const uint32_t home = wave / SHARE;
     char* strip = reinterpret_cast<char*>(home == 0 ? s0 : home == 1 ? s1 : home == 2 ? s2 : s3) + wave % SHARE * STRIP;
-    const size_t col = n0 + wn * WN + lane % PER * N;
     [[maybe_unused]] float bias[N] = {};
     if constexpr (EPILOGUE)
         if (a.bias) row_values<N>((const T*)a.bias, 0, col, a.cols, bias);
@@ -874,22 +905,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
                         *reinterpret_cast<mx_f32x4*>(to) = mx_f32x4{y0, y1, y2, y3};
                 }
         __builtin_amdgcn_wave_barrier();
-        constexpr int STORES = NOW * 32 * PER / 64, AT_ONCE = EPILOGUE ? 4 : STORES;
 #pragma unroll 1
         for (int k0 = 0; k0 < STORES; k0 += AT_ONCE) {
-            // an epilogue's reads of the residual are under way together
             [[maybe_unused]] float add[EPILOGUE ? AT_ONCE : 1][N] = {};
             if constexpr (EPILOGUE)
-                if (a.residual)
+                if (a.residual && !early)
 #pragma unroll
-                    for (int k = 0; k < AT_ONCE; ++k) {
-                        const size_t r = m0 + wm * WM + i0 * 32 + (k0 + k) * (64 / PER) + lane / PER;
-                        if (r < a.rows) row_values<N>((const T*)a.residual, r * a.cols, col, a.cols, add[k]);
-                    }
+                    for (int k = 0; k < AT_ONCE; ++k)
+                        if (row_of(i0 / NOW * STORES + k0 + k) < a.rows)
+                            row_values<N>((const T*)a.residual, row_of(i0 / NOW * STORES + k0 + k) * a.cols, col, a.cols, add[k]);
 #pragma unroll
             for (int k = 0; k < AT_ONCE; ++k) {
                 const uint32_t row = (k0 + k) * (64 / PER) + lane / PER;
-                const size_t r = m0 + wm * WM + i0 * 32 + row;
+                const size_t r = row_of(i0 / NOW * STORES + k0 + k);
                 const auto slot = [&](uint32_t c) {
                     return *reinterpret_cast<const uint4*>(strip + row * ROW + (c & ~7u) * 16 + ((c % 8 ^ row % 8) * 16));
                 };
@@ -897,6 +925,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
                 if constexpr (!EPILOGUE) {
                     v = slot(lane % PER);
                 } else {
+                    if constexpr (EARLY)
+                        if (early) values_of_16<T>(residual[i0 / NOW * STORES + k], add[k]);
                     float y[N];
 #pragma unroll
                     for (int e = 0; e < N; e += 4) {
