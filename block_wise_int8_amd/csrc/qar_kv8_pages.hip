@@ -77,15 +77,14 @@ __global__ __launch_bounds__(kThreads) void kv8_free_kernel(FreeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup of sixteen waves decides who gets which page: what a sequence
-// gets depends on what all before it took.  Its scans are ballots within a
-// wave and sixteen counts in LDS.
-
-constexpr int kScan = 1024, kWaves = kScan / 64;
+// One workgroup decides who gets which page: what a sequence gets depends on
+// what all before it took.  Its scans are shuffles within a wave and the waves'
+// counts in LDS.
 
 // This thread's offset among the threads' counts, in thread order, and their
 // sum.  `sums` is used again by the next call, after a barrier of its own.
-__device__ __forceinline__ uint32_t scan(uint32_t count, uint32_t& total, uint32_t (&sums)[kWaves]) {
+template <int WAVES>
+__device__ __forceinline__ uint32_t scan(uint32_t count, uint32_t& total, uint32_t (&sums)[WAVES]) {
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
     uint32_t sum = count;
 #pragma unroll
@@ -99,7 +98,7 @@ __device__ __forceinline__ uint32_t scan(uint32_t count, uint32_t& total, uint32
     uint32_t before = sum - count;
     total = 0;
 #pragma unroll
-    for (int v = 0; v < kWaves; ++v) {
+    for (int v = 0; v < WAVES; ++v) {
         before += (uint32_t)v < wave ? sums[v] : 0;
         total += sums[v];
     }
@@ -123,19 +122,31 @@ struct ReserveArgs {
 constexpr int kSequences = 4096;         // what the arrays below hold
 constexpr uint32_t kHasAll = ~0u, kLastOwner = ~1u;
 
-__global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
+// Four waves meet at a barrier sooner than sixteen, and meet a dozen times (64
+// beams: 7.8 against 8.6 us); more than 256 sequences take sixteen.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv8_reserve_kernel(ReserveArgs a) {
+    constexpr int RUN = 4096 / THREADS;           // neighbouring pages that a thread looks at
     __shared__ alignas(16) int32_t shared_page[kSequences];   // the page that a sequence goes on in, -1: at a page's start; -2: nowhere
     __shared__ uint32_t begin[kSequences + 1];    // of the sequence's looked-at entries, among all sequences'
     __shared__ uint32_t short_of[kSequences];     // the first page that it did not get, or one of the two above
-    __shared__ int32_t found[4 * kScan];          // free pages that nobody has taken yet
-    __shared__ uint32_t sums[kWaves];
+    __shared__ int32_t found[RUN * THREADS];      // free pages that nobody has taken yet
+    __shared__ uint32_t sums[THREADS / 64];
     const uint32_t tid = threadIdx.x;
+    // which of its pages from `first` on are free; the first are asked for at once
+    const auto look = [&](uint32_t first) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int k = 0; k < RUN; ++k) mask |= (uint32_t)(a.refs[min(first + RUN * tid + k, a.pages - 1)] <= 0 && first + RUN * tid + k < a.pages) << k;
+        return mask;
+    };
+    uint32_t free_mask = look(0);
     const auto length_of = [&](uint32_t b) { return clamp_length(a.lengths[b], a.width * kPage); };
     const auto end_of = [&](uint32_t b, uint32_t n) {
         return (uint32_t)min((uint64_t)n + (uint32_t)max(a.tokens[b], 0), (uint64_t)a.width * kPage);
     };
 
-    for (uint32_t b = tid; b < a.batch; b += kScan) {
+    for (uint32_t b = tid; b < a.batch; b += THREADS) {
         const uint32_t n = length_of(b), end = end_of(b, n);
         int32_t id = -1;
         if (end == n) {
@@ -152,7 +163,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
 
     // copies, and the entries that each sequence looks at
     uint32_t entries = 0;
-    for (uint32_t base = 0; base < a.batch; base += kScan) {
+    for (uint32_t base = 0; base < a.batch; base += THREADS) {
         const uint32_t b = base + tid;
         uint32_t count = 0;
         if (b < a.batch && shared_page[b] != -2) {
@@ -188,7 +199,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
     // front as far as they are needed
     bool ran_out = false;
     uint32_t next_page = 0, have = 0, taken = 0;  // pages looked at; found and not taken: found[taken .. taken + have)
-    for (uint32_t base = 0; base < entries; base += kScan) {
+    for (uint32_t base = 0; base < entries; base += THREADS) {
         const uint32_t e = base + tid;
         uint32_t b = 0, w = 0;
         bool copies = false, wants = false;
@@ -212,18 +223,13 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
         while (served < total) {
             if (have == 0) {
                 if (next_page >= a.pages) break;
-                // four neighbouring pages to a thread
-                uint32_t count = 0, mask = 0;
-                const uint32_t p0 = next_page + 4 * tid;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (p0 + k < a.pages && a.refs[p0 + k] <= 0) mask |= 1u << k, ++count;
+                if (next_page) free_mask = look(next_page);
                 uint32_t sum;
-                uint32_t at = scan(count, sum, sums);
+                uint32_t at = scan(__popc(free_mask), sum, sums);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (mask >> k & 1) found[at++] = (int32_t)(p0 + k);
-                next_page += 4 * kScan;
+                for (int k = 0; k < RUN; ++k)
+                    if (free_mask >> k & 1) found[at++] = (int32_t)(next_page + RUN * tid + k);
+                next_page += RUN * THREADS;
                 have = sum, taken = 0;
                 __syncthreads();
                 continue;
@@ -249,7 +255,7 @@ __global__ __launch_bounds__(kScan) void kv8_reserve_kernel(ReserveArgs a) {
         __syncthreads();
     }
 
-    for (uint32_t b = tid; b < a.batch; b += kScan) {
+    for (uint32_t b = tid; b < a.batch; b += THREADS) {
         const uint32_t n = length_of(b), end = end_of(b, n);
         const uint32_t lacks = short_of[b];
         uint32_t room = shared_page[b] == -2 ? 0 : end - n;
@@ -274,10 +280,10 @@ struct CompactArgs {
     size_t entries;                      // of the table
 };
 
-constexpr int kRun = 8;                  // neighbouring pages to a thread
+constexpr int kScan = 1024, kRun = 8;    // threads, neighbouring pages to each
 
 __global__ __launch_bounds__(kScan) void kv8_compact_kernel(CompactArgs a) {
-    __shared__ uint32_t sums[kWaves];
+    __shared__ uint32_t sums[kScan / 64];
     const uint32_t tid = threadIdx.x, half = a.pages / 2;
     uint32_t count = 0;
     for (uint32_t p = tid; p < a.pages; p += kScan) count += a.refs[p] > 0;
@@ -404,7 +410,8 @@ hipError_t launch_kv8_reserve(const Kv8& c, int32_t* refs, const int32_t* tokens
                               int32_t* target, hipStream_t st) {
     static_assert(kSequences == kKv8MaxSequences, "arrays");
     const ReserveArgs a = {const_cast<int32_t*>(c.table), refs, c.lengths, tokens, room, source, target, c.batch, c.width, c.pages};
-    return launch_threads(kv8_reserve_kernel, 1, kScan, st, a);
+    return c.batch <= 256 ? launch_threads(kv8_reserve_kernel<256>, 1, 256, st, a)
+                          : launch_threads(kv8_reserve_kernel<1024>, 1, 1024, st, a);
 }
 
 hipError_t launch_kv8_compact(const Kv8& c, int32_t* refs, int32_t* source, int32_t* target, hipStream_t st) {
