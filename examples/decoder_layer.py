@@ -1,5 +1,6 @@
-"""One decoder layer of a served model on libqar: 4-bit projections, an 8-bit
-paged cache, attention that remembers what it attended to, and eviction when a
+"""One decoder layer of a served model on libqar: 4-bit projections with their
+activations and residuals, normed and rotated queries and keys, an 8-bit paged
+cache, attention that remembers what it attended to, and eviction when a
 conversation outgrows its budget.
 
     python examples/decoder_layer.py            # on an MI355X
@@ -29,6 +30,9 @@ class DecoderLayer:
         self.qkv = weights((heads + 2 * kv_heads) * dim, hidden)
         self.out = weights(hidden, heads * dim)
         self.up, self.down = weights(4 * hidden, hidden), weights(hidden, 4 * hidden)
+        self.up_bias = (torch.randn(4 * hidden, generator=g, device="cuda") * 0.1).bfloat16()
+        self.q_gain, self.k_gain = ((1 + 0.1 * torch.randn(dim, generator=g, device="cuda")).bfloat16() for _ in range(2))
+        self.frequencies = 1e4 ** (-torch.arange(dim // 2, device="cuda", dtype=torch.float32) / (dim // 2))
         # two sets of pages in one pool: eviction moves from one to the other
         self.width = capacity // qar.QAR_KV8_PAGE
         self.cache = qar.KvCache.empty(2 * batch * self.width, kv_heads, dim, batch, self.width)
@@ -37,6 +41,7 @@ class DecoderLayer:
         self.spare = qar.KvCache(self.cache.k, self.cache.k_scales, self.cache.v, self.cache.v_scales, tables[1].clone(),
                                  torch.zeros_like(self.cache.lengths))
         self.received = torch.zeros((batch, kv_heads, capacity), device="cuda")   # what each token was attended to with
+        self.positions = torch.zeros_like(self.cache.lengths)             # tokens seen, kept or not
         self.longest = 0
 
     def evict(self, keep, recent):
@@ -50,36 +55,52 @@ class DecoderLayer:
     def step(self, x):
         """x [batch, tokens, hidden] (bf16) -> the layer's output, the new tokens in the cache."""
         batch, tokens, _ = x.shape
-        qkv = qar.qar_mx4_linear(x.reshape(batch * tokens, -1), *self.qkv).reshape(batch, tokens, -1, self.dim)
-        q, k, v = (t.contiguous() for t in qkv.split((self.heads, self.kv_heads, self.kv_heads), dim=2))
+        q, k, v = self.project(x, self.positions)
         starts = self.cache.lengths.clone()
         qar.qar_kv8_append(self.cache, starts, k, v)
         self.cache.lengths += tokens
+        self.positions += tokens
         self.longest += tokens
         attended = qar.qar_kv8_attention(self.cache, q, weights=self.received)
         self.last = q, attended
-        x = x + qar.qar_mx4_linear(attended.reshape(batch * tokens, -1), *self.out).reshape(x.shape)
-        up = qar.qar_mx4_linear(x.reshape(batch * tokens, -1), *self.up)
-        return x + qar.qar_mx4_linear(torch.nn.functional.silu(up), *self.down).reshape(x.shape)
+        return self.finish(x, attended)
+
+    def project(self, x, positions):
+        """x [batch, tokens, hidden] -> the queries, keys and values of its tokens, which begin at positions[b]."""
+        batch, tokens, _ = x.shape
+        qkv = qar.qar_mx4_linear(x.reshape(batch * tokens, -1), *self.qkv).reshape(batch, tokens, -1, self.dim)
+        return qar.qar_norm_rotate(qkv, self.heads, self.kv_heads, positions, self.frequencies, q_gain=self.q_gain,
+                                   k_gain=self.k_gain, eps=1e-6)
+
+    def finish(self, x, attended):
+        """The layer behind its attention."""
+        rows = x.reshape(-1, self.hidden)
+        rows = qar.qar_mx4_linear_fused(attended.reshape(rows.shape[0], -1), *self.out, residual=rows)
+        up = qar.qar_mx4_linear_fused(rows, *self.up, bias=self.up_bias, activation="silu")
+        return qar.qar_mx4_linear_fused(up, *self.down, residual=rows).reshape(x.shape)
 
     def attention_error(self):
-        """The last step's attention against a 64-bit softmax over the cache's values: the largest difference, relative to
-        the largest output."""
-        q, attended = self.last
-        batch, tokens, heads, _ = q.shape
-        n = int(self.cache.lengths.max())
-        k, v = (t.double() for t in qar.qar_kv8_read(self.cache, torch.zeros_like(self.cache.lengths), n, torch.float32))
-        group = heads // self.kv_heads
-        worst = size = 0.0
-        for b in range(batch):
-            m = int(self.cache.lengths[b])
-            hidden = torch.ones((tokens, m), dtype=torch.bool, device="cuda").triu(m - tokens + 1)
-            for h in range(heads):
-                s = (q[b, :, h].double() @ k[b, :m, h // group].T * self.dim ** -0.5).masked_fill(hidden, -torch.inf)
-                want = torch.softmax(s, 1) @ v[b, :m, h // group]
-                worst = max(worst, (attended[b, :, h].double() - want).abs().max().item())
-                size = max(size, want.abs().max().item())
-        return worst / size
+        """The last step's attention against a 64-bit softmax."""
+        return attention_error(self.cache, *self.last)
+
+
+def attention_error(cache, q, attended):
+    """Attention of q over a cache against a 64-bit softmax over the cache's values: the largest difference, relative to the
+    largest output."""
+    batch, tokens, heads, dim = q.shape
+    n = int(cache.lengths.max())
+    k, v = (t.double() for t in qar.qar_kv8_read(cache, torch.zeros_like(cache.lengths), n, torch.float32))
+    group = heads // k.shape[2]
+    worst = size = 0.0
+    for b in range(batch):
+        m = int(cache.lengths[b])
+        hidden = torch.ones((tokens, m), dtype=torch.bool, device="cuda").triu(m - tokens + 1)
+        for h in range(heads):
+            s = (q[b, :, h].double() @ k[b, :m, h // group].T * dim ** -0.5).masked_fill(hidden, -torch.inf)
+            want = torch.softmax(s, 1) @ v[b, :m, h // group]
+            worst = max(worst, (attended[b, :, h].double() - want).abs().max().item())
+            size = max(size, want.abs().max().item())
+    return worst / size
 
 
 def main(prompt=200, generate=160, capacity=256, keep=128, recent=32, seed=1):
