@@ -1287,7 +1287,8 @@ qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t
     qar_status st = check_owned(cache, refs);
     if (st != QAR_OK) return st;
     const size_t count = cache->batch;
-    if (keep) st = check_lists(CacheRanges(cache), cache, refs, &keep, &count, 1);
+    // a workgroup reads its sequence's keep before it writes the length
+    if (keep && keep != cache->lengths) st = check_lists(CacheRanges(cache), cache, refs, &keep, &count, 1);
     if (st != QAR_OK) return st;
     const hipError_t e = qar::launch_kv8_free(kernel_cache(cache), refs, keep, (hipStream_t)stream);
     return e == hipSuccess ? QAR_OK : hip_fail(e, "qar_kv8_free");

@@ -1085,7 +1085,8 @@ def _why_kv8_fork(cache, refs, parents, into):
 
 
 def qar_kv8_free(cache: KvCache, refs: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> None:
-    """Every sequence is cut to its first keep[b] (int32[batch]; default: no) tokens; the pages behind them are released."""
+    """Every sequence is cut to its first keep[b] (int32[batch]; default: no) tokens; the pages behind them are released.
+    ``cache.lengths`` as ``keep`` releases only what was given ahead."""
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_free(cache, refs, keep)

@@ -669,7 +669,8 @@ qar_status qar_kv8_fork(const qar_kv8_cache* cache, int32_t* refs, const int32_t
 /*
  * free: every sequence is cut to its first min(lengths[b], max(keep[b], 0))
  * tokens (to none where keep is NULL).  Pages wholly behind them, those given
- * ahead among them, are released and their entries become -1.
+ * ahead among them, are released and their entries become -1.  keep may be
+ * cache->lengths itself: then only what was given ahead is released.
  */
 qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t* keep, void* stream);
 /*
@@ -678,7 +679,8 @@ qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t
  * gets a page in its place: source[b] and target[b] are then the two, whose
  * content the caller copies (qar_kv8_copy) before it appends; otherwise both
  * are -1.  Behind its last page every page up to lengths[b] + tokens[b] that is
- * not there is given.  Pages are taken lowest free number first.  When none is
+ * not there is given; those that are there count as its own, so a sequence that
+ * is to lose tokens is cut back with qar_kv8_free and not by its length alone.  Pages are taken lowest free number first.  When none is
  * left a sequence keeps what it got.  lengths are not changed.
  *   tokens   [in]  int32[batch]; below 1 counts as none.
  *   room     [out] int32[batch]: for how many tokens there is room now, at most

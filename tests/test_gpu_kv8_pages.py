@@ -124,6 +124,15 @@ def test_random_calls(seed):
             books.lengths = [n + t for n, t in zip(books.lengths, take.tolist())]
 
 
+def test_free_what_was_given_ahead():
+    """The lengths themselves as what is kept."""
+    books = Books(30, [[3, 4, 5, 6], [7, -1, 8, -1], [9, 10, -1, -1]], [70, 64, 0])
+    qar.qar_kv8_free(books.cache, books.refs, books.cache.lengths)
+    ref.free(books.table, books.lengths, books.host_refs, list(books.lengths))
+    books.check("free")
+    assert books.table == [[3, 4, -1, -1], [7, -1, -1, -1], [-1] * 4]
+
+
 def test_reserve_from_one_to_many():
     """Sixty-four go on in one page: all but the last copy it; with other owners besides, the last as well."""
     for others in (0, 1):
