@@ -367,8 +367,19 @@ __device__ __forceinline__ void lay_out_products() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DIM>
-constexpr int kManyLds = kPage * DIM * 2 * 2 + kPage * DIM * 2;     // a page in binary16, and the next one's codes
+// Where a tile's pages end: own ones only as far as its last row sees.
+__device__ __forceinline__ uint32_t pages_end(const SharedArgs& a, const Work& work, bool own) {
+    if (!own) return work.last;
+    const Seq seq(a, work.first_seq);
+    const int32_t i = min((int32_t)(min(work.first_row + kTileRows, a.rows) - 1) / (int32_t)a.group, seq.m - 1);
+    const int32_t keys = seq.n - seq.m + i + 1;
+    return min(work.last, seq.m > 0 && keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u);
+}
+
+template <int DIM, int IN>
+constexpr bool kScoresAhead = DIM == 128 && IN == kInBF16;
+template <int DIM, int IN>         // a page in binary16 and the next one's codes, or two in binary16
+constexpr int kManyLds = kPage * DIM * 2 * (kScoresAhead<DIM, IN> ? 4 : 3);
 
 template <int DIM, int IN>
 __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& work, bool own, char* lds) {
@@ -383,14 +394,7 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     const uint32_t h = work.head, first = work.first;
     const uint32_t first_row = work.first_row + wave * 32;
 
-    // Own pages: only as far as the tile's last row sees.
-    uint32_t last = work.last;
-    if (own) {
-        const Seq seq(a, work.first_seq);
-        const int32_t i = min((int32_t)(min(work.first_row + kTileRows, a.rows) - 1) / (int32_t)a.group, seq.m - 1);
-        const int32_t keys = seq.n - seq.m + i + 1;
-        last = min(last, seq.m > 0 && keys > 0 ? (uint32_t)(keys + kPage - 1) / kPage : 0u);
-    }
+    const uint32_t last = pages_end(a, work, own);
     const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
     struct Page {
         int32_t id;
@@ -572,6 +576,248 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
 }
 
+// The same a page ahead: the scores of the next page are formed between the
+// exponentials of this one, the next codes go into the other half of LDS between
+// the products with the values, and one barrier a page is enough.  A wave has
+// its matrix and its vector instructions side by side that way, which a second
+// workgroup on the CU gives the other bodies.  For bf16 and 128 channels only:
+// 64 leave too few products to hide the exponentials behind (8 prompts x 8
+// sequences 28.7 -> 33.5 us), 256 and fp32 have no registers for a second page.
+// 64 sequences behind 32,768 tokens 78.4 -> 72.1 us, 65,536 tokens 130 -> 115
+// us in this kernel, 800 query rows a head 172 -> 166 us, from four pages a
+// workgroup on no worse.
+
+template <int DIM, int IN>
+__device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Work& work, bool own, char* lds) {
+    constexpr int U = DIM / 64;                        // 16-byte loads of a thread, keys and values each
+    constexpr int KR = DIM / 8;                        // slots of a row of keys
+    constexpr int FK = DIM / 8, FV = DIM / 8, D = DIM / 32;   // fragments of keys, of values; tiles of outputs
+    constexpr int AHEAD = 4;
+    enum : int { kVector = 0x2, kMatrix = 0x8, kLdsRead = 0x100, kLdsWrite = 0x200, kExp = 0x400 };
+    static_assert(kScoresAhead<DIM, IN>);
+    const auto k_swizzle = [](uint32_t row) { return row % 16; };
+    constexpr int BYTES = kPage * DIM * 2;             // of a page's keys, or values
+    const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64), r = lane % 32,
+                   g = lane / 32;
+    const uint32_t h = work.head, first = work.first;
+    const uint32_t first_row = work.first_row + wave * 32;
+    const uint32_t last = pages_end(a, work, own);
+    const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
+    struct Page {
+        int32_t id;
+        float ks, vs;          // 0 for a page that is not there
+    };
+    uint32_t base = first;
+    int32_t my_id;
+    float my_ks, my_vs;
+    auto look_up = [&] {
+        my_id = valid_page(table[min(base + lane, work.last - 1)], a.c.pages);
+        const size_t at = (size_t)max(my_id, 0) * a.c.heads + h;
+        my_ks = a.c.k_scales[at], my_vs = a.c.v_scales[at];
+        __builtin_amdgcn_s_waitcnt(0x0f70);            // the loads: here, not before every use
+        if (my_id < 0) my_ks = my_vs = 0.0f;
+    };
+    auto page_at = [&](uint32_t page) {
+        if (page - base >= 64) {
+            base = page;
+            look_up();
+        }
+        const uint32_t i = page - base;
+        return Page{__builtin_amdgcn_readlane(my_id, i),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i)),
+                    __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i))};
+    };
+    uint4 kr[U], vr[U];
+    auto fetch = [&](const int8_t* codes, int32_t id, uint4 (&to)[U]) {
+        const int8_t* from = codes + ((size_t)max(id, 0) * a.c.heads + h) * (kPage * DIM) + tid * 16;
+#pragma unroll
+        for (int u = 0; u < U; ++u) to[u] = *reinterpret_cast<const uint4*>(from + u * kThreads * 16);
+    };
+    auto write_k = [&](int buffer) {
+        auto k_tile = reinterpret_cast<kv_half8*>(lds + buffer * BYTES);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid;
+            const uint32_t key = i / (DIM / 16), lr = exchange_bits_2_3(key), c = i % (DIM / 16) * 2;
+            k_tile[lr * KR + (c ^ k_swizzle(lr))] = half_codes(kr[u].x, kr[u].y);
+            k_tile[lr * KR + ((c + 1) ^ k_swizzle(lr))] = half_codes(kr[u].z, kr[u].w);
+        }
+    };
+    auto write_v = [&](int buffer) {
+        auto v_tile = reinterpret_cast<kv_half8*>(lds + (2 + buffer) * BYTES);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = u * kThreads + tid, d = i / 4, e = i % 4 * 2;
+            v_tile[d * 8 + (e ^ d / 2 % 8)] = half_codes(vr[u].x, vr[u].y);
+            v_tile[d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
+        }
+    };
+    look_up();
+    Page now = page_at(first), next = page_at(first + 1), after = page_at(first + 2);
+    fetch(a.c.k, now.id, kr);
+    fetch(a.c.v, now.id, vr);
+
+    kv_half8 q[DIM / 16][1];
+    float undo;
+    int32_t limit, all_see;
+    {
+        const Row row(a, work, first_row + r);
+        Query<IN, DIM, 8, 16> raw;
+        raw.load(a.q, row.there ? row.query : 0, g * 8, row.there);
+        limit = row.there ? row.limit : INT32_MAX;
+        all_see = limit;
+#pragma unroll
+        for (int d = 16; d; d /= 2) all_see = min(all_see, __shfl_xor(all_see, d));
+        all_see = __builtin_amdgcn_readfirstlane(all_see);
+        undo = raw.template convert<32, 1>(a.negative, q) * a.scale;
+    }
+    const uint32_t k_first = r * (KR * 16) + (g ^ k_swizzle(r)) * 16, v_first = r * 128 + (g ^ r / 2 % 8) * 16;
+    uint32_t k_at = k_first, v_at = v_first;
+    auto k_fragment = [&](int buffer, int f) {
+        return *reinterpret_cast<const kv_half8*>(lds + buffer * BYTES + (k_at ^ (f / 2 * 32)) + f % 2 * 32 * KR * 16);
+    };
+    auto v_fragment = [&](int buffer, int f) {
+        return *reinterpret_cast<const kv_half8*>(lds + (2 + buffer) * BYTES + (v_at ^ (f / D * 32)) + f % D * 32 * 128);
+    };
+
+    kv_f32x16 o[D] = {};
+    Unit unit;
+    float top = -FLT_MAX, total = 0.0f;
+    kv_f32x16 s0[2] = {}, s1[2];                       // scores of even and odd pages, counted from the first
+    write_k(0);
+    fetch(a.c.k, next.id, kr);
+    write_v(0);
+    fetch(a.c.v, next.id, vr);
+    lds_barrier();
+#pragma unroll
+    for (int f = 0; f < FK; ++f) s0[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_fragment(0, f), q[f / 2][0], s0[f % 2], 0, 0, 0);
+    write_k(1);
+    fetch(a.c.k, after.id, kr);
+    lds_barrier();
+
+    // Enters with page's scores in s, its values and the next page's keys in LDS
+    // and the codes of the next values and the keys after them in registers.
+    uint32_t page = first;
+    auto step = [&](auto PARITY, kv_f32x16 (&s)[2], kv_f32x16 (&s_next)[2]) {
+        constexpr int even = decltype(PARITY)::value, odd = 1 - even;
+        const int32_t key0 = (int32_t)(page * kPage);
+        float factor = now.ks * undo;
+        if (key0 + kPage > all_see || now.id < 0) {
+            const int32_t sees = (now.id < 0 ? 0 : limit) - key0 - (int32_t)g * 8;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    s[t][k] = 32 * t + 16 * (k / 8) + k % 8 < sees ? s[t][k] * factor : -INFINITY;
+            factor = 1.0f;
+        }
+        // new to the compiler at each page: it would keep an address for every fragment
+        k_at = k_first, v_at = v_first;
+        asm volatile("" : "+v"(k_at), "+v"(v_at));
+        constexpr int N1 = FK / 4;
+        kv_half8 kf[FK];
+        s_next[0] = s_next[1] = kv_f32x16{};
+#pragma unroll
+        for (int f = 0; f < AHEAD; ++f) kf[f] = k_fragment(odd, f);
+#pragma unroll
+        for (int f = 0; f < N1; ++f) {
+            if (f + AHEAD < FK) kf[f + AHEAD] = k_fragment(odd, f + AHEAD);
+            s_next[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[f], q[f / 2][0], s_next[f % 2], 0, 0, 0);
+        }
+        float m = max3(s[0][15], s[1][15], s[0][14]);
+        float m1 = max3(s[1][14], s[0][13], s[1][13]);
+#pragma unroll
+        for (int k = 0; k < 12; k += 2) {
+            m = max3(m, s[0][k], s[0][k + 1]);
+            m1 = max3(m1, s[1][k], s[1][k + 1]);
+        }
+        m = max3(m, s[0][12], s[1][12]);
+        m = fmaxf(max_over_32(fmaxf(m, m1)) * factor, top);
+        const float shrink_all = unit.next(now.vs);
+        if (__any(m > top + 1.5f) || shrink_all != 1.0f) {
+            const float grown = m > top + 1.5f ? m : top, shrink = __builtin_amdgcn_exp2f(top - grown);
+            total *= shrink;
+#pragma unroll
+            for (int d = 0; d < D; ++d) o[d] *= shrink * shrink_all;
+            top = grown;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const float off = unit.lift - top;
+        kv_half8 p[4][1];
+        float sum = 0.0f;
+#pragma unroll
+        for (int f = N1; f < FK; ++f) {
+            if (f + AHEAD < FK) kf[f + AHEAD] = k_fragment(odd, f + AHEAD);
+            s_next[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[f], q[f / 2][0], s_next[f % 2], 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u / 2][u % 2 * 8 + k], factor, off));
+            sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            half_terms<1>(x, p[u]);
+        }
+        total = __builtin_fmaf(sum, unit.drop, total);
+        constexpr int N2 = FK - N1;
+#pragma unroll
+        for (int f = N1; f < FK; ++f) {
+            __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+            if (f + AHEAD < FK) __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kVector, (32 + N2 - 1) / N2, 0);
+            __builtin_amdgcn_sched_group_barrier(kExp, (32 + N2 - 1) / N2, 0);
+            __builtin_amdgcn_sched_group_barrier(kVector, 52 / N2, 0);
+        }
+        // the numerators are wanted here, not where they are used
+        asm volatile("" : "+v"(p[0][0]), "+v"(p[1][0]), "+v"(p[2][0]), "+v"(p[3][0]), "+v"(total));
+        __builtin_amdgcn_sched_barrier(0);
+        const Page last_but = page_at(page + 3);
+        __builtin_amdgcn_sched_barrier(0);
+        kv_half8 vf[FV];
+#pragma unroll
+        for (int f = 0; f < AHEAD; ++f) vf[f] = v_fragment(even, f);
+#pragma unroll
+        for (int f = 0; f < FV; ++f) {
+            if (f + AHEAD < FV) vf[f + AHEAD] = v_fragment(even, f + AHEAD);
+            o[f % D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[f], p[f / D][0], o[f % D], 0, 0, 0);
+        }
+        write_k(even);
+        write_v(odd);
+        __builtin_amdgcn_sched_group_barrier(kLdsRead, AHEAD, 0);
+#pragma unroll
+        for (int f = 0; f < FV; ++f) {
+            __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+            if (f + AHEAD < FV) __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(kVector, 40 * U / FV, 0);
+            if (f % 2) __builtin_amdgcn_sched_group_barrier(kLdsWrite, 4 * U * 2 / FV, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(a.c.v, after.id, vr);
+        fetch(a.c.k, last_but.id, kr);
+        lds_barrier();                               // the next pages are there, these have been read
+        now = next, next = after, after = last_but;
+        ++page;
+    };
+    while (page + 1 < last) {
+        step(std::integral_constant<int, 0>{}, s0, s1);
+        step(std::integral_constant<int, 1>{}, s1, s0);
+    }
+    if (page < last) step(std::integral_constant<int, 0>{}, s0, s1);
+
+    total = sum_over_32(total);
+    if (first_row + r >= work.row_count) return;
+    const size_t at = Row(a, work, first_row + r).item * (a.prefix_slots + a.own_slots) + work.slot;
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<kv_f32x4*>(a.part + at * DIM + d * 32 + k * 2 + g * 4) =
+                kv_f32x4{o[d][k], o[d][k + 1], o[d][k + 2], o[d][k + 3]} * unit.unit;
+    if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
+}
+
+
 // ---------------------------------------------------------------------------
 // the kernels: one form for both kinds of tiles, or many rows for the prefix
 // and few for the own pages.  The prefix comes first and leaves a CU half empty
@@ -584,7 +830,8 @@ enum : int { kFew = 0, kMany = 1, kManyFew = 2 };
 template <int DIM, int MT, int IN, int FORM>
 __global__ __launch_bounds__(kThreads, DIM == 256 || (FORM == kFew && MT == 2) ? 1 : 2)
     void kv8_shared_kernel(SharedArgs a, uint32_t prefix_units) {
-    constexpr int BYTES = FORM == kFew ? kFewLds<DIM> : FORM == kMany ? kManyLds<DIM> : std::max(kFewLds<DIM>, kManyLds<DIM>);
+    constexpr int FEW = FORM == kMany ? 0 : kFewLds<DIM>, MANY = FORM == kFew ? 0 : kManyLds<DIM, IN>;
+    constexpr int BYTES = std::max(FEW, MANY);
     __shared__ alignas(16) char lds[BYTES];
     const bool own = blockIdx.x >= prefix_units;
     const uint32_t unit = own ? blockIdx.x - prefix_units : blockIdx.x;
@@ -594,15 +841,13 @@ __global__ __launch_bounds__(kThreads, DIM == 256 || (FORM == kFew && MT == 2) ?
     else
         work.of_prefix(a, unit, FORM == kFew ? 16 * MT : kTileRows);
     if (!work.any) return;
-    if constexpr (FORM == kFew) {
-        attend_few<DIM, MT, IN>(a, work, lds);
-    } else if constexpr (FORM == kMany) {
-        attend_many<DIM, IN>(a, work, own, lds);
-    } else {
-        if (own)
-            attend_few<DIM, MT, IN>(a, work, lds);
+    if (FORM == kFew || (FORM == kManyFew && own)) {
+        if constexpr (FORM != kMany) attend_few<DIM, MT, IN>(a, work, lds);
+    } else if constexpr (FORM != kFew) {
+        if constexpr (kScoresAhead<DIM, IN>)
+            attend_many_ahead<DIM, IN>(a, work, own, lds);
         else
-            attend_many<DIM, IN>(a, work, false, lds);
+            attend_many<DIM, IN>(a, work, own, lds);
     }
 }
 
