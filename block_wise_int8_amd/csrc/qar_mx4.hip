@@ -710,12 +710,14 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
-template <int OUT, int BM, int BN, int WM, int WN, bool EPILOGUE>
+template <int OUT, int BM, int BN, int WM, int WN, bool EPILOGUE, bool DEEP>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(LinearArgs a) {
     static_assert(BM == BN, "one size of buffer");
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
     constexpr int TM = WM / 32, TN = WN / 32, LOADS = BM * 8 / NT;
+    static_assert(!DEEP || BM == 64, "eight buffers, loads that arrive() can count");
     __shared__ uint4 s0[BM * 8], s1[BM * 8], s2[BM * 8], s3[BM * 8], s4[BM * 8];
+    __shared__ uint4 s5[DEEP ? BM * 8 : 1], s6[DEEP ? BM * 8 : 1], s7[DEEP ? BM * 8 : 1];
     const uint32_t tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const uint32_t wm = wave / (BN / WN), wn = wave % (BN / WN);
 
@@ -753,7 +755,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     const uint32_t* as_tile = reinterpret_cast<const uint32_t*>(a.x_scales) + (m0 + wm * WM) / 32 * chunks * 64 + lane;
     const uint32_t* bs_tile = reinterpret_cast<const uint32_t*>(a.w_tiles) + (n0 + wn * WN) / 32 * chunks * 64 + lane;
     int sa[TM], sb[TN];
-    auto fetch_scales = [&](uint32_t chunk) {
+    auto fetch_scales = [&](uint32_t chunk, int (&sa)[TM], int (&sb)[TN]) {
         const uint32_t c = min(chunk, chunks - 1);
 #pragma unroll
         for (int i = 0; i < TM; ++i) sa[i] = (int)as_tile[((size_t)i * chunks + c) * 64];
@@ -806,7 +808,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
         step(std::integral_constant<int, 1>{}, xs, ws, fx, fw, ca, cb, [&] {
 #pragma unroll
             for (int i = LOADS / 2; i < LOADS; ++i) fetch_w(c + 1, w_next, i);
-            fetch_scales(c + 1);
+            fetch_scales(c + 1, sa, sb);
             asm volatile("" ::: "memory");          // x last: what arrive() lets pass
         });
         step(std::integral_constant<int, 2>{}, xs, ws, fx, fw, ca, cb, [&] {
@@ -818,31 +820,116 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
             for (int i = LOADS / 2; i < LOADS; ++i) fetch_x(c + 2, x_after, i);
         });
     };
+    using T = std::conditional_t<OUT == kOutBF16, uint16_t, float>;
+    using S = std::conditional_t<EPILOGUE, float, T>;
+    // A buffer to a wave, or half of one: all are read out, and none is being written.
+    constexpr int ROW = WN * sizeof(S), SHARE = NT / 64 > 4 ? 2 : 1, STRIP = BM * 128 / SHARE;
+    constexpr int NOW = std::min(STRIP / (32 * ROW), TM);
+    static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
+    constexpr int N = 16 / sizeof(T), PER = WN / N;  // columns of a lane, lanes to a row
+    constexpr int STORES = NOW * 32 * PER / 64, ALL = STORES * (TM / NOW);
+    const size_t col = n0 + wn * WN + lane % PER * N;
+    // A tile inside a bf16 output's columns asks for all of its residual before it
+    // waits for the last loads to LDS (8192 x 5376 x 21504: 693 -> 625 us with
+    // GELU); binary32, twice the registers, four stores' worth at a time.  Small
+    // tiles, one wave to a SIMD, have registers enough to ask before their first
+    // chunk (300 x 5760 x 2880, binary32: 17.8 -> 17.1 us).
+    constexpr bool EARLY = EPILOGUE && (sizeof(T) == 2 || DEEP);
+    constexpr int AT_ONCE = EPILOGUE && !EARLY ? 4 : STORES;
+    [[maybe_unused]] uint4 residual[EARLY ? ALL : 1];
+    const bool early = EARLY && a.residual && n0 + BN <= a.cols;
+    const auto row_of = [&](int k) {                // of store k
+        return m0 + wm * WM + k / STORES * (NOW * 32) + k % STORES * (64 / PER) + lane / PER;
+    };
+    const auto ask_for_residual = [&] {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) fetch_x(0, s0, i);
+        for (int k = 0; k < ALL; ++k)
+            if constexpr (EARLY)                     // for rows behind the last, the last: it goes nowhere
+                __builtin_memcpy(&residual[k], (const T*)a.residual + std::min(row_of(k), a.rows - 1) * a.cols + col, 16);
+    };
+
+    if constexpr (DEEP) {
+        // A small tile's products of a chunk are over long before memory answers:
+        // three chunks are under way, in four pairs of buffers.  The sums are
+        // formed in the same order.
+        int da[4][TM], db[4][TN];
+        auto fetch = [&](uint32_t c, uint4* xs, uint4* ws, int (&ca)[TM], int (&cb)[TN]) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) fetch_w(0, s1, i);
-    fetch_scales(0);
-    asm volatile("" ::: "memory");
+            for (int i = 0; i < LOADS; ++i) fetch_x(c, xs, i);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) fetch_x(1, s2, i);
-    // Whole rounds of the buffers and then the rest, nested: where paths meet
-    // on which different loads are the last, the compiler would wait for all.
-    uint32_t c = 0;
-    for (; c + 5 <= chunks; c += 5) {
-        chunk(c, s0, s1, s3, s4);
-        chunk(c + 1, s2, s3, s0, s1);
-        chunk(c + 2, s4, s0, s2, s3);
-        chunk(c + 3, s1, s2, s4, s0);
-        chunk(c + 4, s3, s4, s1, s2);
-    }
-    if (c < chunks) {
-        chunk(c, s0, s1, s3, s4);
-        if (c + 1 < chunks) {
+            for (int i = 0; i < LOADS; ++i) fetch_w(c, ws, i);
+            fetch_scales(c, ca, cb);
+            asm volatile("" ::: "memory");          // whole chunks: what arrive() counts
+        };
+        constexpr int PER = 2 * LOADS + TM + TN;
+        auto products = [&](auto P, const uint4* xs, const uint4* ws) {
+            constexpr int p = decltype(P)::value;
+            step(std::integral_constant<int, 0>{}, xs, ws, fx0, fw0, da[p], db[p], [] {});
+            step(std::integral_constant<int, 1>{}, xs, ws, fx0, fw0, da[p], db[p], [] {});
+            step(std::integral_constant<int, 2>{}, xs, ws, fx0, fw0, da[p], db[p], [] {});
+            step(std::integral_constant<int, 3>{}, xs, ws, fx0, fw0, da[p], db[p], [] {});
+        };
+        auto deep_chunk = [&](auto P, uint32_t c, uint4* xs, uint4* ws, uint4* x_next, uint4* w_next) {
+            constexpr int before = (decltype(P)::value + 3) % 4;
+            arrive<2 * PER>();                      // all but chunks c + 1 and c + 2
+            fetch(c + 3, x_next, w_next, da[before], db[before]);
+            products(P, xs, ws);
+        };
+        if (early) ask_for_residual();
+        asm volatile("" ::: "memory");
+        fetch(0, s0, s1, da[0], db[0]);
+        fetch(1, s2, s3, da[1], db[1]);
+        fetch(2, s4, s5, da[2], db[2]);
+        constexpr std::integral_constant<int, 0> P0{};
+        constexpr std::integral_constant<int, 1> P1{};
+        constexpr std::integral_constant<int, 2> P2{};
+        constexpr std::integral_constant<int, 3> P3{};
+        uint32_t c = 0;
+        for (; c + 4 <= chunks; c += 4) {
+            deep_chunk(P0, c, s0, s1, s6, s7);
+            deep_chunk(P1, c + 1, s2, s3, s0, s1);
+            deep_chunk(P2, c + 2, s4, s5, s2, s3);
+            deep_chunk(P3, c + 3, s6, s7, s4, s5);
+        }
+        if (c < chunks) {
+            arrive<2 * PER>();
+            products(P0, s0, s1);
+            if (c + 1 < chunks) {
+                arrive<PER>();
+                products(P1, s2, s3);
+                if (c + 2 < chunks) {
+                    arrive<0>();
+                    products(P2, s4, s5);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) fetch_x(0, s0, i);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) fetch_w(0, s1, i);
+        fetch_scales(0, sa, sb);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) fetch_x(1, s2, i);
+        // Whole rounds of the buffers and then the rest, nested: where paths meet
+        // on which different loads are the last, the compiler would wait for all.
+        uint32_t c = 0;
+        for (; c + 5 <= chunks; c += 5) {
+            chunk(c, s0, s1, s3, s4);
             chunk(c + 1, s2, s3, s0, s1);
-            if (c + 2 < chunks) {
-                chunk(c + 2, s4, s0, s2, s3);
-                if (c + 3 < chunks) chunk(c + 3, s1, s2, s4, s0);
+            chunk(c + 2, s4, s0, s2, s3);
+            chunk(c + 3, s1, s2, s4, s0);
+            chunk(c + 4, s3, s4, s1, s2);
+        }
+        if (c < chunks) {
+            chunk(c, s0, s1, s3, s4);
+            if (c + 1 < chunks) {
+                chunk(c + 1, s2, s3, s0, s1);
+                if (c + 2 < chunks) {
+                    chunk(c + 2, s4, s0, s2, s3);
+                    if (c + 3 < chunks) chunk(c + 3, s1, s2, s4, s0);
+                }
             }
         }
     }
@@ -855,29 +942,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     // With an epilogue they pass as binary32: bias, activation and residual come
     // on the way out, where a lane's columns are the same for all of its rows and
     // the residual is read in whole lines, and the result is rounded once.
-    using T = std::conditional_t<OUT == kOutBF16, uint16_t, float>;
-    using S = std::conditional_t<EPILOGUE, float, T>;
-    // A buffer to a wave, or half of one: all are read out, and none is being written.
-    constexpr int ROW = WN * sizeof(S), SHARE = NT / 64 > 4 ? 2 : 1, STRIP = BM * 128 / SHARE;
-    constexpr int NOW = std::min(STRIP / (32 * ROW), TM);
-    static_assert(NOW > 0 && TM % NOW == 0 && NT / 64 <= 8 && ROW % 128 == 0, "strips");
-    constexpr int N = 16 / sizeof(T), PER = WN / N;  // columns of a lane, lanes to a row
-    constexpr int STORES = NOW * 32 * PER / 64, ALL = STORES * (TM / NOW);
-    const size_t col = n0 + wn * WN + lane % PER * N;
-    // A tile inside a bf16 output asks for all of its residual before it waits
-    // for the last loads to LDS (8192 x 5376 x 21504: 693 -> 625 us with GELU);
-    // binary32, twice the registers, four stores' worth at a time.
-    constexpr bool EARLY = EPILOGUE && sizeof(T) == 2;
-    constexpr int AT_ONCE = EPILOGUE && !EARLY ? 4 : STORES;
-    [[maybe_unused]] uint4 residual[EARLY ? ALL : 1];
-    const bool early = EARLY && a.residual && m0 + BM <= a.rows && n0 + BN <= a.cols;
-    const auto row_of = [&](int k) {                // of store k
-        return m0 + wm * WM + k / STORES * (NOW * 32) + k % STORES * (64 / PER) + lane / PER;
-    };
-    if (early) {
-#pragma unroll
-        for (int k = 0; k < ALL; ++k)
-            if constexpr (EARLY) __builtin_memcpy(&residual[k], (const T*)a.residual + row_of(k) * a.cols + col, 16);
+    if (!DEEP && early) {
+        ask_for_residual();
         arrive<ALL>();
     } else {
         arrive<0>();                                // nothing may write to LDS that is no longer this workgroup's
@@ -986,11 +1052,11 @@ hipError_t few_rows(const LinearArgs& a, hipStream_t st) {
     return launch_threads(mx4_few_rows_kernel<IN, MT, 1, NW, FUSED, EPILOGUE>, groups_for(a.cols, 16), NW * 64, st, a);
 }
 
-template <int IN, int BM, int BN, int WM, int WN, bool EPILOGUE>
+template <int OUT, int BM, int BN, int WM, int WN, bool EPILOGUE, bool DEEP = false>
 hipError_t tiled(LinearArgs& a, hipStream_t st) {
     a.row_tiles = groups_for(a.rows, BM);
     a.col_tiles = groups_for(a.cols, BN);
-    return launch_threads(mx4_tiled_kernel<IN, BM, BN, WM, WN, EPILOGUE>, a.row_tiles * a.col_tiles,
+    return launch_threads(mx4_tiled_kernel<OUT, BM, BN, WM, WN, EPILOGUE, DEEP>, a.row_tiles * a.col_tiles,
                           (BM / WM) * (BN / WN) * 64, st, a);
 }
 
@@ -1089,6 +1155,12 @@ hipError_t linear(LinearArgs a, int kind, const uint8_t* w_scales, void* workspa
         constexpr int out = decltype(OUT)::value;
         if (tiles(256) >= 256) return tiled<out, 256, 256, 128, 64, EPILOGUE>(a, st);
         if (tiles(128) >= 256) return tiled<out, 128, 128, 64, 64, EPILOGUE>(a, st);
+        // with more than two tiles to a CU, others on it fill the waits, as long as
+        // their buffers fit.  Three chunks under way against one to two: 300 rows of
+        // 5760 x 2880 (225 tiles) 15.8 against 18.1 us, 128 of 21504 x 5376 (168) 40
+        // against 50, 500 of 3840 x 3840 (480) 14.2 against 15.1, but 100 of
+        // 5376 x 21504 (672) 27.5 against 24.5.
+        if (tiles(64) <= 512) return tiled<out, 64, 64, 32, 64, EPILOGUE, true>(a, st);
         return tiled<out, 64, 64, 32, 64, EPILOGUE>(a, st);
     };
     return a.out_kind == kOutBF16 ? go(std::integral_constant<int, kOutBF16>{}) : go(std::integral_constant<int, kOutF32>{});

@@ -109,6 +109,21 @@ def test_mixtures(name, bias, residual, rows, cols, out):
     _check(rows, 96, cols, BF16, out, bias, name, residual)
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("chunks", range(1, 11))
+def test_few_tiles_over_every_number_of_chunks(chunks, out):
+    """Few tiles ask for 256 of k three chunks ahead, in a ring of four; whole tiles and ones past the edge."""
+    for rows, inner, cols in [(130, 256 * chunks, 200), (128, 256 * chunks - 90, 128)]:
+        _check(rows, inner, cols, BF16, out, True, None, True)
+        _check(rows, inner, cols, F32, out, False, None, False)
+
+
+def test_more_tiles_than_two_a_cu():
+    """Beside the forms for few tiles: 66 x 33,000 are 1,032 tiles of 64."""
+    _check(66, 800, 33_000, BF16, BF16, True, "silu", True)
+    _check(66, 800, 33_000, F32, F32, True, None, True)
+
+
 def test_without_an_epilogue_it_is_the_product():
     rng = np.random.default_rng(2)
     for rows, inner, cols in [(4, 64, 100), (50, 100, 60), (200, 320, 300)]:
