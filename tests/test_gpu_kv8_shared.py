@@ -165,6 +165,53 @@ def test_a_nan_stays_in_its_row():
         assert torch.equal(got[~rows], clean[~rows])
 
 
+@pytest.mark.parametrize("heads,kv_heads,dim,members", [(16, 2, 128, 8), (8, 2, 256, 8), (2, 2, 128, 80)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_rows_over_absent_pages_and_scales_far_apart(heads, kv_heads, dim, members, dtype):
+    """What the bodies for many rows do a page ahead: the next page may be absent, the last one or in another unit."""
+    rng = np.random.default_rng(dim + members)
+    for pages in (1, 2, 3, 5, 12):
+        prefix = 64 * pages + 20
+        lengths = [prefix + 1 + i for i in range(members)]
+        absent = [(b, p) for b in range(members) for p in range(pages) if pages > 3 and p % 5 in (0, 3)]
+        c = _shared_cache(rng, kv_heads, dim, [0, members], [prefix], lengths, pages + 3, absent=absent)
+        c["v_scales"] *= np.exp2(rng.integers(-30, 31, c["v_scales"].shape)).astype(np.float32)
+        c["k_scales"] *= np.exp2(rng.integers(-6, 2, c["k_scales"].shape)).astype(np.float32)
+        _check(c, [0, members], [prefix], 1, heads, dtype, seed=pages)
+        _check(c, [0, members], [prefix], 20, heads, dtype, seed=pages, scale=-0.05)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_more_pages_than_are_looked_up_at_once(dtype):
+    """256 tiles of own rows: one slot of up to 70 pages each.  One head of two sequences is compared."""
+    rng = np.random.default_rng(16)
+    c = _shared_cache(rng, 8, 128, [0, 4], [128], [64 * 70 - 5, 64 * 69, 64 * 66 + 1, 4000], 70)
+    q = torch.from_numpy(rng.standard_normal((4, 1024, 8, 128)).astype(np.float32)).to(dtype)
+    out = qar.qar_kv8_attention_shared(ref.to_cache(c), q.to(DEV), _ints(0, 4), _ints(128)).double().cpu().numpy()
+    part = {**c, **{n: np.ascontiguousarray(c[n][:, 5:6]) for n in ("k", "v", "k_scales", "v_scales")}}
+    for b in (0, 1):
+        one = {**part, "page_table": c["page_table"][b:b + 1], "lengths": c["lengths"][b:b + 1]}
+        mine = q[b:b + 1, :, 5:6]
+        want = ref.attend(one, mine.float().numpy(), [1024], 128 ** -0.5)
+        tol, _ = _attention_tolerance(want, mine, dtype, 128, int(c["lengths"][b]) + PAGE)
+        assert (np.abs(out[b:b + 1, :, 5:6] - want["out"]) <= tol).all()
+
+
+def test_a_nan_stays_in_its_row_of_many():
+    rng = np.random.default_rng(17)
+    c = _shared_cache(rng, 2, 128, [0, 20], [900], [901 + i for i in range(20)], 16)
+    cache = ref.to_cache(c)
+    q = torch.from_numpy(rng.standard_normal((20, 2, 8, 128)).astype(np.float32)).to(DEV)
+    for dtype in DTYPES:
+        clean = qar.qar_kv8_attention_shared(cache, q.to(dtype), _ints(0, 20), _ints(900))
+        bad = q.to(dtype).clone()
+        bad[7, 1, 3, 5] = float("nan")
+        got = qar.qar_kv8_attention_shared(cache, bad, _ints(0, 20), _ints(900))
+        rows = torch.isnan(got).all(3)
+        assert rows[7, 1, 3] and rows.sum() == 1
+        assert torch.equal(got[~rows], clean[~rows])
+
+
 def test_equal_calls_and_workspaces():
     """Equal bits whatever the workspace held; nothing behind the output or the workspace's stated end is written."""
     rng = np.random.default_rng(14)
