@@ -817,13 +817,12 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
     if (g == 0) a.stats[at * 2] = top, a.stats[at * 2 + 1] = total;
 }
 
-
 // ---------------------------------------------------------------------------
 // the kernels: one form for both kinds of tiles, or many rows for the prefix
 // and few for the own pages.  The prefix comes first and leaves a CU half empty
 // (see `plan_for`); there the own pages, which wait for memory, run beside it:
-// 64 sequences of 32 heads x 128 behind 32,768 tokens 70 us, in two launches
-// 87, in turn eight by eight 93.
+// 64 sequences of 32 heads x 128 behind 32,768 tokens 77 us, in two launches
+// 87, in turn eight by eight 93, all before the scores were formed a page ahead.
 
 enum : int { kFew = 0, kMany = 1, kManyFew = 2 };
 
@@ -948,13 +947,15 @@ bool is_few(int dim, size_t rows) { return rows <= (dim == 256 ? 16 : 32); }
 // host goes by their averages and bounds.  A slot more for a row is a row of
 // outputs more to write and to read again, so there are no more than fill the
 // CUs: of many rows one workgroup a CU with 128 or 256 channels (64 sequences
-// behind 32,768 tokens, 32 heads x 128: one 70 us, two 82, three 81; 16 heads x
-// 256, 32 sequences: 89, 99, 118), three with 64, whose pages are shorter (64
-// heads: 89, 76, 70); of few rows and of own pages one (eight sequences behind
-// 32,768 tokens 34 us, with two 45; 800 rows of four sequences each behind 8,000
-// tokens 135 and 160).  Where a slot would be more than 64 pages long, two
-// workgroups share a CU's units better than one uses them (64 sequences behind
-// 131,072 tokens 234 against 275 us).
+// behind 32,768 tokens, 32 heads x 128: one 66 us, one and a half 69, two 73,
+// three 81; 16 heads x 256, 32 sequences: 89, 99, 118), three with 64, whose
+// pages are shorter (64 heads: 89, 76, 70); of few rows and of own pages one
+// (eight sequences behind 32,768 tokens 34 us, with two 45).  Where a slot would
+// be more than 56 pages long, two workgroups share a CU's units better than one
+// uses them (64 sequences behind 65,536 tokens 105 against 112 us, behind 131,072
+// 190 against 212; fp32 156 against 175 and 285 against 330; at 48 pages bf16 90
+// against 86), but not more than two: 800 rows behind 8,000 tokens, in two slots
+// as it is, 135 us and in four 168.
 struct Plan {
     bool prefix_few, own_few;
     uint32_t prefix_rows, own_rows;      // of a tile
@@ -974,7 +975,8 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
     p.prefix_tiles = (uint32_t)(all / p.prefix_rows) + groups;
     const size_t likely = groups == 1 ? (all + p.prefix_rows - 1) / p.prefix_rows : (all / p.prefix_rows + (groups + 1) / 2);
     p.prefix_slots = slots_for(likely * kv_heads, width, !p.prefix_few && dim == 64 ? 768 : 256);
-    if (!p.prefix_few && dim == 128 && width / p.prefix_slots > 64) p.prefix_slots *= 2;
+    if (!p.prefix_few && dim == 128 && width / p.prefix_slots > 56)
+        p.prefix_slots = std::max(p.prefix_slots, (uint32_t)(512 / (likely * kv_heads)));
     p.own_few = is_few(dim, rows);
     p.own_rows = p.own_few ? few_rows(dim, rows) : kTileRows;
     p.own_tiles = (rows + p.own_rows - 1) / p.own_rows;
