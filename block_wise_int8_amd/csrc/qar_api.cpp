@@ -1311,7 +1311,6 @@ qar_status qar_kv8_reserve(const qar_kv8_cache* cache, int32_t* refs, const int3
 }
 
 qar_status qar_kv8_compact(const qar_kv8_cache* cache, int32_t* refs, int32_t* source, int32_t* target, void* stream) {
-    if (cache && cache->batch == 0) return QAR_OK;
     qar_status st = check_owned(cache, refs);
     if (st != QAR_OK) return st;
     if (cache->pages < 2) return QAR_OK;             // nothing can move

@@ -680,8 +680,9 @@ qar_status qar_kv8_free(const qar_kv8_cache* cache, int32_t* refs, const int32_t
  * content the caller copies (qar_kv8_copy) before it appends; otherwise both
  * are -1.  Behind its last page every page up to lengths[b] + tokens[b] that is
  * not there is given; those that are there count as its own, so a sequence that
- * is to lose tokens is cut back with qar_kv8_free and not by its length alone.  Pages are taken lowest free number first.  When none is
- * left a sequence keeps what it got.  lengths are not changed.
+ * is to lose tokens is cut back with qar_kv8_free and not by its length alone.
+ * Pages are taken lowest free number first.  When none is left a sequence keeps
+ * what it got.  lengths are not changed.
  *   tokens   [in]  int32[batch]; below 1 counts as none.
  *   room     [out] int32[batch]: for how many tokens there is room now, at most
  *                  tokens[b]; 0 for one whose shared or missing page could not be
@@ -697,7 +698,8 @@ qar_status qar_kv8_reserve(const qar_kv8_cache* cache, int32_t* refs, const int3
  * ones below L, the lowest with the lowest.  refs and the cache's table follow;
  * what other tables name is found in the lists.  The caller copies the pages
  * (qar_kv8_copy), and may then give the pool from page L on to others.
- *   source, target  [out] int32[pages / 2]: the moves, -1 behind them.
+ *   source, target  [out] int32[pages / 2]: the moves, -1 behind them.  (A cache
+ *                   without sequences is refused here: lists would be left unset.)
  */
 qar_status qar_kv8_compact(const qar_kv8_cache* cache, int32_t* refs, int32_t* source, int32_t* target, void* stream);
 /*

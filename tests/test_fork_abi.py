@@ -76,8 +76,9 @@ def test_fork_refusals(L):
 def test_free_and_reserve_and_compact_refusals(L):
     _, free, reserve, compact, _ = _calls(L)
     c = ctypes.byref(_struct())
-    for call in (free, reserve, compact):
+    for call in (free, reserve):
         assert call(ctypes.byref(_struct(batch=0))) == OK
+    assert compact(ctypes.byref(_struct(batch=0))) == INV                                # its lists would stay unset
     assert free(c, keep=600 * M + 2) == MIS and free(c, keep=REFS) == INV and free(c, keep=500 * M + 4) == INV
     for name in ("tokens", "room", "source", "target"):
         assert reserve(c, **{name: None}) == INV and reserve(c, **{name: 1000 * M + 2}) == MIS, name
