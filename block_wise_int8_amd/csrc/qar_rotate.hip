@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
 #pragma unroll
             for (int k = 0; k < E; ++k) {
                 const uint32_t pair = PAIRS == kHalves ? unit[i] * E + k : (at[i][k / (E / 2)] + k % (E / 2) * 2) / 2;
-                turn[i][k] = pair < a.pairs ? table[pair] : make_float2(1.0f, 0.0f);
+                turn[i][k] = table[std::min(pair, (uint32_t)DIM / 2 - 1)];    // behind the pairs unused
             }
     }
 
@@ -194,8 +194,10 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
                         const float2 t = turn[i][k];
                         float* z = y[i][k / (E / 2)] + k % (E / 2) * 2;
                         const float u = z[0], v = z[1];
-                        z[0] = u * t.x - v * t.y;
-                        z[1] = v * t.x + u * t.y;
+                        // behind the pairs neither is touched, were the other infinite
+                        const bool pair = (at[i][k / (E / 2)] + k % (E / 2) * 2) / 2 < a.pairs;
+                        z[0] = pair ? u * t.x - v * t.y : u;
+                        z[1] = pair ? v * t.x + u * t.y : v;
                     }
             }
         } else {

@@ -111,6 +111,25 @@ def test_each_head_for_itself():
     assert torch.equal(q[0][same_q], qc[0][same_q]) and torch.equal(k[0][same_k], kc[0][same_k])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pairs", [0, 3, 16, 21])
+def test_channels_that_are_not_rotated_are_copied(pairs, interleaved, dtype):
+    """Bit for bit without a norm: infinities, NaN and negative zeros beside each other."""
+    g = torch.Generator().manual_seed(pairs)
+    x = torch.randn((2, 3, 6, 64), generator=g).to(dtype)
+    x[..., 2 * pairs:][torch.rand(x[..., 2 * pairs:].shape, generator=g) < 0.2] = float("inf")
+    x[..., 2 * pairs:][torch.rand(x[..., 2 * pairs:].shape, generator=g) < 0.2] = -0.0
+    x[..., 2 * pairs:][torch.rand(x[..., 2 * pairs:].shape, generator=g) < 0.1] = float("nan")
+    f = torch.from_numpy(_frequencies(pairs)).to(DEV) if pairs else None
+    got = qar.qar_norm_rotate(x.to(DEV), 4, 1, torch.tensor([5, 7], dtype=torch.int32, device=DEV), f, interleaved=interleaved)
+    for y, z in zip(got, (x[:, :, :4], x[:, :, 4:5], x[:, :, 5:])):
+        assert torch.equal(torch.isnan(y[..., 2 * pairs:].cpu()), torch.isnan(z[..., 2 * pairs:]))
+        y, z = (torch.nan_to_num(t[..., 2 * pairs:].cpu(), nan=1.0, posinf=float("inf")) for t in (y, z))
+        assert torch.equal(y, z) and torch.equal(torch.signbit(y), torch.signbit(z))
+        assert torch.isfinite(got[0][..., :2 * pairs]).all()
+
+
 def test_outputs_given_and_surroundings_left_alone():
     x = torch.randn((2, 3, 8, 64), generator=torch.Generator().manual_seed(8))
     room = torch.full((3, 4096), 7.0, device=DEV)
