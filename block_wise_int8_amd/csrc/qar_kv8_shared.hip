@@ -87,6 +87,37 @@ struct Seq {
           m(a.q_lens ? clamp_length(a.q_lens[b], a.queries) : (int32_t)a.queries) {}
 };
 
+// The group that has tile number `tile` of all groups' tiles of rows, and its
+// first tile's number; {0, 0, 0} behind the last tile.  So the workgroups
+// without work are the last: spare ones between others leave CUs idle beside
+// CUs with two.
+__device__ __forceinline__ Group group_of_tile(const SharedArgs& a, uint32_t tile, uint32_t tile_rows, uint32_t& first_tile) {
+    const uint32_t lane = threadIdx.x % 64;
+    uint32_t before = 0;
+    for (uint32_t base = 0; base < a.groups; base += 64) {
+        const uint32_t g = min(base + lane, a.groups - 1);
+        const uint32_t start = (uint32_t)clamp_length(a.starts[g], a.c.batch), end = (uint32_t)clamp_length(a.starts[g + 1], a.c.batch);
+        const uint32_t pages = (uint32_t)clamp_length(a.prefix[g], a.c.width * kPage) / kPage;
+        const uint32_t count = base + lane < a.groups && end > start ? ((end - start) * a.rows + tile_rows - 1) / tile_rows : 0;
+        uint32_t sum = count;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const uint32_t other = __shfl_up(sum, d);
+            if (lane >= (uint32_t)d) sum += other;
+        }
+        const uint64_t mask = __ballot(before + sum > tile);
+        if (mask) {
+            const int i = __builtin_ctzll(mask);
+            first_tile = before + (uint32_t)__builtin_amdgcn_readlane((int)(sum - count), i);
+            return Group{(uint32_t)__builtin_amdgcn_readlane((int)start, i), (uint32_t)__builtin_amdgcn_readlane((int)end, i),
+                         (uint32_t)__builtin_amdgcn_readlane((int)pages, i)};
+        }
+        before += (uint32_t)__builtin_amdgcn_readlane((int)sum, 63);
+    }
+    first_tile = tile;
+    return Group{0, 0, 0};
+}
+
 // What a workgroup does: a tile of rows of one key head, a slot of pages.  Row
 // r is row r % a.rows of sequence first_seq + r / a.rows; that is its query
 // r / a.group with head r % a.group of the key head's group.
@@ -97,14 +128,12 @@ struct Work {
     __device__ __forceinline__ void of_prefix(const SharedArgs& a, uint32_t unit, uint32_t tile_rows) {
         slot = unit % a.prefix_slots;
         head = unit / a.prefix_slots % a.c.heads;
-        // group g's tiles begin at g plus the whole tiles of all rows before it: room for a last, partial tile of each
         const uint32_t tile = unit / a.prefix_slots / a.c.heads;
-        const auto first_tile = [&](uint32_t start, uint32_t g) { return (uint32_t)((uint64_t)start * a.rows / tile_rows) + g; };
-        uint32_t index = 0;
-        const Group g = last_group(a, tile, index, first_tile);
+        uint32_t first_tile;
+        const Group g = group_of_tile(a, tile, tile_rows, first_tile);
         first_seq = g.start;
-        row_count = g.end > g.start ? (g.end - g.start) * a.rows : 0;
-        first_row = (tile - first_tile(g.start, index)) * tile_rows;
+        row_count = (g.end - g.start) * a.rows;
+        first_row = (tile - first_tile) * tile_rows;
         const Cut cut(g.pages, a.prefix_slots);
         first = slot * cut.per;
         last = min(first + cut.per, g.pages);
@@ -154,12 +183,12 @@ __device__ __forceinline__ int32_t lanes16_min(int32_t v) {
 // few rows: a wave takes a page at a time, from memory to registers (the
 // layout of kv8_attend_few_kernel, qar_kv8.hip).
 
-constexpr int kFewWaves = 4;
+constexpr int kFewWaves = 4, kFewRows = 16;
 
 template <int DIM>
 constexpr int kFewLds = kFewWaves * 16 * (DIM + 4) * 4 + 2 * kFewWaves * 16 * 4 + 16 * 8;
 
-template <int DIM, int MT, int IN>
+template <int DIM, int IN>
 __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work, char* lds) {
     constexpr int NW = kFewWaves;
     constexpr int T = IN == kInBF16 ? 1 : 2;
@@ -180,24 +209,17 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
     };
     look_up(first + wave + lane * NW);
 
-    Query<IN, DIM, 16, 64> raw[MT];
-    int32_t limit[MT], all_see = INT32_MAX;                  // every row sees the keys below
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const Row row(a, work, work.first_row + i * 16 + r);
-        raw[i].load(a.q, row.there ? row.query : 0, g * 16, row.there);
-        limit[i] = row.there ? row.limit : INT32_MAX;        // rows that are not there are not stored
-        all_see = min(all_see, lanes16_min(limit[i]));
-    }
-    all_see = __builtin_amdgcn_readfirstlane(all_see);
-    kv_half8 q[MT][DIM / 32][T];
-    float undo[MT];
+    const Row row(a, work, work.first_row + r);
+    Query<IN, DIM, 16, 64> raw;
+    raw.load(a.q, row.there ? row.query : 0, g * 16, row.there);
+    const int32_t limit = row.there ? row.limit : INT32_MAX; // rows that are not there are not stored
+    const int32_t all_see = __builtin_amdgcn_readfirstlane(lanes16_min(limit));   // every row sees the keys below
+    kv_half8 q[DIM / 32][T];
+    float undo;
 
-    kv_f32x4 o[MT][VC] = {};
+    kv_f32x4 o[VC] = {};
     Unit unit;
-    float top[MT], total[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) top[i] = -FLT_MAX, total[i] = 0.0f;
+    float top = -FLT_MAX, total = 0.0f;
 
     const size_t head_bytes = (size_t)kPage * DIM;
     const uint32_t k_at = (r / 4 * 16 + r % 4) * DIM + g * 16, v_at = r * kPage + g * 16;
@@ -221,17 +243,14 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
         int32_t id = __builtin_amdgcn_readlane(my_id, 0);
         load_k(id);
         load_v(id);
-        if (base == first + wave) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) undo[i] = raw[i].template convert<16, T>(a.negative, q[i]) * a.scale;
-        }
+        if (base == first + wave) undo = raw.template convert<16, T>(a.negative, q) * a.scale;
         for (uint32_t i = 0; i < count; ++i) {
             const int32_t next = __builtin_amdgcn_readlane(my_id, min(i + 1, count - 1));
             const float ks = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_ks), i));
             const float vs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, my_vs), i));
             const int32_t key0 = (int32_t)((base + i * NW) * kPage);
 
-            kv_f32x4 s[MT][4] = {};
+            kv_f32x4 s[4] = {};
 #pragma unroll
             for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -241,57 +260,49 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
                     for (int t = 0; t < 4; ++t)
                         k[t] = u ? half_codes(kr[t][c].z, kr[t][c].w) : half_codes(kr[t][c].x, kr[t][c].y);
 #pragma unroll
-                    for (int j = 0; j < MT; ++j)
+                    for (int e = 0; e < T; ++e)
 #pragma unroll
-                        for (int e = 0; e < T; ++e)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t)
-                                s[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[t], q[j][2 * c + u][e], s[j][t], 0, 0, 0);
+                        for (int t = 0; t < 4; ++t)
+                            s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[t], q[2 * c + u][e], s[t], 0, 0, 0);
                 }
             if (i + 1 < count) load_k(next);
 
             const float shrink_all = unit.next(vs);
             if (shrink_all != 1.0f)
 #pragma unroll
-                for (int j = 0; j < MT; ++j)
+                for (int c = 0; c < VC; ++c) o[c] *= shrink_all;
+            kv_half8 p[2][T];
+            float factor = ks * undo;
+            if (key0 + kPage > all_see || id < 0) {
+                const int32_t sees = (id < 0 ? 0 : limit) - key0 - (int32_t)g * 16;
 #pragma unroll
-                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink_all;
-            kv_half8 p[MT][2][T];
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                float factor = ks * undo[j];
-                if (key0 + kPage > all_see || id < 0) {
-                    const int32_t sees = (id < 0 ? 0 : limit[j]) - key0 - (int32_t)g * 16;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) s[j][t][k] = 4 * t + k < sees ? s[j][t][k] * factor : -INFINITY;
-                    factor = 1.0f;
-                }
-                float m = max3(s[j][0][0], s[j][0][1], s[j][0][2]);
-#pragma unroll
-                for (int k = 3; k < 15; k += 2) m = max3(m, s[j][k / 4][k % 4], s[j][(k + 1) / 4][(k + 1) % 4]);
-                m = fmaxf(max_over_16(fmaxf(m, s[j][3][3])) * factor, top[j]);
-                if (__any(m > top[j])) {
-                    const float shrink = __builtin_amdgcn_exp2f(top[j] - m);
-                    total[j] *= shrink;
-#pragma unroll
-                    for (int c = 0; c < VC; ++c) o[j][c] *= shrink;
-                    top[j] = m;
-                }
-                const float off = unit.lift - m;
-                float sum = 0.0f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float x[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][2 * u + k / 4][k % 4], factor, off));
-                    sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-                    half_terms<T>(x, p[j][u]);
-                }
-                total[j] = __builtin_fmaf(sum, unit.drop, total[j]);
+                    for (int k = 0; k < 4; ++k) s[t][k] = 4 * t + k < sees ? s[t][k] * factor : -INFINITY;
+                factor = 1.0f;
             }
+            float m = max3(s[0][0], s[0][1], s[0][2]);
+#pragma unroll
+            for (int k = 3; k < 15; k += 2) m = max3(m, s[k / 4][k % 4], s[(k + 1) / 4][(k + 1) % 4]);
+            m = fmaxf(max_over_16(fmaxf(m, s[3][3])) * factor, top);
+            if (__any(m > top)) {
+                const float shrink = __builtin_amdgcn_exp2f(top - m);
+                total *= shrink;
+#pragma unroll
+                for (int c = 0; c < VC; ++c) o[c] *= shrink;
+                top = m;
+            }
+            const float off = unit.lift - m;
+            float sum = 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * u + k / 4][k % 4], factor, off));
+                sum += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                half_terms<T>(x, p[u]);
+            }
+            total = __builtin_fmaf(sum, unit.drop, total);
 #pragma unroll
             for (int c = 0; c < VC; c += 2) {
                 const kv_half8 v[2][2] = {{half_codes(vr[c].x, vr[c].y), half_codes(vr[c + 1].x, vr[c + 1].y)},
@@ -301,48 +312,39 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
 #pragma unroll
                     for (int e = 0; e < T; ++e)
 #pragma unroll
-                        for (int j = 0; j < MT; ++j)
-#pragma unroll
-                            for (int d = 0; d < 2; ++d)
-                                o[j][c + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u][d], p[j][u][e], o[j][c + d], 0, 0, 0);
+                        for (int d = 0; d < 2; ++d)
+                            o[c + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u][d], p[u][e], o[c + d], 0, 0, 0);
             }
             if (i + 1 < count) load_v(next);
             id = next;
         }
     }
 
-    // the waves' results meet in LDS, 16 rows at a time
+    // the waves' results meet in LDS
     size_t* items = reinterpret_cast<size_t*>(lds);
     auto tops = reinterpret_cast<float (*)[16]>(lds + 16 * 8), totals = tops + NW;
     auto os = reinterpret_cast<float (*)[16][DIM + 4]>(totals + NW);
+    total = sum_over_16(total);
+    if (g == 0) tops[wave][r] = top, totals[wave][r] = total;
+    if (threadIdx.x < 16) items[r] = row.item;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const uint32_t row0 = work.first_row + j * 16;
-        if (j) __syncthreads();
-        if (row0 < work.row_count) {
-            total[j] = sum_over_16(total[j]);
-            if (g == 0) tops[wave][r] = top[j], totals[wave][r] = total[j];
-            if (threadIdx.x < 16) items[r] = Row(a, work, row0 + r).item;
+    for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[c] * unit.unit;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 16 * DIM; i += NW * 64) {
+        const uint32_t row16 = i / DIM, d = i % DIM;
+        if (work.first_row + row16 >= work.row_count) break;
+        float m = tops[0][row16], l = 0.0f, y = 0.0f;
 #pragma unroll
-            for (int c = 0; c < VC; ++c) *reinterpret_cast<kv_f32x4*>(&os[wave][r][c * 16 + g * 4]) = o[j][c] * unit.unit;
+        for (int w = 1; w < NW; ++w) m = fmaxf(m, tops[w][row16]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = __builtin_amdgcn_exp2f(tops[w][row16] - m);
+            l = __builtin_fmaf(totals[w][row16], f, l);
+            y = __builtin_fmaf(os[w][row16][d], f, y);
         }
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < 16 * DIM; i += NW * 64) {
-            const uint32_t row16 = i / DIM, d = i % DIM;
-            if (row0 + row16 >= work.row_count) break;
-            float m = tops[0][row16], l = 0.0f, y = 0.0f;
-#pragma unroll
-            for (int w = 1; w < NW; ++w) m = fmaxf(m, tops[w][row16]);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float f = __builtin_amdgcn_exp2f(tops[w][row16] - m);
-                l = __builtin_fmaf(totals[w][row16], f, l);
-                y = __builtin_fmaf(os[w][row16][d], f, y);
-            }
-            const size_t at = items[row16] * (a.prefix_slots + a.own_slots) + work.slot;
-            a.part[at * DIM + d] = y;
-            if (d == 0) a.stats[at * 2] = m, a.stats[at * 2 + 1] = l;
-        }
+        const size_t at = items[row16] * (a.prefix_slots + a.own_slots) + work.slot;
+        a.part[at * DIM + d] = y;
+        if (d == 0) a.stats[at * 2] = m, a.stats[at * 2 + 1] = l;
     }
 }
 
@@ -826,8 +828,8 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
 
 enum : int { kFew = 0, kMany = 1, kManyFew = 2 };
 
-template <int DIM, int MT, int IN, int FORM>
-__global__ __launch_bounds__(kThreads, DIM == 256 || (FORM == kFew && MT == 2) ? 1 : 2)
+template <int DIM, int IN, int FORM>
+__global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2)
     void kv8_shared_kernel(SharedArgs a, uint32_t prefix_units) {
     constexpr int FEW = FORM == kMany ? 0 : kFewLds<DIM>, MANY = FORM == kFew ? 0 : kManyLds<DIM, IN>;
     constexpr int BYTES = std::max(FEW, MANY);
@@ -836,12 +838,12 @@ __global__ __launch_bounds__(kThreads, DIM == 256 || (FORM == kFew && MT == 2) ?
     const uint32_t unit = own ? blockIdx.x - prefix_units : blockIdx.x;
     Work work;
     if (own)
-        work.of_own(a, unit, FORM == kMany ? kTileRows : 16 * MT);
+        work.of_own(a, unit, FORM == kMany ? kTileRows : kFewRows);
     else
-        work.of_prefix(a, unit, FORM == kFew ? 16 * MT : kTileRows);
+        work.of_prefix(a, unit, FORM == kFew ? kFewRows : kTileRows);
     if (!work.any) return;
     if (FORM == kFew || (FORM == kManyFew && own)) {
-        if constexpr (FORM != kMany) attend_few<DIM, MT, IN>(a, work, lds);
+        if constexpr (FORM != kMany) attend_few<DIM, IN>(a, work, lds);
     } else if constexpr (FORM != kFew) {
         if constexpr (kScoresAhead<DIM, IN>)
             attend_many_ahead<DIM, IN>(a, work, own, lds);
@@ -938,10 +940,14 @@ hipError_t with_kind(int kind, F f) {
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Rows of the few-row kernel's tile.  Two tiles of 16 rows at 256 channels
-// would not fit a wave's registers.
-uint32_t few_rows(int dim, uint32_t rows) { return dim == 256 || rows <= 16 ? 16 : 32; }
-bool is_few(int dim, size_t rows) { return rows <= (dim == 256 ? 16 : 32); }
+// Rows that go to tiles of 16, which read the same pages at the same time, and
+// not to one of 128.  16, 32 and 64 rows a tile's worth at a time, against 128:
+// 32 rows x 256 channels behind 32,768 tokens 53 against 77 us, 64 rows 78
+// against 86; 48 rows x 64 20.6 against 26.4, 64 rows of 8 prompts 25.2 against
+// 27.4; 32 rows x 128 24.7 against 33.6, but 48 rows of 8 prompts 43.5 against
+// 38.4.  (A tile of two times 16 rows reads a page once, but holds so many
+// registers that a SIMD has one wave: 32 rows x 128 33, x 64 23.8 against 17.3.)
+bool is_few(int dim, size_t rows) { return rows <= (dim == 128 ? 32 : 64); }
 
 // How a call is cut.  Group sizes, prefixes and lengths are on the device; the
 // host goes by their averages and bounds.  A slot more for a row is a row of
@@ -950,9 +956,9 @@ bool is_few(int dim, size_t rows) { return rows <= (dim == 256 ? 16 : 32); }
 // behind 32,768 tokens, 32 heads x 128: one 66 us, one and a half 69, two 73,
 // three 81; 16 heads x 256, 32 sequences: 89, 99, 118), three with 64, whose
 // pages are shorter (64 heads: 89, 76, 70); of few rows and of own pages one
-// (eight sequences behind 32,768 tokens 34 us, with two 45).  Where a slot would
-// be more than 56 pages long, two workgroups share a CU's units better than one
-// uses them (64 sequences behind 65,536 tokens 105 against 112 us, behind 131,072
+// (eight sequences behind 32,768 tokens 25 us, with two 29; behind 131,072 tokens
+// 63 and 84).  Where a slot of many rows would be more than 56 pages long, two
+// workgroups share a CU's units better than one uses them (64 sequences behind 65,536 tokens 105 against 112 us, behind 131,072
 // 190 against 212; fp32 156 against 175 and 285 against 330; at 48 pages bf16 90
 // against 86), but not more than two: 800 rows behind 8,000 tokens, in two slots
 // as it is, 135 us and in four 168.
@@ -962,23 +968,33 @@ struct Plan {
     uint32_t prefix_tiles, own_tiles, prefix_slots, own_slots;
 };
 
+// As many slots as give `target` workgroups, or up to twice as many where that
+// leaves a tenth or more of the CUs' time empty (20 groups x 8 heads: 320
+// workgroups are two rounds, 480 as well: 66 -> 56 us).
 uint32_t slots_for(size_t units, uint32_t width, size_t target) {
     const size_t want = (target + units - 1) / units, most = (width + 3) / 4;
-    return (uint32_t)(want < most ? want : most);
+    if (want >= most) return (uint32_t)most;
+    // a CU's longest share, in pages of the axis: rounds of workgroups by slots
+    const auto rounds = [&](size_t slots) { return (units * slots + 255) / 256; };
+    size_t best = want;
+    if (units * want * 10 < rounds(want) * 256 * 9)
+        for (size_t s = want + 1; s <= 2 * want && s <= most; ++s)
+            if (rounds(s) * best * 10 < rounds(best) * s * 9) best = s;
+    return (uint32_t)best;
 }
 
 Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups) {
     Plan p = {};
     const size_t all = (size_t)batch * rows, mean = (all + groups - 1) / groups;
     p.prefix_few = is_few(dim, mean);
-    p.prefix_rows = p.prefix_few ? few_rows(dim, (uint32_t)mean) : kTileRows;
+    p.prefix_rows = p.prefix_few ? kFewRows : kTileRows;
     p.prefix_tiles = (uint32_t)(all / p.prefix_rows) + groups;
-    const size_t likely = groups == 1 ? (all + p.prefix_rows - 1) / p.prefix_rows : (all / p.prefix_rows + (groups + 1) / 2);
+    const size_t likely = groups * ((mean + p.prefix_rows - 1) / p.prefix_rows);   // groups of one size
     p.prefix_slots = slots_for(likely * kv_heads, width, !p.prefix_few && dim == 64 ? 768 : 256);
     if (!p.prefix_few && dim == 128 && width / p.prefix_slots > 56)
         p.prefix_slots = std::max(p.prefix_slots, (uint32_t)(512 / (likely * kv_heads)));
     p.own_few = is_few(dim, rows);
-    p.own_rows = p.own_few ? few_rows(dim, rows) : kTileRows;
+    p.own_rows = p.own_few ? kFewRows : kTileRows;
     p.own_tiles = (rows + p.own_rows - 1) / p.own_rows;
     p.own_slots = slots_for((size_t)batch * kv_heads * p.own_tiles, width, 256);
     return p;
@@ -1009,22 +1025,11 @@ hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t que
         return with_kind(kind, [&](auto K) {
             const uint32_t prefix_units = p.prefix_tiles * c.heads * p.prefix_slots;
             const uint32_t own_units = c.batch * c.heads * p.own_tiles * p.own_slots;
-            constexpr int two = D() == 256 ? 1 : 2;                      // tiles of 16 rows
-            const auto attend = [&](bool few, uint32_t rows, uint32_t prefix, uint32_t own) {
-                const auto go = [&](auto kernel) { return launch_threads(kernel, prefix + own, kThreads, st, a, prefix); };
-                if (!few) return go(kv8_shared_kernel<D(), 1, K(), kMany>);
-                return rows == 16 ? go(kv8_shared_kernel<D(), 1, K(), kFew>) : go(kv8_shared_kernel<D(), two, K(), kFew>);
-            };
-            hipError_t e;
-            if (p.prefix_few == p.own_few && p.prefix_rows == p.own_rows) {
-                e = attend(p.own_few, p.own_rows, prefix_units, own_units);
-            } else if (!p.prefix_few && p.own_rows == 16) {
-                e = launch_threads(kv8_shared_kernel<D(), 1, K(), kManyFew>, prefix_units + own_units, kThreads, st, a,
-                                   prefix_units);
-            } else {
-                e = attend(p.prefix_few, p.prefix_rows, prefix_units, 0);
-                if (e == hipSuccess) e = attend(p.own_few, p.own_rows, 0, own_units);
-            }
+            const auto attend = [&](auto kernel) { return launch_threads(kernel, prefix_units + own_units, kThreads, st, a, prefix_units); };
+            // a group's rows are a sequence's at least: few of all are few of each
+            const hipError_t e = p.prefix_few  ? attend(kv8_shared_kernel<D(), K(), kFew>)
+                                 : p.own_few ? attend(kv8_shared_kernel<D(), K(), kManyFew>)
+                                             : attend(kv8_shared_kernel<D(), K(), kMany>);
             if (e != hipSuccess) return e;
             return p.prefix_slots + p.own_slots > 4
                        ? launch_threads(kv8_shared_join_kernel<D(), K(), kJoinRows>, (uint32_t)items, kJoinRows * D() / 4, st, a)

@@ -165,7 +165,8 @@ def test_a_nan_stays_in_its_row():
         assert torch.equal(got[~rows], clean[~rows])
 
 
-@pytest.mark.parametrize("heads,kv_heads,dim,members", [(16, 2, 128, 8), (8, 2, 256, 8), (2, 2, 128, 80)])
+@pytest.mark.parametrize("heads,kv_heads,dim,members", [(16, 2, 128, 8), (8, 2, 256, 8), (8, 2, 256, 20),
+                                                           (2, 2, 128, 80)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_many_rows_over_absent_pages_and_scales_far_apart(heads, kv_heads, dim, members, dtype):
     """What the bodies for many rows do a page ahead: the next page may be absent, the last one or in another unit."""
