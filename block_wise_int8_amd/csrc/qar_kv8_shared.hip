@@ -955,13 +955,15 @@ bool is_few(int dim, size_t rows) { return rows <= (dim == 128 ? 32 : 64); }
 // CUs: of many rows one workgroup a CU with 128 or 256 channels (64 sequences
 // behind 32,768 tokens, 32 heads x 128: one 66 us, one and a half 69, two 73,
 // three 81; 16 heads x 256, 32 sequences: 89, 99, 118), three with 64, whose
-// pages are shorter (64 heads: 89, 76, 70); of few rows and of own pages one
-// (eight sequences behind 32,768 tokens 25 us, with two 29; behind 131,072 tokens
-// 63 and 84).  Where a slot of many rows would be more than 56 pages long, two
-// workgroups share a CU's units better than one uses them (64 sequences behind 65,536 tokens 105 against 112 us, behind 131,072
-// 190 against 212; fp32 156 against 175 and 285 against 330; at 48 pages bf16 90
-// against 86), but not more than two: 800 rows behind 8,000 tokens, in two slots
-// as it is, 135 us and in four 168.
+// pages are shorter (64 heads: 89, 76, 70); of few rows one with 128 or 256 (eight
+// sequences behind 32,768 tokens 25 us, with two 29; behind 131,072 tokens 63 and
+// 84), two with 64 (8 prompts x 8 sequences of 4,000 tokens: one 25.3, two 23.1,
+// three 24.2; 8,000 tokens: 39, 32, 32); of own pages one.  Where a slot of many
+// rows would be more than 56 pages long, two workgroups share a CU's units better
+// than one uses them (64 sequences behind 65,536 tokens 105 against 112 us, behind
+// 131,072 190 against 212; fp32 156 against 175 and 285 against 330; at 48 pages
+// bf16 90 against 86), but not more than two: 800 rows behind 8,000 tokens, in two
+// slots as it is, 135 us and in four 168.
 struct Plan {
     bool prefix_few, own_few;
     uint32_t prefix_rows, own_rows;      // of a tile
@@ -990,7 +992,7 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
     p.prefix_rows = p.prefix_few ? kFewRows : kTileRows;
     p.prefix_tiles = (uint32_t)(all / p.prefix_rows) + groups;
     const size_t likely = groups * ((mean + p.prefix_rows - 1) / p.prefix_rows);   // groups of one size
-    p.prefix_slots = slots_for(likely * kv_heads, width, !p.prefix_few && dim == 64 ? 768 : 256);
+    p.prefix_slots = slots_for(likely * kv_heads, width, dim != 64 ? 256 : p.prefix_few ? 512 : 768);
     if (!p.prefix_few && dim == 128 && width / p.prefix_slots > 56)
         p.prefix_slots = std::max(p.prefix_slots, (uint32_t)(512 / (likely * kv_heads)));
     p.own_few = is_few(dim, rows);
