@@ -584,7 +584,8 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
 // its matrix and its vector instructions side by side that way, which a second
 // workgroup on the CU gives the other bodies.  For bf16 and 128 channels only:
 // 64 leave too few products to hide the exponentials behind (8 prompts x 8
-// sequences 28.7 -> 33.5 us), 256 and fp32 have no registers for a second page.
+// sequences, in tiles of 128 rows, 28.7 -> 33.5 us), 256 and fp32 have no
+// registers for a second page.
 // 64 sequences behind 32,768 tokens 78.4 -> 72.1 us, 65,536 tokens 130 -> 115
 // us in this kernel, 800 query rows a head 172 -> 166 us, from four pages a
 // workgroup on no worse.
