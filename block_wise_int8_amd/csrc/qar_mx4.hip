@@ -437,10 +437,10 @@ __device__ __forceinline__ void activate(float (&y)[N], int activation) {
     case kActRelu: all([](float v) { return v < 0.0f ? 0.0f : v; }); break;
     case kActSilu: all([&](float v) { return over(v, 1.0f + exp_of<EXACT>(-v)); }); break;
     case kActGelu:
-        // v (1 - h) above 0, v h below
+        // v (1 - h) above 0, v h below.  From 64 on h is 0, which an infinity must not meet.
         all([](float v) {
-            const float h = half_erfc<EXACT>(fabsf(v));
-            return __builtin_fmaf(-fabsf(v), h, v < 0.0f ? 0.0f : v);
+            const float a = fminf(fabsf(v), 64.0f);
+            return __builtin_fmaf(-a, half_erfc<EXACT>(a), v < 0.0f ? 0.0f : v);
         });
         break;
     case kActGeluTanh:

@@ -478,7 +478,8 @@ qar_status qar_mx4_linear(const void* x, qar_dtype dtype, size_t rows, size_t in
  *   activation  y -> y, max(y, 0), y / (1 + e^-y), y (1 + erf(y / sqrt 2)) / 2, or
  *              y (1 + tanh(sqrt(2 / pi) (y + 0.044715 y^3))) / 2; each to 2^-16
  *              of itself where the result is bf16, else to 2^-21 (below 2^-119
- *              it may be 0).
+ *              it may be 0).  Of +infinity each is +infinity; of -infinity the
+ *              second and fourth are 0, the third and fifth NaN.
  *   residual   [in, optional] rows * cols elements of out_dtype, 16-byte
  *              aligned; may be `out` itself.
  *   workspace  that of qar_mx4_linear.
