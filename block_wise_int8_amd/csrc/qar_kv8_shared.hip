@@ -155,6 +155,26 @@ struct Work {
     }
 };
 
+// The sequence whose table names the pages that `work` has of a prefix: the
+// first of the group, or, where that holds fewer tokens (it ended or was cut back,
+// and its entries are gone), the group's longest, which holds all that any row
+// sees.  The lengths are asked for while the first one's entries are on their way.
+__device__ __forceinline__ uint32_t prefix_holder(const SharedArgs& a, const Work& work) {
+    const int32_t top = a.c.width * kPage;
+    if ((uint32_t)clamp_length(a.c.lengths[work.first_seq], top) >= work.last * kPage) return work.first_seq;
+    const uint32_t count = work.row_count / a.rows;
+    int32_t most = -1;
+    uint32_t which = 0;
+    for (uint32_t i = threadIdx.x % 64; i < count; i += 64) {
+        const int32_t n = clamp_length(a.c.lengths[work.first_seq + i], top);
+        if (n > most) most = n, which = i;
+    }
+    int32_t longest = most;
+#pragma unroll
+    for (int d = 32; d; d /= 2) longest = max(longest, __shfl_xor(longest, d));
+    return work.first_seq + (uint32_t)__builtin_amdgcn_readlane((int)which, __builtin_ctzll(__ballot(most == longest)));
+}
+
 // A row of the queries, and of the parts.
 struct Row {
     bool there;
@@ -189,25 +209,31 @@ template <int DIM>
 constexpr int kFewLds = kFewWaves * 16 * (DIM + 4) * 4 + 2 * kFewWaves * 16 * 4 + 16 * 8;
 
 template <int DIM, int IN>
-__device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work, char* lds) {
+__device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work, bool own, char* lds) {
     constexpr int NW = kFewWaves;
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int KC = DIM / 64, VC = DIM / 16;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
     const uint32_t h = work.head, first = work.first, last = work.last;
+    uint32_t seq = work.first_seq;
     int32_t my_id;
     float my_ks, my_vs;
-    auto look_up = [&](uint32_t page) {
-        my_id = -1, my_ks = my_vs = 0.0f;
-        if (page < last) {
-            my_id = valid_page(a.c.table[(size_t)work.first_seq * a.c.width + page], a.c.pages);
-            if (my_id >= 0) {
-                my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
-                my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
-            }
+    auto look_up_id = [&](uint32_t page) {
+        my_id = page < last ? valid_page(a.c.table[(size_t)seq * a.c.width + page], a.c.pages) : -1;
+    };
+    auto look_up_scales = [&] {
+        my_ks = my_vs = 0.0f;
+        if (my_id >= 0) {
+            my_ks = a.c.k_scales[(size_t)my_id * a.c.heads + h];
+            my_vs = a.c.v_scales[(size_t)my_id * a.c.heads + h];
         }
     };
-    look_up(first + wave + lane * NW);
+    look_up_id(first + wave + lane * NW);
+    if (!own) {
+        seq = prefix_holder(a, work);
+        if (seq != work.first_seq) look_up_id(first + wave + lane * NW);
+    }
+    look_up_scales();
 
     const Row row(a, work, work.first_row + r);
     Query<IN, DIM, 16, 64> raw;
@@ -238,7 +264,10 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
     };
 
     for (uint32_t base = first + wave; base < last; base += 64 * NW) {
-        if (base != first + wave) look_up(base + lane * NW);
+        if (base != first + wave) {
+            look_up_id(base + lane * NW);
+            look_up_scales();
+        }
         const uint32_t count = min(64u, (last - base + NW - 1) / NW);
         int32_t id = __builtin_amdgcn_readlane(my_id, 0);
         load_k(id);
@@ -397,7 +426,7 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     const uint32_t first_row = work.first_row + wave * 32;
 
     const uint32_t last = pages_end(a, work, own);
-    const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
+    uint32_t seq = work.first_seq;
     struct Page {
         int32_t id;
         float ks, vs;          // 0 for a page that is not there: what page 0 holds must not matter
@@ -405,8 +434,10 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     uint32_t base = first;
     int32_t my_id;
     float my_ks, my_vs;
-    auto look_up = [&] {
-        my_id = valid_page(table[min(base + lane, work.last - 1)], a.c.pages);
+    auto look_up_id = [&] {
+        my_id = valid_page(a.c.table[(size_t)seq * a.c.width + min(base + lane, work.last - 1)], a.c.pages);
+    };
+    auto look_up_scales = [&] {
         const size_t at = (size_t)max(my_id, 0) * a.c.heads + h;
         my_ks = my_id < 0 ? 0.0f : a.c.k_scales[at];
         my_vs = my_id < 0 ? 0.0f : a.c.v_scales[at];
@@ -414,7 +445,8 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     auto page_at = [&](uint32_t page) {
         if (page - base >= 64) {
             base = page;
-            look_up();
+            look_up_id();
+            look_up_scales();
         }
         const uint32_t i = page - base;
         return Page{__builtin_amdgcn_readlane(my_id, i),
@@ -429,7 +461,12 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
             to_lds(a.c.v + at + u * kThreads * 16, v_codes + u * kThreads + wave * 64);
         }
     };
-    look_up();
+    look_up_id();
+    if (!own) {
+        seq = prefix_holder(a, work);
+        if (seq != work.first_seq) look_up_id();
+    }
+    look_up_scales();
     Page now = page_at(first), next = page_at(first + 1);
     fetch(now.id);
 
@@ -605,7 +642,7 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
     const uint32_t h = work.head, first = work.first;
     const uint32_t first_row = work.first_row + wave * 32;
     const uint32_t last = pages_end(a, work, own);
-    const int32_t* table = a.c.table + (size_t)work.first_seq * a.c.width;
+    uint32_t seq = work.first_seq;
     struct Page {
         int32_t id;
         float ks, vs;          // 0 for a page that is not there
@@ -613,8 +650,10 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
     uint32_t base = first;
     int32_t my_id;
     float my_ks, my_vs;
-    auto look_up = [&] {
-        my_id = valid_page(table[min(base + lane, work.last - 1)], a.c.pages);
+    auto look_up_id = [&] {
+        my_id = valid_page(a.c.table[(size_t)seq * a.c.width + min(base + lane, work.last - 1)], a.c.pages);
+    };
+    auto look_up_scales = [&] {
         const size_t at = (size_t)max(my_id, 0) * a.c.heads + h;
         my_ks = a.c.k_scales[at], my_vs = a.c.v_scales[at];
         __builtin_amdgcn_s_waitcnt(0x0f70);            // the loads: here, not before every use
@@ -623,7 +662,8 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
     auto page_at = [&](uint32_t page) {
         if (page - base >= 64) {
             base = page;
-            look_up();
+            look_up_id();
+            look_up_scales();
         }
         const uint32_t i = page - base;
         return Page{__builtin_amdgcn_readlane(my_id, i),
@@ -655,7 +695,12 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
             v_tile[d * 8 + ((e + 1) ^ d / 2 % 8)] = half_codes(vr[u].z, vr[u].w);
         }
     };
-    look_up();
+    look_up_id();
+    if (!own) {
+        seq = prefix_holder(a, work);
+        if (seq != work.first_seq) look_up_id();
+    }
+    look_up_scales();
     Page now = page_at(first), next = page_at(first + 1), after = page_at(first + 2);
     fetch(a.c.k, now.id, kr);
     fetch(a.c.v, now.id, vr);
@@ -844,7 +889,7 @@ __global__ __launch_bounds__(kThreads, DIM == 256 ? 1 : 2)
         work.of_prefix(a, unit, FORM == kFew ? kFewRows : kTileRows);
     if (!work.any) return;
     if (FORM == kFew || (FORM == kManyFew && own)) {
-        if constexpr (FORM != kMany) attend_few<DIM, IN>(a, work, lds);
+        if constexpr (FORM != kMany) attend_few<DIM, IN>(a, work, own, lds);
     } else if constexpr (FORM != kFew) {
         if constexpr (kScoresAhead<DIM, IN>)
             attend_many_ahead<DIM, IN>(a, work, own, lds);

@@ -582,10 +582,12 @@ qar_status qar_kv8_attention(const qar_kv8_cache* cache, const void* q, qar_dtyp
 /*
  * The same attention for a batch whose sequences share their first tokens:
  * group g is sequences starts[g] .. starts[g + 1] - 1, and its sequences' tables
- * name the same pages for their first prefix[g] tokens.  The pages wholly among
- * these are read once for all of the group's queries (through the table of its
- * first sequence), the others sequence by sequence; the result is that of
- * qar_kv8_attention up to the order of the sums, whatever the lengths.
+ * name the same pages for their first prefix[g] tokens, as far as each has
+ * tokens: one may be shorter, or have ended and hold none.  The pages wholly
+ * among these are read once for all of the group's queries (through the table of
+ * its first sequence, or of its longest one where the first is shorter), the
+ * others sequence by sequence; the result is that of qar_kv8_attention up to the
+ * order of the sums, whatever the lengths.
  * Sequences outside all groups share nothing.
  *   starts     [in] int32[groups + 1], ascending, 0 .. batch; 1 <= groups <= batch.
  *   prefix     [in] int32[groups]; below 0 counts as 0.
