@@ -158,22 +158,29 @@ struct Work {
 // The sequence whose table names the pages that `work` has of a prefix: the
 // first of the group, or, where that holds fewer tokens (it ended or was cut back,
 // and its entries are gone), the group's longest, which holds all that any row
-// sees.  The lengths are asked for while the first one's entries are on their way.
-__device__ __forceinline__ uint32_t prefix_holder(const SharedArgs& a, const Work& work) {
-    const int32_t top = a.c.width * kPage;
-    if ((uint32_t)clamp_length(a.c.lengths[work.first_seq], top) >= work.last * kPage) return work.first_seq;
-    const uint32_t count = work.row_count / a.rows;
-    int32_t most = -1;
-    uint32_t which = 0;
-    for (uint32_t i = threadIdx.x % 64; i < count; i += 64) {
-        const int32_t n = clamp_length(a.c.lengths[work.first_seq + i], top);
-        if (n > most) most = n, which = i;
-    }
-    int32_t longest = most;
+// sees.  And where they end: pages behind the longest sequence hold nothing yet,
+// their scales neither.  The lengths are asked for while the first one's entries
+// are on their way.
+struct Holder {
+    uint32_t seq, last;
+    __device__ __forceinline__ Holder(const SharedArgs& a, const Work& work) : seq(work.first_seq), last(work.last) {
+        const int32_t top = a.c.width * kPage;
+        if ((uint32_t)clamp_length(a.c.lengths[seq], top) >= last * kPage) return;
+        const uint32_t count = work.row_count / a.rows;
+        int32_t most = -1;
+        uint32_t which = 0;
+        for (uint32_t i = threadIdx.x % 64; i < count; i += 64) {
+            const int32_t n = clamp_length(a.c.lengths[work.first_seq + i], top);
+            if (n > most) most = n, which = i;
+        }
+        int32_t longest = most;
 #pragma unroll
-    for (int d = 32; d; d /= 2) longest = max(longest, __shfl_xor(longest, d));
-    return work.first_seq + (uint32_t)__builtin_amdgcn_readlane((int)which, __builtin_ctzll(__ballot(most == longest)));
-}
+        for (int d = 32; d; d /= 2) longest = max(longest, __shfl_xor(longest, d));
+        longest = __builtin_amdgcn_readfirstlane(longest);
+        seq += (uint32_t)__builtin_amdgcn_readlane((int)which, __builtin_ctzll(__ballot(most == longest)));
+        last = min(last, (uint32_t)(longest + kPage - 1) / kPage);
+    }
+};
 
 // A row of the queries, and of the parts.
 struct Row {
@@ -214,8 +221,8 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
     constexpr int T = IN == kInBF16 ? 1 : 2;
     constexpr int KC = DIM / 64, VC = DIM / 16;
     const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, r = lane % 16, g = lane / 16;
-    const uint32_t h = work.head, first = work.first, last = work.last;
-    uint32_t seq = work.first_seq;
+    const uint32_t h = work.head, first = work.first;
+    uint32_t seq = work.first_seq, last = work.last;
     int32_t my_id;
     float my_ks, my_vs;
     auto look_up_id = [&](uint32_t page) {
@@ -230,8 +237,12 @@ __device__ __forceinline__ void attend_few(const SharedArgs& a, const Work& work
     };
     look_up_id(first + wave + lane * NW);
     if (!own) {
-        seq = prefix_holder(a, work);
-        if (seq != work.first_seq) look_up_id(first + wave + lane * NW);
+        const Holder holder(a, work);
+        last = holder.last;
+        if (holder.seq != seq || last != work.last) {
+            seq = holder.seq;
+            look_up_id(first + wave + lane * NW);
+        }
     }
     look_up_scales();
 
@@ -398,9 +409,8 @@ __device__ __forceinline__ void lay_out_products() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Where a tile's pages end: own ones only as far as its last row sees.
-__device__ __forceinline__ uint32_t pages_end(const SharedArgs& a, const Work& work, bool own) {
-    if (!own) return work.last;
+// Where a tile's own pages end: as far as its last row sees.
+__device__ __forceinline__ uint32_t own_pages_end(const SharedArgs& a, const Work& work) {
     const Seq seq(a, work.first_seq);
     const int32_t i = min((int32_t)(min(work.first_row + kTileRows, a.rows) - 1) / (int32_t)a.group, seq.m - 1);
     const int32_t keys = seq.n - seq.m + i + 1;
@@ -425,8 +435,7 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
     const uint32_t h = work.head, first = work.first;
     const uint32_t first_row = work.first_row + wave * 32;
 
-    const uint32_t last = pages_end(a, work, own);
-    uint32_t seq = work.first_seq;
+    uint32_t seq = work.first_seq, last = work.last;
     struct Page {
         int32_t id;
         float ks, vs;          // 0 for a page that is not there: what page 0 holds must not matter
@@ -462,9 +471,15 @@ __device__ __forceinline__ void attend_many(const SharedArgs& a, const Work& wor
         }
     };
     look_up_id();
-    if (!own) {
-        seq = prefix_holder(a, work);
-        if (seq != work.first_seq) look_up_id();
+    if (own) {
+        last = own_pages_end(a, work);
+    } else {
+        const Holder holder(a, work);
+        last = holder.last;
+        if (holder.seq != seq) {
+            seq = holder.seq;
+            look_up_id();
+        }
     }
     look_up_scales();
     Page now = page_at(first), next = page_at(first + 1);
@@ -641,8 +656,7 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
                    g = lane / 32;
     const uint32_t h = work.head, first = work.first;
     const uint32_t first_row = work.first_row + wave * 32;
-    const uint32_t last = pages_end(a, work, own);
-    uint32_t seq = work.first_seq;
+    uint32_t seq = work.first_seq, last = work.last;
     struct Page {
         int32_t id;
         float ks, vs;          // 0 for a page that is not there
@@ -696,9 +710,15 @@ __device__ __forceinline__ void attend_many_ahead(const SharedArgs& a, const Wor
         }
     };
     look_up_id();
-    if (!own) {
-        seq = prefix_holder(a, work);
-        if (seq != work.first_seq) look_up_id();
+    if (own) {
+        last = own_pages_end(a, work);
+    } else {
+        const Holder holder(a, work);
+        last = holder.last;
+        if (holder.seq != seq) {
+            seq = holder.seq;
+            look_up_id();
+        }
     }
     look_up_scales();
     Page now = page_at(first), next = page_at(first + 1), after = page_at(first + 2);

@@ -50,6 +50,23 @@ def test_several_groups(dim, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("members", [3, 90])
+def test_pages_behind_all_lengths_do_not_matter(members, dim, dtype):
+    """All of a group's sequences end before their prefix does.  The pages between were given ahead: their scales are not set,
+    here infinite or next to it."""
+    rng = np.random.default_rng(members)
+    lengths = [70 + i for i in range(members)]
+    c = _shared_cache(rng, 2, dim, [0, members], [9 * PAGE], lengths, 10)
+    used = c["page_table"][0, :-(-max(lengths) // PAGE)]
+    for p, scale in enumerate((np.inf, 3e38, 1e30)):
+        page = c["page_table"][0, 8 - p]
+        assert page not in used
+        c["v_scales"][page] = scale
+    _check(c, [0, members], [9 * PAGE], 1, 4, dtype, seed=members)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("dim,heads", [(128, 8), (64, 40)])
 def test_beams_that_end(dim, heads, dtype):
     """The library's own calls: beams fork from a prompt, some get no parent, some end and are released; starts and prefix
