@@ -1201,7 +1201,7 @@ qar_status qar_norm_rotate(const void* qkv, qar_dtype dtype, size_t batch, size_
         (pairs && !aligned(frequencies, 4)) || (q_gain && !aligned(q_gain, 16)) || (k_gain && !aligned(k_gain, 16)))
         return QAR_ERR_MISALIGNED;
     const size_t row = ((size_t)heads + 2 * (size_t)kv_heads) * dim;
-    // a workgroup a token, or up to heads / 16 + 1 more where tokens are few
+    // a workgroup a token, or a few where tokens are few
     if (batch > kMaxGroups / tokens || batch * tokens > kMaxGroups / 2 || batch * tokens > QAR_MAX_ELEMENTS / row)
         return QAR_ERR_INVALID_ARG;
     const size_t rows = batch * tokens, size = dtype_bytes(dtype);

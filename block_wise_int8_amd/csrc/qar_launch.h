@@ -108,7 +108,8 @@ struct RotateCall {
     uint32_t heads, kv_heads, pairs;
     bool norm, interleaved, each_token;
     float eps;
-    uint32_t parts;              // workgroups of a token: the launcher's
+    uint32_t parts;              // the launcher's: workgroups of a token ...
+    size_t first;                // ... and a launch's first token
 };
 hipError_t launch_norm_rotate(RotateCall a, int kind, int dim, hipStream_t st);
 

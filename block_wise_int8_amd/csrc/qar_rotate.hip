@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void norm_rotate_kernel(RotateCall a) {
     __shared__ float2 table[DIM / 2];
     __shared__ float rows[PAIRS == kSplitHalves ? H : 1][PAIRS == kSplitHalves ? DIM + 4 : 1];
     const uint32_t tid = threadIdx.x, l = tid % L, mine = tid / L;
-    const size_t token = blockIdx.x / a.parts;
+    const size_t token = a.first + blockIdx.x / a.parts;
     const uint32_t part = blockIdx.x % a.parts, all = a.heads + 2 * a.kv_heads, rotated = a.heads + a.kv_heads;
     const uint32_t per = (all + a.parts - 1) / a.parts, first = part * per, last = min(first + per, all);
 
@@ -248,12 +248,18 @@ hipError_t launch_norm_rotate(RotateCall a, int kind, int dim, hipStream_t st) {
     // few tokens: a token's heads spread over workgroups, each at least one pass
     const uint32_t at_once = kThreads / (dim / 16), all = a.heads + 2 * a.kv_heads, most = (all + at_once - 1) / at_once;
     a.parts = a.rows >= 1024 ? 1 : (uint32_t)std::min<size_t>(most, (1024 + a.rows - 1) / a.rows);
-    const uint32_t groups = (uint32_t)a.rows * a.parts;
-    const auto go = [&](auto IN) {
+    const auto go = [&](auto IN, uint32_t groups) {
         constexpr int K = decltype(IN)::value;
         return dim == 64 ? launch<64, K>(a, groups, st) : dim == 128 ? launch<128, K>(a, groups, st) : launch<256, K>(a, groups, st);
     };
-    return kind == kInBF16 ? go(std::integral_constant<int, kInBF16>{}) : go(std::integral_constant<int, kInF32>{});
+    // a launch has less than 2^32 threads
+    constexpr size_t most_rows = ((size_t)1 << 32) / kThreads - 1;
+    hipError_t e = hipSuccess;
+    for (a.first = 0; e == hipSuccess && a.first < a.rows; a.first += most_rows) {
+        const uint32_t groups = (uint32_t)std::min(a.rows - a.first, most_rows) * a.parts;
+        e = kind == kInBF16 ? go(std::integral_constant<int, kInBF16>{}, groups) : go(std::integral_constant<int, kInF32>{}, groups);
+    }
+    return e;
 }
 
 } // namespace qar
