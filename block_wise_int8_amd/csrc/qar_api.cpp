@@ -1139,10 +1139,16 @@ qar_status qar_kv8_evict(const qar_kv8_cache* cache, const qar_kv8_cache* into, 
 // ---------------------------------------------------------------------------
 // attention behind prefixes that sequences share
 
+static bool kv8_shared_ok(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads, uint32_t dim, uint32_t width,
+                          uint32_t groups) {
+    return groups != 0 && groups <= batch && kv8_rows_ok(batch, queries, heads, kv_heads, width) &&
+           qar::kv8_shared_fits(batch, kv_heads, queries * (heads / kv_heads), (int)dim, width, groups);
+}
+
 size_t qar_kv8_attention_shared_workspace_bytes(uint32_t batch, uint32_t queries, uint32_t heads, uint32_t kv_heads,
                                                 uint32_t dim, uint32_t table_width, uint32_t groups) {
-    if (batch == 0 || queries == 0 || table_width == 0 || groups == 0 || groups > batch ||
-        (dim != 64 && dim != 128 && dim != 256) || !kv8_rows_ok(batch, queries, heads, kv_heads, table_width))
+    if (batch == 0 || queries == 0 || table_width == 0 || (dim != 64 && dim != 128 && dim != 256) ||
+        !kv8_shared_ok(batch, queries, heads, kv_heads, dim, table_width, groups))
         return 0;
     return qar::kv8_shared_workspace(batch, kv_heads, queries * (heads / kv_heads), (int)dim, table_width, groups);
 }
@@ -1154,8 +1160,8 @@ qar_status qar_kv8_attention_shared(const qar_kv8_cache* cache, const void* q, q
     if (cache && (cache->batch == 0 || queries == 0)) return QAR_OK;
     const qar_status st = check_cache(cache);
     if (st != QAR_OK) return st;
-    if (!q || !out || !starts || !prefix || groups == 0 || groups > cache->batch ||
-        !kv8_rows_ok(cache->batch, queries, heads, cache->kv_heads, cache->table_width))
+    if (!q || !out || !starts || !prefix ||
+        !kv8_shared_ok(cache->batch, queries, heads, cache->kv_heads, cache->dim, cache->table_width, groups))
         return QAR_ERR_INVALID_ARG;
     if (!dtype_ok(dtype)) return QAR_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(starts, 4) || !aligned(prefix, 4) || (q_lens && !aligned(q_lens, 4)))
@@ -1237,7 +1243,8 @@ static qar_status check_owned(const qar_kv8_cache* c, const int32_t* refs) {
     if (st != QAR_OK) return st;
     if (!refs) return QAR_ERR_INVALID_ARG;
     if (!aligned(refs, 4)) return QAR_ERR_MISALIGNED;
-    if ((size_t)c->batch * c->table_width > kMaxGroups) return QAR_ERR_INVALID_ARG;
+    // a thread an entry, a workgroup of 256 a sequence: less than 2^32 of them
+    if ((size_t)c->batch * c->table_width > kMaxGroups || c->batch >= (1u << 24)) return QAR_ERR_INVALID_ARG;
     const CacheRanges held(c);
     if (held.touches(range(refs, (size_t)c->pages * 4))) return QAR_ERR_INVALID_ARG;
     for (int i = 4; i < 6; ++i)

@@ -1068,7 +1068,16 @@ Plan plan_for(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_
     return p;
 }
 
+bool joined_by_eight(const Plan& p) { return p.prefix_slots + p.own_slots > 4; }
+
 } // namespace
+
+bool kv8_shared_fits(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups) {
+    const Plan p = plan_for(batch, kv_heads, rows, dim, width, groups);
+    const size_t units = (size_t)p.prefix_tiles * kv_heads * p.prefix_slots + (size_t)batch * kv_heads * p.own_tiles * p.own_slots;
+    const size_t join = (size_t)batch * kv_heads * rows * (dim / 4) * (joined_by_eight(p) ? kJoinRows : 1);
+    return units * kThreads <= UINT32_MAX && join + kJoinRows * dim / 4 <= UINT32_MAX;
+}
 
 size_t kv8_shared_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups) {
     const Plan p = plan_for(batch, kv_heads, rows, dim, width, groups);
@@ -1099,7 +1108,7 @@ hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t que
                                  : p.own_few ? attend(kv8_shared_kernel<D(), K(), kManyFew>)
                                              : attend(kv8_shared_kernel<D(), K(), kMany>);
             if (e != hipSuccess) return e;
-            return p.prefix_slots + p.own_slots > 4
+            return joined_by_eight(p)
                        ? launch_threads(kv8_shared_join_kernel<D(), K(), kJoinRows>, (uint32_t)items, kJoinRows * D() / 4, st, a)
                        : launch_threads(kv8_shared_join_kernel<D(), K(), 1>, (uint32_t)((items + kJoinRows - 1) / kJoinRows),
                                         kJoinRows * D() / 4, st, a);

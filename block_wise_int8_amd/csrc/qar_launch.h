@@ -137,6 +137,8 @@ hipError_t launch_kv8_evict(const Kv8& c, const Kv8& into, const float* weights,
                             int32_t* kept, float* moved, hipStream_t st);
 
 // Attention behind prefixes that sequences share (qar_kv8_shared.hip).
+// Whether its launches have less than 2^32 threads each.
+bool kv8_shared_fits(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups);
 size_t kv8_shared_workspace(uint32_t batch, uint32_t kv_heads, uint32_t rows, int dim, uint32_t width, uint32_t groups);
 hipError_t launch_kv8_shared(const Kv8& c, const void* q, int kind, uint32_t queries, uint32_t heads, const int32_t* starts,
                              const int32_t* prefix, uint32_t groups, const int32_t* q_lens, float scale, void* out,

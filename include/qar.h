@@ -658,7 +658,8 @@ qar_status qar_norm_rotate(const void* qkv, qar_dtype dtype, size_t batch, size_
  * result is that of serving the sequences in order, so equal calls give equal
  * tables.  Entries outside the pool are pages that are not there, as everywhere.
  * Caches of several layers whose page tables are the same take one call for the
- * table, and one qar_kv8_copy for each layer.
+ * table, and one qar_kv8_copy for each layer.  batch < 2^24 and
+ * batch * table_width < 2^31.
  *
  * fork: sequence b of `into` goes on from sequence parents[b] of `cache`: its
  * length, and the same pages up to it (their counts grow); no entries behind.
