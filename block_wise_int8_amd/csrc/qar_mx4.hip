@@ -366,8 +366,8 @@ __device__ __forceinline__ float tanh_exponent(float v, float& low) {
 
 // Half the complementary error function of a / sqrt 2, a >= 0: e^(-a^2 / 2)
 // times t Q(t), t = 1 / (1 + k a).  Q was fitted to the scaled function for the
-// smallest relative error over 0 .. 14 (2^-24.9, or 2^-16.9); behind that the
-// exponential leaves nothing.
+// smallest relative error over 0 .. 14 (2^-23.6 with the coefficients as they are
+// rounded here, or 2^-16.9); behind that the exponential leaves nothing.
 template <bool EXACT>
 __device__ __forceinline__ float half_erfc(float a) {
     const float square = a * a;
@@ -830,8 +830,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx4_tiled_kernel(L
     constexpr int STORES = NOW * 32 * PER / 64, ALL = STORES * (TM / NOW);
     const size_t col = n0 + wn * WN + lane % PER * N;
     // A tile inside a bf16 output's columns asks for all of its residual before it
-    // waits for the last loads to LDS (8192 x 5376 x 21504: 693 -> 625 us with
-    // GELU); binary32, twice the registers, four stores' worth at a time.  Small
+    // waits for the last loads to LDS (8192 x 5376 x 21504 with bias and GELU: the
+    // call 693 -> 633 to 650 us); binary32, twice the registers, four stores' worth at a time.  Small
     // tiles, one wave to a SIMD, have registers enough to ask before their first
     // chunk (300 x 5760 x 2880, binary32: 17.8 -> 17.1 us).
     constexpr bool EARLY = EPILOGUE && (sizeof(T) == 2 || DEEP);
