@@ -1000,8 +1000,8 @@ def qar_kv8_attention_shared(cache: KvCache, q: torch.Tensor, starts: torch.Tens
                              stream=None) -> torch.Tensor:
     """qar_kv8_attention for sequences that share their first tokens' pages, which are read once for each group:
     sequences starts[g] .. starts[g + 1] - 1 (int32[groups + 1]) have their first prefix[g] (int32[groups]) tokens in
-    common.  ``workspace`` (at least lib().qar_kv8_attention_shared_workspace_bytes(...) bytes) is allocated with torch
-    when not given."""
+    common, as far as each has tokens.  ``workspace`` (at least lib().qar_kv8_attention_shared_workspace_bytes(...) bytes)
+    is allocated with torch when not given."""
     if stream is not None:
         with _as_current(stream):
             return qar_kv8_attention_shared(cache, q, starts, prefix, q_lens, scale, out, workspace)
